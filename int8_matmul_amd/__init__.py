@@ -35,6 +35,8 @@ __all__ = [
     "smoothquant_quantize_weight", "smoothquant_prepare", "smoothquant_linear",
     "cache_bytes", "new_cache", "cache_reset", "cache_stats", "linear_cached", "prepare_cached",
     "gemm_cached", "STATUS",
+    "KVCache", "KVBatch", "Rope", "new_kv_cache", "kv_append", "kv_read", "kv_attention",
+    "kv_attention_plan", "kv_attention_workspace_bytes", "new_kv_attention_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -130,6 +132,18 @@ def load_library() -> ctypes.CDLL:
     L.llm_int8_stages.restype = ctypes.c_int
     L.llm_int8_stages.argtypes = [vp, vp, vp, ctypes.c_float, i64, i64, i64, vp, vp, sz, vp, vp, vp,
                                   vp, vp, vp, vp, vp]
+    i32 = ctypes.c_int32
+    L.int8_kv_append.restype = ctypes.c_int
+    L.int8_kv_append.argtypes = [vp, i64, vp, i64, ctypes.c_int, vp, vp, vp, vp]
+    L.int8_kv_read.restype = ctypes.c_int
+    L.int8_kv_read.argtypes = [vp, vp, ctypes.c_int, vp, i64, vp, i64, vp]
+    L.int8_kv_attention_workspace_bytes.restype = sz
+    L.int8_kv_attention_workspace_bytes.argtypes = [vp, vp, i32]
+    L.int8_kv_attention_plan.restype = ctypes.c_int
+    L.int8_kv_attention_plan.argtypes = [vp, vp, i32, i32, vp, vp]
+    L.int8_kv_attention.restype = ctypes.c_int
+    L.int8_kv_attention.argtypes = [vp, i64, ctypes.c_int, i32, ctypes.c_float, vp, i32, i32, vp, vp,
+                                    vp, i64, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -586,3 +600,261 @@ def stages(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold: float
                              _ptr(r["outlier_idx"]), _ptr(r["Xq"]), _ptr(r["sX"]),
                              _ptr(r["X_out"]), _ptr(r["acc"]), _stream(dev)))
     return r
+
+
+# ---------------------------------------------------------------------------
+# The int8 key/value cache (include/llm_int8_kv.h)
+# ---------------------------------------------------------------------------
+
+_KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+class _CKVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _CKVBatch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32),
+                ("seqs", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32)]
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class KVCache:
+    """Keys and values in int8, with one scale for each page of tokens and head:
+    k, v int8 [pages, heads, page_size, head_dim], k_scale, v_scale fp32 [pages, heads].
+
+    Holds the tensors and their description for the library; the checks are
+    made here, once.  The tensors may change in place."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        _require(k, torch.int8, "k", 4)
+        _require(v, torch.int8, "v", 4)
+        _require(k_scale, torch.float32, "k_scale", 2)
+        _require(v_scale, torch.float32, "v_scale", 2)
+        if v.shape != k.shape or k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+            raise ValueError(f"shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}, "
+                             f"k_scale {tuple(k_scale.shape)}, v_scale {tuple(v_scale.shape)}")
+        _same_device(k, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_size, self.head_dim = k.shape
+        self.device = k.device
+        self._c = _CKVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.pages, self.heads,
+                            self.page_size, self.head_dim)
+        self._ref = ctypes.addressof(self._c)
+
+
+class KVBatch:
+    """Sequences and their new rows: q_start int32 [seqs + 1], kv_len int32 [seqs],
+    table int32 [seqs, width] of page numbers (rows may be strided).
+
+    The rows q_start[s] .. q_start[s + 1] - 1 of the packed token tensors are
+    the last ones of sequence s, which has kv_len[s] tokens with them.
+    ``tokens`` is the packed tensors' row count; ``max_q`` and ``max_kv`` are
+    at least the longest chunk and the longest sequence (the lengths
+    themselves stay on the GPU).  The tensors may change in place, so one
+    object serves every step of a captured graph."""
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, tokens: int,
+                 max_q: int, max_kv: int):
+        _require(q_start, torch.int32, "q_start", 1)
+        _require(kv_len, torch.int32, "kv_len", 1)
+        if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32:
+            raise TypeError("table must be a 2-dim torch.int32 tensor")
+        if table.device.type != "cuda":
+            raise ValueError(f"table must be on a GPU device, got {table.device}")
+        S = kv_len.shape[0]
+        if q_start.shape[0] != S + 1 or table.shape[0] != S:
+            raise ValueError(f"shape mismatch: q_start {tuple(q_start.shape)}, kv_len {tuple(kv_len.shape)}, "
+                             f"table {tuple(table.shape)}")
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("table's rows must be contiguous")
+        _same_device(q_start, kv_len=kv_len, table=table)
+        width = table.shape[1]
+        stride = table.stride(0) if S > 1 else width
+        if S > 1 and stride < width:
+            raise ValueError("table's rows overlap")
+        for name, n in (("tokens", tokens), ("max_q", max_q), ("max_kv", max_kv)):
+            if not 0 <= n < 1 << 31:
+                raise ValueError(f"{name} must be in [0, 2^31), got {n}")
+        self.q_start, self.kv_len, self.table = q_start, kv_len, table
+        self.seqs, self.tokens, self.max_q, self.max_kv = S, tokens, max_q, max_kv
+        self.device = q_start.device
+        self._c = _CKVBatch(_ptr(q_start), _ptr(kv_len), _ptr(table), stride, width, S, tokens, max_q,
+                            max_kv)
+        self._ref = ctypes.addressof(self._c)
+
+
+class Rope:
+    """Rotation of the first 2 * cos.shape[1] values of every head by position:
+    cos, sin fp32 [rows, dims / 2]; pairs (i, i + dims/2), or (2i, 2i + 1) if
+    ``interleaved``."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
+        _require(cos, torch.float32, "cos", 2)
+        _require(sin, torch.float32, "sin", 2)
+        if sin.shape != cos.shape:
+            raise ValueError(f"shape mismatch: cos {tuple(cos.shape)}, sin {tuple(sin.shape)}")
+        _same_device(cos, sin=sin)
+        self.cos, self.sin, self.interleaved, self.device = cos, sin, bool(interleaved), cos.device
+        self._c = _CRope(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
+        self._ref = ctypes.addressof(self._c)
+
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _kv_tokens(t: torch.Tensor, name: str, batch: KVBatch, heads: int | None, dim: int) -> int:
+    """Checks a packed token tensor [tokens, heads, dim] with dense rows and
+    returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _KV_DTYPES:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != batch.tokens or t.shape[2] != dim or (heads is not None
+                                                                           and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape ({batch.tokens}, {'heads' if heads is None else heads}, "
+                         f"{dim}), got {tuple(t.shape)}")
+    if t.device != batch.device:
+        raise ValueError(f"{name} is on {t.device}, expected {batch.device}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}'s rows must be dense [heads, head_dim]")
+    # a single row has no step: its stride may be anything
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def _kv_place(batch: KVBatch, cache: KVCache, rope: Rope | None = None) -> None:
+    if not isinstance(batch, KVBatch) or not isinstance(cache, KVCache):
+        raise TypeError("batch must be a KVBatch and cache a KVCache")
+    if rope is not None and not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope or None")
+    if cache.device != batch.device or (rope is not None and rope.device != batch.device):
+        raise ValueError(f"batch, cache and rope must be on one device, got {batch.device}, {cache.device}"
+                         + ("" if rope is None else f", {rope.device}"))
+
+
+def _kv_call(name: str, device: torch.device, *args) -> None:
+    """The library launches on the current device: make it the tensors'."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    if status != 0:
+        raise Int8MatmulError(name, status)
+
+
+def new_kv_cache(pages: int, heads: int, head_dim: int, page_size: int, device) -> KVCache:
+    """An empty cache (codes and scales zero)."""
+    k = torch.zeros((pages, heads, page_size, head_dim), dtype=torch.int8, device=device)
+    ks = torch.zeros((pages, heads), dtype=torch.float32, device=device)
+    return KVCache(k, torch.zeros_like(k), ks, torch.zeros_like(ks))
+
+
+def kv_append(K: torch.Tensor, V: torch.Tensor, cache: KVCache, batch: KVBatch,
+              rope: Rope | None = None) -> KVCache:
+    """Store the batch's new keys and values, fp16 or bf16 [tokens, heads, head_dim]
+    (rows may be strided), the keys rotated by their positions on the way."""
+    _kv_place(batch, cache, rope)
+    ks = _kv_tokens(K, "K", batch, cache.heads, cache.head_dim)
+    vs = _kv_tokens(V, "V", batch, cache.heads, cache.head_dim)
+    if V.dtype != K.dtype:
+        raise TypeError(f"V must be {K.dtype} like K, got {V.dtype}")
+    _kv_call("int8_kv_append", batch.device, K.data_ptr(), ks, V.data_ptr(), vs, _KV_DTYPES[K.dtype],
+             None if rope is None else rope._ref, batch._ref, cache._ref)
+    return cache
+
+
+def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.float16,
+            out: tuple | None = None):
+    """The values of the batch's rows back from the cache: (K, V), each
+    [tokens, heads, head_dim] of ``dtype``.  Rows of no sequence are not written."""
+    _kv_place(batch, cache)
+    if dtype not in _KV_DTYPES:
+        raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+    if out is None:
+        shape = (batch.tokens, cache.heads, cache.head_dim)
+        out = (torch.empty(shape, dtype=dtype, device=cache.device),
+               torch.empty(shape, dtype=dtype, device=cache.device))
+    K, V = out
+    ks = _kv_tokens(K, "out[0]", batch, cache.heads, cache.head_dim)
+    vs = _kv_tokens(V, "out[1]", batch, cache.heads, cache.head_dim)
+    if K.dtype != dtype or V.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, got {K.dtype} and {V.dtype}")
+    _kv_call("int8_kv_read", batch.device, cache._ref, batch._ref, _KV_DTYPES[dtype], K.data_ptr(), ks,
+             V.data_ptr(), vs)
+    return K, V
+
+
+def kv_attention_workspace_bytes(batch: KVBatch, cache: KVCache, q_heads: int) -> int:
+    """Bytes of workspace that ``kv_attention`` needs (0: none)."""
+    return int(load_library().int8_kv_attention_workspace_bytes(batch._ref, cache._ref, q_heads))
+
+
+def new_kv_attention_workspace(batch: KVBatch, cache: KVCache, q_heads: int) -> torch.Tensor:
+    return torch.empty(kv_attention_workspace_bytes(batch, cache, q_heads), dtype=torch.uint8,
+                       device=cache.device)
+
+
+KV_PATHS = {0: "empty", 1: "few", 2: "tiled"}
+
+
+def kv_attention_plan(batch: KVBatch, cache: KVCache, q_heads: int, window: int = 0) -> dict:
+    """How ``kv_attention`` runs a batch of this shape: path, and the most
+    parts that a sequence's keys are split into."""
+    path, splits = ctypes.c_int32(), ctypes.c_int32()
+    _check("int8_kv_attention_plan",
+           load_library().int8_kv_attention_plan(batch._ref, cache._ref, q_heads, window,
+                                                 ctypes.byref(path), ctypes.byref(splits)))
+    return dict(path=KV_PATHS[path.value], splits=splits.value)
+
+
+def kv_attention(Q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float | None = None,
+                 rope: Rope | None = None, causal: bool = True, window: int = 0,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the batch's rows Q, fp16 or bf16 [tokens, q_heads, head_dim],
+    over the cache, after their keys and values were appended.
+
+    ``scale`` defaults to 1/sqrt(head_dim); ``rope`` rotates Q on the way;
+    ``window`` > 0 lets a row see its own and the window - 1 tokens before;
+    ``lse`` fp32 [tokens, q_heads] receives the log of each row's sum (-inf
+    for a row that sees no key; its output is 0)."""
+    _kv_place(batch, cache, rope)
+    D = cache.head_dim
+    qs = _kv_tokens(Q, "Q", batch, None, D)
+    Hq = Q.shape[1]
+    if out is None:
+        out = torch.empty((batch.tokens, Hq, D), dtype=Q.dtype, device=Q.device)
+        os_ = Hq * D
+    else:
+        os_ = _kv_tokens(out, "out", batch, Hq, D)
+        if out.dtype != Q.dtype:
+            raise TypeError(f"out must be {Q.dtype} like Q, got {out.dtype}")
+    if lse is not None:
+        _require(lse, torch.float32, "lse", 2)
+        if tuple(lse.shape) != (batch.tokens, Hq) or lse.device != Q.device:
+            raise ValueError(f"lse must be ({batch.tokens}, {Hq}) on {Q.device}, got {tuple(lse.shape)} "
+                             f"on {lse.device}")
+    if workspace is None:
+        workspace = new_kv_attention_workspace(batch, cache, Hq)
+    else:
+        _require(workspace, torch.uint8, "workspace", 1)
+        if workspace.device != Q.device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {Q.device}")
+    _kv_call("int8_kv_attention", batch.device, Q.data_ptr(), qs, _KV_DTYPES[Q.dtype], Hq,
+             float(D ** -0.5 if scale is None else scale), None if rope is None else rope._ref,
+             int(bool(causal)), window, batch._ref, cache._ref, out.data_ptr(), os_,
+             _ptr(lse), workspace.data_ptr(), workspace.numel())
+    return out
