@@ -29,8 +29,8 @@
  *     chunk longer than max_q has the tokens past it left out, and a page
  *     number outside [0, pages) is never followed: nothing is stored there,
  *     reading gives zeros, and attention treats its tokens as masked.
- *   - Inputs must be finite where they are read; so must the scales of pages
- *     with stored tokens.  Codes and scales of tokens that no query sees,
+ *   - Inputs must be finite where they are read; the scales of pages with
+ *     stored tokens finite and >= 0.  Codes and scales of tokens that no query sees,
  *     and rows outside [q_start[0], q_start[seqs]), may hold anything.
  */
 #ifndef LLM_INT8_KV_H
@@ -72,7 +72,7 @@ typedef struct li8_kv_batch {
     int32_t tokens;         /* rows of the packed tensors                  */
     int32_t max_q;          /* >= the longest chunk                        */
     int32_t max_kv;         /* >= the longest sequence,
-                               <= table_width * page_size                  */
+                               <= table_width * page_size and 2^30         */
 } li8_kv_batch;
 
 /*
@@ -135,6 +135,7 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  * the matrix units: q as 15-bit integers of its row's largest magnitude
  * (two int8 parts) times the key codes, exact in int32; the softmax in fp32;
  * the probabilities rounded to fp16 times the value codes, summed in fp32.
+ *   scale   >= 0 and finite
  *   Q, O    [tokens][q_heads][head_dim], rows q_stride, o_stride apart;
  *           O must not alias Q
  *   rope    as for the keys; a negative position (only without `causal`

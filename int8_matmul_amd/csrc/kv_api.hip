@@ -11,6 +11,7 @@ using namespace li8;
 namespace {
 
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+constexpr int32_t kMaxKeys = 1 << 30;   // positions and a step past them stay below 2^31
 
 bool off_by(const void *p, uintptr_t align) { return ((uintptr_t)p & (align - 1)) != 0; }
 
@@ -27,7 +28,8 @@ li8_status check_sizes(const li8_kv_batch *b, const li8_kv_cache *c)
         return LI8_ERR_SHAPE;
     if (c->heads < 1 || c->heads > 65535 || c->pages < 0 || c->pages > kMaxGrid)
         return LI8_ERR_SHAPE;
-    if (b->seqs < 0 || b->tokens < 0 || b->max_q < 0 || b->max_kv < 0 || b->table_width < 0 ||
+    if (b->seqs < 0 || b->tokens < 0 || b->max_q < 0 || b->max_kv < 0 || b->max_kv > kMaxKeys ||
+        b->table_width < 0 ||
         b->table_stride < b->table_width)
         return LI8_ERR_SHAPE;
     if (b->max_kv > (int64_t)b->table_width * c->page_size)
@@ -97,7 +99,7 @@ li8_status check_heads(const li8_kv_batch *b, const li8_kv_cache *c, int32_t q_h
     if (rows * group > kMaxGrid)
         return LI8_ERR_SHAPE;
     const KvPlan p = kv_plan(*b, *c, q_heads, window);
-    if ((double)b->seqs * c->heads * p.blocks * std::max(p.splits, p.used) > (double)kMaxGrid)
+    if (((double)b->seqs * c->heads + 8) * p.blocks * std::max(p.splits, p.used) > (double)kMaxGrid)
         return LI8_ERR_SHAPE;
     return LI8_OK;
 }
@@ -182,7 +184,7 @@ li8_status int8_kv_attention(const void *Q, int64_t q_stride, li8_dtype dtype, i
 {
     LI8_TRY(check_sizes(batch, cache));
     LI8_TRY(check_heads(batch, cache, q_heads, window));
-    if (bad_dtype(dtype) || !isfinite(scale) || (causal != 0 && causal != 1))
+    if (bad_dtype(dtype) || !isfinite(scale) || scale < 0.0f || (causal != 0 && causal != 1))
         return LI8_ERR_INVALID_ARG;
     KvRope r;
     LI8_TRY(check_rope(rope, batch, cache, &r));

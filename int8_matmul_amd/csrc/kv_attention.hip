@@ -43,7 +43,7 @@ struct AttnArgs {
     float *part_o, *part_m;            // [item][split][used][D], [item][split][used]
     float scale;                       // scale * log2(e)
     int group, causal, window;
-    int blocks, used, splits, chunk;
+    int cols, blocks, used, splits, chunk;
 };
 
 // Where a workgroup's columns lie.
@@ -332,6 +332,330 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_few(KvArgs a, AttnArgs t)
         t.lse[row * (int64_t)(a.heads * t.group) + head] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
+// ---------------------------------------------------------------------------
+// Many columns: 32 columns per wave, kTileWaves waves; the workgroup walks
+// its keys in steps of 64 that all waves read from LDS.  K stays int8 there
+// (16 MFMAs 32x32x32 i8 per step and wave for the two query parts), V is
+// turned into fp16 and transposed on its way in, once for all waves.
+// ---------------------------------------------------------------------------
+constexpr int kTileWaves = 8;
+constexpr int kTileCols = 32 * kTileWaves;
+constexpr int kTileKeys = 64;
+constexpr float kFar = -12.0f;         // log2: value scales this far below the largest
+
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// 16-byte chunks of the LDS tiles are permuted within 128 bytes so that
+// neither the fragment reads (32 rows, one chunk each) nor the writes of V
+// (rows 4 apart) meet in a bank.
+template <int D>
+__device__ __forceinline__ int k_place(int row, int chunk)
+{
+    if constexpr (D == 128)
+        return row * 128 + 16 * (chunk ^ (row & 7));
+    return row * 64 + 16 * (chunk ^ ((row >> 1) & 3));
+}
+
+__device__ __forceinline__ int v_place(int d, int chunk) { return d * 128 + 16 * (chunk ^ ((d ^ (d >> 3)) & 7)); }
+
+template <int D>
+struct TileLds {
+    static constexpr int K = kTileKeys * D, V = D * kTileKeys * 2;
+    static constexpr int stage = K + V;
+    static constexpr int q_row = D + 16;
+    static constexpr int bytes = 2 * stage > 2 * kTileCols * q_row ? 2 * stage : 2 * kTileCols * q_row;
+};
+
+template <int D, bool BF16>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnArgs t, int pairs, int lanes)
+{
+    constexpr int NT = 64 * kTileWaves, CPR = D / 8, KS = D / 32, DB = D / 32;
+    constexpr int NI = kTileKeys * D / 16 / NT > 0 ? kTileKeys * D / 16 / NT : 1;   // staging items of a thread
+    constexpr int ITEMS = kTileKeys * D / 16;
+    using L = TileLds<D>;
+    __shared__ __align__(16) char smem[L::bytes];
+    __shared__ float s_f[kTileCols];
+    __shared__ __align__(16) float s_sc[2][4][4];   // [buffer][ks, 1/vs, log2 vs, vs][group of 16 keys]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // Blocks of one (sequence, head) share its keys: all on 8 / lanes of the
+    // XCDs (the hardware deals workgroups to the 8 XCDs in turn), the last
+    // block, which sees the most keys, first.
+    const int j = blockIdx.x / lanes, per = t.blocks * t.splits;
+    const int pair = (j / per) * lanes + blockIdx.x % lanes;
+    if (pair >= pairs)
+        return;
+    const int rest = j % per, sp = rest % t.splits;
+    const int item = pair * t.blocks + (t.blocks - 1 - rest / t.splits);
+    Block b;
+    if (!locate(a, t, item, kTileCols, b))
+        return;
+    const int ts = b.span.base + sp * t.chunk;
+    const int te = min(b.span.hi, ts + t.chunk);
+    if (ts >= te && t.splits > 1)
+        return;
+
+#pragma unroll
+    for (int k = 0; k < CPR / 2; k++) {
+        const int it = tid + NT * k, qc = it / CPR, cc = it % CPR;
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f;
+        if (qc < b.nc) {
+            const int c = b.c0 + qc, i = c / t.group, g = c - i * t.group;
+            load_rotated8<BF16>(t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D,
+                                cc, t.rope, max(b.q.begin + i, 0), x);
+        }
+        uint2 hi, lo;
+        split_query<D>(x, hi, lo, f);
+        *reinterpret_cast<uint2 *>(smem + qc * L::q_row + 8 * cc) = hi;
+        *reinterpret_cast<uint2 *>(smem + (kTileCols + qc) * L::q_row + 8 * cc) = lo;
+        if (cc == 0)
+            s_f[qc] = f * t.scale;
+    }
+    __syncthreads();
+    const int col = lane & 31, half = lane >> 5, qcol = 32 * wid + col;
+    v4i qh[KS], ql[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++) {
+        qh[ks] = *reinterpret_cast<const v4i *>(smem + qcol * L::q_row + 32 * ks + 16 * half);
+        ql[ks] = *reinterpret_cast<const v4i *>(smem + (kTileCols + qcol) * L::q_row + 32 * ks + 16 * half);
+    }
+    const float f = s_f[qcol];
+    __syncthreads();
+
+    // keys this lane's column sees, [clo, chi), and what all columns of the
+    // wave see, [wlo, whi), or any of them, [ulo, uhi)
+    const int pos = b.q.begin + (b.c0 + qcol) / t.group;
+    int chi = t.causal ? min(te, pos + 1) : te;
+    int clo = t.window > 0 ? max((int64_t)0, (int64_t)pos + 1 - t.window) : 0;
+    if (qcol >= b.nc)
+        chi = clo = 0;
+    const int c_first = 32 * wid, c_last = min(32 * wid + 31, b.nc - 1);
+    const int p_first = b.q.begin + (b.c0 + c_first) / t.group, p_last = b.q.begin + (b.c0 + c_last) / t.group;
+    const KvSpan seen = kv_span(p_first, p_last, te, t.causal != 0, t.window);
+    const bool idle = c_first >= b.nc;
+    const int whi = c_last < 32 * wid + 31 ? 0 : t.causal ? min(te, p_first + 1) : te;
+    const int wlo = t.window > 0 ? max((int64_t)0, (int64_t)p_last + 1 - t.window) : 0;
+
+    const int32_t *table = a.table + (int64_t)b.s * a.table_stride;
+    const int page = 1 << a.page_shift;
+    uint4 rk[NI];
+    uint32_t rv[NI][4];
+    float rks = 0.0f, rvs = 0.0f;
+    bool rok = false;
+    auto page_of = [&](int key, bool &ok) {
+        const int pid = table[min(key >> a.page_shift, a.table_width - 1)];
+        ok = (unsigned)pid < (unsigned)a.pages && (key & ~15) < te && (key | 15) >= b.span.lo;
+        return (int64_t)(ok ? pid : 0) * a.heads + b.h;
+    };
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < NI; k++) {
+            const int it = (tid + NT * k) % ITEMS;
+            const int row = it / (D / 16), chunk = it % (D / 16);
+            bool ok;
+            int64_t ph = page_of(t0 + row, ok);
+            rk[k] = *reinterpret_cast<const uint4 *>(a.k + ((ph * D) << a.page_shift) +
+                                                     ((t0 + row) & (page - 1)) * D + 16 * chunk);
+            const int dg = it % (D / 4), sb = it / (D / 4), key = t0 + 4 * sb;
+            ph = page_of(key, ok);
+            const int8_t *p = a.v + ((ph * D) << a.page_shift) + (key & (page - 1)) * D + 4 * dg;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                rv[k][e] = *reinterpret_cast<const uint32_t *>(p + e * D);
+        }
+        const int64_t ph = page_of(t0 + 16 * (tid & 3), rok);
+        rks = a.ks[ph];
+        rvs = a.vs[ph];
+    };
+    auto store = [&](int buf) {
+        char *lk = smem + buf * L::stage, *lv = lk + L::K;
+#pragma unroll
+        for (int k = 0; k < NI; k++) {
+            const int it = tid + NT * k;
+            if (ITEMS < NT && it >= ITEMS)
+                break;
+            const int row = it / (D / 16), chunk = it % (D / 16);
+            *reinterpret_cast<uint4 *>(lk + k_place<D>(row, chunk)) = rk[k];
+            // 4 keys x 4 dims, keys 4sb .. 4sb+3: quarter q of its group of
+            // 16 is part q/2 of the chunk that half q%2 reads
+            const int dg = it % (D / 4), sb = it / (D / 4), q = sb & 3;
+            uint32_t u[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                u[e] = rv[k][e] ^ 0x80808080u;
+            const int chunk_v = 2 * (sb >> 2) + (q & 1), part = 8 * (q >> 1);
+            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg, chunk_v) + part) =
+                make_uint2(codes_f16<0>(u[0], u[1]), codes_f16<0>(u[2], u[3]));
+            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg + 1, chunk_v) + part) =
+                make_uint2(codes_f16<1>(u[0], u[1]), codes_f16<1>(u[2], u[3]));
+            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg + 2, chunk_v) + part) =
+                make_uint2(codes_f16<2>(u[0], u[1]), codes_f16<2>(u[2], u[3]));
+            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg + 3, chunk_v) + part) =
+                make_uint2(codes_f16<3>(u[0], u[1]), codes_f16<3>(u[2], u[3]));
+        }
+        if (tid < 4) {
+            s_sc[buf][0][tid] = rok ? rks : -1.0f;
+            s_sc[buf][1][tid] = rok && rvs > 0.0f ? 1.0f / rvs : 0.0f;
+            s_sc[buf][2][tid] = rok ? log2f(rvs) : -INFINITY;
+            s_sc[buf][3][tid] = rok ? rvs : 0.0f;
+        }
+    };
+
+    v16f acc[DB] = {};
+    float m = kNone, l = 0.0f, vref = 0.0f, lref = kNone;   // lref: log2 of vref
+    const int steps = ts < te ? (te - ts + kTileKeys - 1) / kTileKeys : 0;
+    if (steps > 0) {
+        load(ts);
+        store(0);
+        load(ts + kTileKeys);
+    }
+    __syncthreads();
+    for (int i = 0; i < steps; i++) {
+        const int t0 = ts + kTileKeys * i;
+        const char *lk = smem + (i & 1) * L::stage, *lv = lk + L::K;
+        if (i + 1 < steps) {
+            store((i + 1) & 1);
+            load(t0 + 2 * kTileKeys);
+        }
+        if (!idle && t0 < seen.hi && t0 + kTileKeys > seen.lo) {
+            const v4f ksc = *reinterpret_cast<const v4f *>(s_sc[i & 1][0]);
+            const v4f ivs = *reinterpret_cast<const v4f *>(s_sc[i & 1][1]);
+            const v4f lvs = *reinterpret_cast<const v4f *>(s_sc[i & 1][2]);
+            const v4f vsc = *reinterpret_cast<const v4f *>(s_sc[i & 1][3]);
+            float x[2][16], fk[4], zm = -INFINITY;
+#pragma unroll
+            for (int gi = 0; gi < 4; gi++)
+                fk[gi] = fmaxf(f * ksc[gi], 1.0e-30f);   // (not 0: a masked score is -inf times it)
+#pragma unroll
+            for (int tt = 0; tt < 2; tt++) {
+                v16i sh = {}, sl = {};
+#pragma unroll
+                for (int ks = 0; ks < KS; ks++) {
+                    const v4i kf = *reinterpret_cast<const v4i *>(lk + k_place<D>(32 * tt + col, 2 * ks + half));
+                    sh = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qh[ks], sh, 0, 0, 0);
+                    sl = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, ql[ks], sl, 0, 0, 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e++)
+                    x[tt][e] = (float)((sh[e] << 7) + sl[e]);
+            }
+            const float kmin = fminf(fminf(ksc[0], ksc[1]), fminf(ksc[2], ksc[3]));
+            const bool whole = t0 >= wlo && t0 + kTileKeys <= whi &&
+                               __builtin_amdgcn_readfirstlane(kmin >= 0.0f ? 1 : 0);
+            if (!whole) {
+#pragma unroll
+                for (int tt = 0; tt < 2; tt++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) {
+                        const int key = t0 + 32 * tt + 8 * (e >> 2) + 4 * half + (e & 3);
+                        const bool see = key < chi && key >= clo && ksc[2 * tt + (e >> 3)] >= 0.0f;
+                        x[tt][e] = see ? x[tt][e] : -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int gi = 0; gi < 4; gi++) {
+                const float *xs = x[gi >> 1] + 8 * (gi & 1);
+                const float g0 = fmaxf(fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])),
+                                       fmaxf(fmaxf(xs[4], xs[5]), fmaxf(xs[6], xs[7])));
+                zm = fmaxf(zm, g0 * fk[gi]);
+            }
+            if (__any(zm > m + 8.0f)) {
+                zm = fmaxf(zm, __shfl_xor(zm, 32, 64));
+                const float mn = fmaxf(m, zm), al = __builtin_amdgcn_exp2f(m - mn);
+#pragma unroll
+                for (int n = 0; n < DB; n++)
+                    acc[n] *= al;
+                l *= al;
+                m = mn;
+            }
+            const float lm = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(
+                int, fmaxf(fmaxf(lvs[0], lvs[1]), fmaxf(lvs[2], lvs[3])))));
+            if (lm > lref) {
+                const float al = __builtin_amdgcn_exp2f(lref - lm);
+#pragma unroll
+                for (int n = 0; n < DB; n++)
+                    acc[n] *= al;
+                lref = lm;
+                vref = fmaxf(fmaxf(vsc[0], vsc[1]), fmaxf(vsc[2], vsc[3]));
+            }
+            // The value scale goes into the exponent, 2^(z - m + log2(vs / vref)),
+            // and out of the sum again, one factor per group of 16 keys.  A
+            // scale too far below the largest would leave fp16's range there:
+            // it is multiplied in afterwards.
+            const float lmin = fminf(fminf(lvs[0], lvs[1]), fminf(lvs[2], lvs[3]));
+            const bool far = __builtin_amdgcn_readfirstlane(lmin - lref < kFar ? 1 : 0);
+            v8h p[4];
+#pragma unroll
+            for (int gi = 0; gi < 4; gi++) {
+                const float lv = lvs[gi] - lref;
+                const bool fr = lv < kFar;
+                const float bias = (fr ? 0.0f : lv) - m;
+                float pe[8], lg = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    pe[e] = __builtin_amdgcn_exp2f(fmaf(x[gi >> 1][8 * (gi & 1) + e], fk[gi], bias));
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    kv_h2 h;
+                    h.x = (_Float16)pe[2 * e];
+                    h.y = (_Float16)pe[2 * e + 1];
+                    lg = __builtin_amdgcn_fdot2(h, (kv_h2){(_Float16)1.0f, (_Float16)1.0f}, lg, false);
+                    p[gi][2 * e] = h.x;
+                    p[gi][2 * e + 1] = h.y;
+                }
+                l = fmaf(lg, fr ? 1.0f : vref * ivs[gi], l);
+                if (far) {
+                    const float ratio = fr ? __builtin_amdgcn_exp2f(lv) : 1.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        p[gi][e] = (_Float16)(pe[e] * ratio);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < DB; n++)
+#pragma unroll
+                for (int gi = 0; gi < 4; gi++) {
+                    const v8h vf = *reinterpret_cast<const v8h *>(lv + v_place(32 * n + col, 2 * gi + half));
+                    acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[gi], acc[n], 0, 0, 0);
+                }
+        }
+        __syncthreads();
+    }
+    if (qcol >= b.nc)
+        return;
+    l += __shfl_xor(l, 32, 64);
+    const float s = l > 0.0f ? vref / l : 0.0f;
+    if (t.splits > 1) {
+        const int64_t at = ((int64_t)item * t.splits + sp) * t.used + qcol;
+#pragma unroll
+        for (int n = 0; n < DB; n++)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4 *>(t.part_o + at * D + 32 * n + 2 * e + 4 * half) =
+                    make_float4(acc[n][e] * s, acc[n][e + 1] * s, acc[n][e + 2] * s, acc[n][e + 3] * s);
+        if (half == 0)
+            t.part_m[at] = l > 0.0f ? m + log2f(l) : kNone;
+        return;
+    }
+    const int c = b.c0 + qcol, i = c / t.group, g = c - i * t.group;
+    const int64_t row = b.q.q0 + i;
+    const int head = b.h * t.group + g;
+    uint16_t *o = t.O + row * t.os + (int64_t)head * D + 4 * half;
+#pragma unroll
+    for (int n = 0; n < DB; n++)
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+            const float x[8] = {acc[n][e] * s, acc[n][e + 1] * s, acc[n][e + 2] * s, acc[n][e + 3] * s,
+                                acc[n][e + 4] * s, acc[n][e + 5] * s, acc[n][e + 6] * s, acc[n][e + 7] * s};
+            const uint4 w = pack8<BF16>(x);
+            *reinterpret_cast<uint2 *>(o + 32 * n + 2 * e) = make_uint2(w.x, w.y);
+            *reinterpret_cast<uint2 *>(o + 32 * n + 2 * e + 8) = make_uint2(w.z, w.w);
+        }
+    if (t.lse && half == 0)
+        t.lse[row * (int64_t)(a.heads * t.group) + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
 // Merges the splits of one column: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M),
 // m_i the split's log2 of its sum.  256 threads: D/8 chunks x split lanes.
 template <int D, bool BF16>
@@ -342,7 +666,7 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t)
     const int tid = threadIdx.x, cc = tid % CPR, sl = tid / CPR;
     const int qc = blockIdx.x % t.used, item = blockIdx.x / t.used;
     Block b;
-    if (!locate(a, t, item, kKvCols, b) || qc >= b.nc)
+    if (!locate(a, t, item, t.cols, b) || qc >= b.nc)
         return;
     const int na = b.span.hi > b.span.lo ? (b.span.hi - b.span.base + t.chunk - 1) / t.chunk : 0;
     float m = kNone, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -395,10 +719,13 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t)
 }
 
 constexpr int kFewTarget = 1024;       // workgroups aimed at: 4 for each CU
+constexpr int kTileTarget = 512;
+constexpr int64_t kTileMinSplit = 1024;
+constexpr int kTileFrom = 64;          // columns from which the tiled kernel is taken
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-int64_t few_items(const li8_kv_batch &b, const li8_kv_cache &c, const KvPlan &p)
+int64_t plan_items(const li8_kv_batch &b, const li8_kv_cache &c, const KvPlan &p)
 {
     return (int64_t)b.seqs * c.heads * p.blocks;
 }
@@ -406,7 +733,16 @@ int64_t few_items(const li8_kv_batch &b, const li8_kv_cache &c, const KvPlan &p)
 template <int D, bool BF16>
 hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipStream_t s)
 {
-    k_kv_few<D, BF16><<<(unsigned)(items * t.splits), 64 * kFewWaves, 0, s>>>(a, t);
+    if (t.cols == kTileCols) {
+        const int64_t pairs = items / t.blocks;
+        // (sequence, head) pairs dealt over the XCDs: 8 lanes, fewer where
+        // that would leave XCDs without work
+        const int lanes = pairs >= 64 ? 8 : (int)std::min<int64_t>(8, pairs & -pairs);
+        k_kv_tiled<D, BF16><<<(unsigned)(round_up(pairs, lanes) * t.blocks * t.splits), 64 * kTileWaves, 0, s>>>(
+            a, t, (int)pairs, lanes);
+    } else {
+        k_kv_few<D, BF16><<<(unsigned)(items * t.splits), 64 * kFewWaves, 0, s>>>(a, t);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || t.splits == 1)
         return e;
@@ -423,17 +759,23 @@ KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, int wi
     if (rows == 0 || b.seqs == 0)
         return p;
     const int64_t cols = rows * group;
-    p.path = LI8_KV_FEW;
-    p.blocks = (int)((cols + kKvCols - 1) / kKvCols);
-    p.used = (int)std::min<int64_t>(kKvCols, cols);
-    const int64_t items = few_items(b, c, p);
+    if (cols >= kTileFrom) {
+        p.path = LI8_KV_TILED;
+        p.cols = kTileCols;
+    } else {
+        p.path = LI8_KV_FEW;
+    }
+    p.blocks = (int)((cols + p.cols - 1) / p.cols);
+    p.used = (int)std::min<int64_t>(p.cols, cols);
+    const int64_t items = plan_items(b, c, p);
     // keys from a span's base to its end at most: a window's keys, the other
     // rows of the block and the rounding of the base
     int64_t span = b.max_kv;
     if (window > 0)
-        span = std::min<int64_t>(span, (int64_t)window + kKvCols + 31);
-    const int64_t chunk = std::max<int64_t>(kKvMinSplit, round_up((items * span + kFewTarget - 1) / kFewTarget,
-                                                                  32 * kFewWaves));
+        span = std::min<int64_t>(span, (int64_t)window + p.cols + 31);
+    const int64_t target = p.path == LI8_KV_TILED ? kTileTarget : kFewTarget;
+    const int64_t least = p.path == LI8_KV_TILED ? kTileMinSplit : kKvMinSplit;
+    const int64_t chunk = std::max(least, round_up((items * span + target - 1) / target, 32 * kFewWaves));
     p.chunk = (int)std::min<int64_t>(chunk, INT32_MAX / 2);
     p.splits = (int)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
     return p;
@@ -442,12 +784,14 @@ KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, int wi
 size_t kv_workspace(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads)
 {
     const KvPlan p = kv_plan(b, c, q_heads, 0);
-    if (p.path != LI8_KV_FEW)
+    if (p.path == LI8_KV_EMPTY)
         return 0;
-    // splits under any window: a part has at least kKvMinSplit keys, and
-    // there are at most kFewTarget / items parts, rounded up
-    const int64_t items = few_items(b, c, p);
-    const int64_t most = std::min<int64_t>((b.max_kv + kKvMinSplit - 1) / kKvMinSplit, kFewTarget / items + 1);
+    // splits under any window: a part has at least `least` keys, and there are
+    // at most target / items parts, rounded up
+    const int64_t items = plan_items(b, c, p);
+    const int64_t target = p.path == LI8_KV_TILED ? kTileTarget : kFewTarget;
+    const int64_t least = p.path == LI8_KV_TILED ? kTileMinSplit : kKvMinSplit;
+    const int64_t most = std::min<int64_t>((b.max_kv + least - 1) / least, target / items + 1);
     if (most <= 1)
         return 0;
     const int64_t parts = items * most * p.used;
@@ -461,14 +805,14 @@ hipError_t launch_kv_attention(KvTokens Q, bool bf16, int q_heads, float scale, 
 {
     const KvPlan p = kv_plan(b, c, q_heads, window);
     const KvArgs a = kv_args(b, c);
-    const int64_t items = few_items(b, c, p);
+    const int64_t items = plan_items(b, c, p);
     AttnArgs t;
     t.Q = Q; t.rope = rope; t.O = O; t.os = os; t.lse = lse;
     t.part_o = reinterpret_cast<float *>(ws);
     t.part_m = reinterpret_cast<float *>(ws + align_up((size_t)items * p.splits * p.used * 4 * c.head_dim, 256));
     t.scale = scale * kLog2e;
     t.group = q_heads / c.heads; t.causal = causal; t.window = window;
-    t.blocks = p.blocks; t.used = p.used; t.splits = p.splits; t.chunk = p.chunk;
+    t.cols = p.cols; t.blocks = p.blocks; t.used = p.used; t.splits = p.splits; t.chunk = p.chunk;
     if (c.head_dim == 128)
         return bf16 ? attention_go<128, true>(a, t, items, s) : attention_go<128, false>(a, t, items, s);
     return bf16 ? attention_go<64, true>(a, t, items, s) : attention_go<64, false>(a, t, items, s);
