@@ -18,8 +18,10 @@
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.h"
+#include "quant_math.h"
 
 namespace li8 {
 namespace {
@@ -41,16 +43,28 @@ struct AttnArgs {
     int64_t os;
     float *lse;
     float *part_o, *part_m;            // [item][split][used][D], [item][split][used]
-    float scale;                       // scale * log2(e)
+    float scale, inv_group;            // scale * log2(e), 1 / group
     int group, causal, window;
     int cols, blocks, used, splits, chunk;
 };
 
-// Where a workgroup's columns lie.
+// Where a workgroup's columns lie.  Column c of a (sequence, head) is row
+// c / group, head c % group of the group.
 struct Block {
     KvSeq q;
     KvSpan span;
     int s, h, c0, nc;                  // sequence, head, first column, columns
+    int i0, g0;                        // row and head of the first column
+    // Row of column c0 + k, k < 256, and its head in g.  In fp32 the quotient
+    // (g0 + k + 1/2) / group is at most 1 + 255 / group and off by less than
+    // 2^-21 of itself, and 1 / (2 group) away from a whole number: its integer
+    // part is right for every group below 2^20.
+    __device__ __forceinline__ int row_of(int k, const AttnArgs &t, int &g) const
+    {
+        const int i = (int)(((float)(g0 + k) + 0.5f) * t.inv_group);
+        g = g0 + k - i * t.group;
+        return i0 + i;
+    }
 };
 
 __device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int item, int cols, Block &b)
@@ -65,9 +79,17 @@ __device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int i
         return false;
     b.c0 = cb * cols;
     b.nc = (int)min((int64_t)cols, ncol - b.c0);
-    b.span = kv_span(b.q.begin + b.c0 / t.group, b.q.begin + (b.c0 + b.nc - 1) / t.group, b.q.len,
-                     t.causal != 0, t.window);
+    b.i0 = b.c0 / t.group;
+    b.g0 = b.c0 - b.i0 * t.group;
+    int g;
+    b.span = kv_span(b.q.begin + b.i0, b.q.begin + b.row_of(b.nc - 1, t, g), b.q.len, t.causal != 0, t.window);
     return true;
+}
+
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), cd = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+    return ab | cd;
 }
 
 // One row's 8 query values (a chunk of D) as two int8 parts; f is the
@@ -83,18 +105,61 @@ __device__ __forceinline__ void split_query(const float x[8], uint2 &hi, uint2 &
 #pragma unroll
     for (int o = 1; o < D / 8; o <<= 1)
         m = fmaxf(m, __shfl_xor(m, o, 64));
-    const float inv = m > 0.0f ? fminf(kQMax / m, FLT_MAX) : 0.0f;
-    f = m * (1.0f / kQMax);
-    uint32_t h[2] = {0, 0}, l[2] = {0, 0};
+    // x inv in [-16256, 16256] plus 1.5 2^23 is rounded half to even to an
+    // integer n in the low bits: n = 128 qh + ql, qh = n >> 7 in -127 .. 127,
+    // ql = n & 127.  (For the least subnormal rows inv is cut to what fp32
+    // holds, which only makes n smaller.)
+    const float inv = m > 0.0f ? fminf(kQMax * __builtin_amdgcn_rcpf(m), FLT_MAX) : 0.0f;
+    f = inv > 0.0f ? 1.0f / inv : 0.0f;
+    uint32_t b[8];
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-        const int qi = (int)fminf(fmaxf(rintf(x[e] * inv), -kQMax), kQMax);
-        const int qh = (qi + 64) >> 7;   // -127 .. 127, and the rest -64 .. 63
-        h[e >> 2] |= ((uint32_t)qh & 0xffu) << (8 * (e & 3));
-        l[e >> 2] |= ((uint32_t)(qi - 128 * qh) & 0xffu) << (8 * (e & 3));
-    }
-    hi = make_uint2(h[0], h[1]);
-    lo = make_uint2(l[0], l[1]);
+    for (int e = 0; e < 8; e++)
+        b[e] = __builtin_bit_cast(uint32_t, fmaf(x[e], inv, 12582912.0f));
+    lo = make_uint2(low_bytes(b[0], b[1], b[2], b[3]) & 0x7f7f7f7fu, low_bytes(b[4], b[5], b[6], b[7]) & 0x7f7f7f7fu);
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        b[e] >>= 7;
+    hi = make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
+}
+
+// The block's query columns into LDS, COLS rows of LQ bytes with the first
+// parts and as many with the second, and their factors.
+template <int D, bool BF16, int COLS, int NT, int LQ>
+__device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t, const Block &b, char *lds,
+                                              float *factor)
+{
+    constexpr int CPR = D / 8, PASSES = COLS * CPR / NT > 0 ? COLS * CPR / NT : 1;
+    constexpr int BATCH = PASSES < 4 ? PASSES : 4;   // rows of a thread in flight
+    const int cc = threadIdx.x % CPR;
+    with_rotation(t.rope, [&](auto rot) {
+        constexpr int ROT = decltype(rot)::value;
+#pragma unroll
+        for (int k0 = 0; k0 < PASSES; k0 += BATCH) {
+            RowChunk w[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; k++) {
+                int g;   // (columns past the last: the last one again)
+                const int qc = min((int)threadIdx.x / CPR + (k0 + k) * (NT / CPR), b.nc - 1);
+                const int i = b.row_of(qc, t, g);
+                fetch_row<ROT>(w[k], t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D,
+                               cc, t.rope, max(b.q.begin + i, 0));
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; k++) {
+                const int qc = threadIdx.x / CPR + (k0 + k) * (NT / CPR);
+                float x[8], f;
+                uint2 hi, lo;
+                rotate_row<BF16, ROT>(w[k], cc, t.rope, x);
+                split_query<D>(x, hi, lo, f);
+                if (COLS * CPR < NT && qc >= COLS)
+                    continue;
+                *reinterpret_cast<uint2 *>(lds + qc * LQ + 8 * cc) = hi;
+                *reinterpret_cast<uint2 *>(lds + (COLS + qc) * LQ + 8 * cc) = lo;
+                if (cc == 0)
+                    factor[qc] = f * t.scale;
+            }
+        }
+    });
 }
 
 // Codes of byte `byte` of two keys' words (already offset by 128: 0..255) as
@@ -172,20 +237,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_few(KvArgs a, AttnArgs t)
         return;                        // (the merging kernel knows how many there are)
     const int qc = tid / CPR, cc = tid % CPR;   // column and chunk of the query and output phases
 
-    if (qc < kKvCols) {
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f;
-        if (qc < b.nc) {
-            const int c = b.c0 + qc, i = c / t.group, g = c - i * t.group;
-            load_rotated8<BF16>(t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D,
-                                cc, t.rope, max(b.q.begin + i, 0), x);
-        }
-        uint2 hi, lo;
-        split_query<D>(x, hi, lo, f);
-        *reinterpret_cast<uint2 *>(smem + qc * LQ + 8 * cc) = hi;
-        *reinterpret_cast<uint2 *>(smem + (kKvCols + qc) * LQ + 8 * cc) = lo;
-        if (cc == 0)
-            s_f[qc] = f * t.scale;
-    }
+    split_queries<D, BF16, kKvCols, 64 * kFewWaves, LQ>(a, t, b, smem, s_f);
     __syncthreads();
     const int col = lane & 15, g = lane >> 4;
     v4i qh[KS], ql[KS];
@@ -198,7 +250,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_few(KvArgs a, AttnArgs t)
     __syncthreads();                   // smem is used again below
 
     // keys this lane's column sees: [clo, chi)
-    const int pos = b.q.begin + (b.c0 + col) / t.group;
+    int gcol;
+    const int pos = b.q.begin + b.row_of(col, t, gcol);
     int chi = t.causal ? min(te, pos + 1) : te;
     const int clo = t.window > 0 ? max((int64_t)0, (int64_t)pos + 1 - t.window) : 0;
     if (col >= b.nc)
@@ -324,7 +377,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_few(KvArgs a, AttnArgs t)
             t.part_m[at] = L > 0.0f ? M + log2f(L) : kNone;
         return;
     }
-    const int c = b.c0 + qc, i = c / t.group, gq = c - i * t.group;
+    int gq;
+    const int i = b.row_of(qc, t, gq);
     const int64_t row = b.q.q0 + i;
     const int head = b.h * t.group + gq;
     *reinterpret_cast<uint4 *>(t.O + row * t.os + (int64_t)head * D + 8 * cc) = pack8<BF16>(o);
@@ -341,10 +395,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_few(KvArgs a, AttnArgs t)
 constexpr int kTileWaves = 8;
 constexpr int kTileCols = 32 * kTileWaves;
 constexpr int kTileKeys = 64;
-constexpr float kFar = -12.0f;         // log2: value scales this far below the largest
+constexpr float kLeast = -100.0f;      // log2 of the smallest relative value scale
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 
 // 16-byte chunks of the LDS tiles are permuted within 128 bytes so that
 // neither the fragment reads (32 rows, one chunk each) nor the writes of V
@@ -364,29 +419,33 @@ struct TileLds {
     static constexpr int K = kTileKeys * D, V = D * kTileKeys * 2;
     static constexpr int stage = K + V;
     static constexpr int q_row = D + 16;
-    static constexpr int bytes = 2 * stage > 2 * kTileCols * q_row ? 2 * stage : 2 * kTileCols * q_row;
+    static constexpr int bytes = 3 * stage > 2 * kTileCols * q_row ? 3 * stage : 2 * kTileCols * q_row;
 };
 
 template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnArgs t, int pairs, int lanes)
+__global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnArgs t, int pairs, int lanes, int deep)
 {
     constexpr int NT = 64 * kTileWaves, CPR = D / 8, KS = D / 32, DB = D / 32;
-    constexpr int NI = kTileKeys * D / 16 / NT > 0 ? kTileKeys * D / 16 / NT : 1;   // staging items of a thread
-    constexpr int ITEMS = kTileKeys * D / 16;
+    constexpr int ITEMS = kTileKeys * D / 16;   // pieces to stage, at most one for each thread
+    static_assert(ITEMS <= NT && ITEMS % 256 == 0, "staging");
     using L = TileLds<D>;
     __shared__ __align__(16) char smem[L::bytes];
     __shared__ float s_f[kTileCols];
-    __shared__ __align__(16) float s_sc[2][4][4];   // [buffer][ks, 1/vs, log2 vs, vs][group of 16 keys]
+    __shared__ __align__(16) float s_sc[3][4][4];   // [buffer][group of 16 keys][k scale, log2 v scale, 0 or -inf]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // Blocks of one (sequence, head) share its keys: all on 8 / lanes of the
-    // XCDs (the hardware deals workgroups to the 8 XCDs in turn), the last
-    // block, which sees the most keys, first.
-    const int j = blockIdx.x / lanes, per = t.blocks * t.splits;
-    const int pair = (j / per) * lanes + blockIdx.x % lanes;
+    // Blocks of one (sequence, head) share its keys: they stay on 8 / lanes
+    // of the XCDs (the hardware deals workgroups to the 8 XCDs in turn).
+    // Where a chunk is most of its sequence (deep == 0) its last blocks see
+    // the most keys and go first, those of all pairs of the lane before any
+    // block that sees fewer: a long block that starts late would run alone at
+    // the end.  Chunks over much longer sequences have blocks alike, and one
+    // pair goes after the other, so that its keys stay in the L2.
+    const int j = blockIdx.x / lanes, ppl = (pairs + lanes - 1) / lanes, per = t.blocks * t.splits;
+    const int pair = (deep ? j / per : j % ppl) * lanes + blockIdx.x % lanes;
     if (pair >= pairs)
         return;
-    const int rest = j % per, sp = rest % t.splits;
+    const int rest = deep ? j % per : j / ppl, sp = rest % t.splits;
     const int item = pair * t.blocks + (t.blocks - 1 - rest / t.splits);
     Block b;
     if (!locate(a, t, item, kTileCols, b))
@@ -396,22 +455,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
     if (ts >= te && t.splits > 1)
         return;
 
-#pragma unroll
-    for (int k = 0; k < CPR / 2; k++) {
-        const int it = tid + NT * k, qc = it / CPR, cc = it % CPR;
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f;
-        if (qc < b.nc) {
-            const int c = b.c0 + qc, i = c / t.group, g = c - i * t.group;
-            load_rotated8<BF16>(t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D,
-                                cc, t.rope, max(b.q.begin + i, 0), x);
-        }
-        uint2 hi, lo;
-        split_query<D>(x, hi, lo, f);
-        *reinterpret_cast<uint2 *>(smem + qc * L::q_row + 8 * cc) = hi;
-        *reinterpret_cast<uint2 *>(smem + (kTileCols + qc) * L::q_row + 8 * cc) = lo;
-        if (cc == 0)
-            s_f[qc] = f * t.scale;
-    }
+    split_queries<D, BF16, kTileCols, NT, L::q_row>(a, t, b, smem, s_f);
     __syncthreads();
     const int col = lane & 31, half = lane >> 5, qcol = 32 * wid + col;
     v4i qh[KS], ql[KS];
@@ -425,207 +469,325 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
 
     // keys this lane's column sees, [clo, chi), and what all columns of the
     // wave see, [wlo, whi), or any of them, [ulo, uhi)
-    const int pos = b.q.begin + (b.c0 + qcol) / t.group;
+    int gcol, gdrop;
+    const int pos = b.q.begin + b.row_of(qcol, t, gcol);
     int chi = t.causal ? min(te, pos + 1) : te;
     int clo = t.window > 0 ? max((int64_t)0, (int64_t)pos + 1 - t.window) : 0;
     if (qcol >= b.nc)
         chi = clo = 0;
     const int c_first = 32 * wid, c_last = min(32 * wid + 31, b.nc - 1);
-    const int p_first = b.q.begin + (b.c0 + c_first) / t.group, p_last = b.q.begin + (b.c0 + c_last) / t.group;
+    const int p_first = b.q.begin + b.row_of(c_first, t, gdrop), p_last = b.q.begin + b.row_of(max(c_last, 0), t, gdrop);
     const KvSpan seen = kv_span(p_first, p_last, te, t.causal != 0, t.window);
     const bool idle = c_first >= b.nc;
     const int whi = c_last < 32 * wid + 31 ? 0 : t.causal ? min(te, p_first + 1) : te;
     const int wlo = t.window > 0 ? max((int64_t)0, (int64_t)p_last + 1 - t.window) : 0;
 
+    // Staging: a wave's 16-byte pieces of K and its 4 x 4 blocks of V lie in
+    // one group of 16 keys, so in one page: the page's address is the wave's,
+    // in scalar registers.  Page numbers are requested two steps ahead of the
+    // data that they address, the data one step ahead of the step that uses
+    // it.  (Page numbers and scales are asked for with a lane's offset of 0,
+    // as vector loads: a scalar load in flight makes every read of LDS wait
+    // for it, since the two count together and end in any order.)
+    int zero;
+    asm("v_mov_b32 %0, 0" : "=v"(zero));
     const int32_t *table = a.table + (int64_t)b.s * a.table_stride;
-    const int page = 1 << a.page_shift;
-    uint4 rk[NI];
-    uint32_t rv[NI][4];
+    const int it = tid % ITEMS, group = wid * 64 % ITEMS / (ITEMS / 4);
+    const int krow = it / (D / 16), kchunk = it % (D / 16), dg = it % (D / 4), sb = it / (D / 4);
+    const uint32_t koff = (krow & 15) * D + 16 * kchunk, voff = 4 * (sb & 3) * D + 4 * dg;
+    const int kput = k_place<D>(krow, kchunk);
+    // 4 keys x 4 dims: quarter q = sb % 4 of a group of 16 keys is part q / 2
+    // of the chunk that half q % 2 reads
+    int vput = L::K + v_place(4 * dg, 2 * (sb >> 2) + (sb & 1)) + 8 * ((sb >> 1) & 1);
+    uint4 rk;
+    uint32_t rv[4];
     float rks = 0.0f, rvs = 0.0f;
     bool rok = false;
-    auto page_of = [&](int key, bool &ok) {
-        const int pid = table[min(key >> a.page_shift, a.table_width - 1)];
-        ok = (unsigned)pid < (unsigned)a.pages && (key & ~15) < te && (key | 15) >= b.span.lo;
-        return (int64_t)(ok ? pid : 0) * a.heads + b.h;
-    };
+    int vpid = 0;
+    auto pages = [&](int t0) { vpid = table[min((t0 + 16 * group) >> a.page_shift, a.table_width - 1) + zero]; };
     auto load = [&](int t0) {
+        const int pid = __builtin_amdgcn_readfirstlane(vpid), key = t0 + 16 * group;
+        rok = (unsigned)pid < (unsigned)a.pages && key < te && key + 16 > b.span.lo;
+        const int64_t ph = (int64_t)(rok ? pid : 0) * a.heads + b.h;
+        const int64_t at = ((ph * D) << a.page_shift) + (key & ((1 << a.page_shift) - 1)) * D;
+        rk = *reinterpret_cast<const uint4 *>(a.k + at + koff);
 #pragma unroll
-        for (int k = 0; k < NI; k++) {
-            const int it = (tid + NT * k) % ITEMS;
-            const int row = it / (D / 16), chunk = it % (D / 16);
-            bool ok;
-            int64_t ph = page_of(t0 + row, ok);
-            rk[k] = *reinterpret_cast<const uint4 *>(a.k + ((ph * D) << a.page_shift) +
-                                                     ((t0 + row) & (page - 1)) * D + 16 * chunk);
-            const int dg = it % (D / 4), sb = it / (D / 4), key = t0 + 4 * sb;
-            ph = page_of(key, ok);
-            const int8_t *p = a.v + ((ph * D) << a.page_shift) + (key & (page - 1)) * D + 4 * dg;
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                rv[k][e] = *reinterpret_cast<const uint32_t *>(p + e * D);
-        }
-        const int64_t ph = page_of(t0 + 16 * (tid & 3), rok);
-        rks = a.ks[ph];
-        rvs = a.vs[ph];
+        for (int e = 0; e < 4; e++)
+            rv[e] = *reinterpret_cast<const uint32_t *>(a.v + at + e * D + voff);
+        rks = a.ks[ph + zero];
+        rvs = a.vs[ph + zero];
     };
     auto store = [&](int buf) {
-        char *lk = smem + buf * L::stage, *lv = lk + L::K;
+        if (ITEMS < NT && tid >= ITEMS)
+            return;
+        const int at = buf * L::stage;
+        asm("" : "+v"(vput));
+        *reinterpret_cast<uint4 *>(smem + at + kput) = rk;
+        uint32_t u[4];
 #pragma unroll
-        for (int k = 0; k < NI; k++) {
-            const int it = tid + NT * k;
-            if (ITEMS < NT && it >= ITEMS)
-                break;
-            const int row = it / (D / 16), chunk = it % (D / 16);
-            *reinterpret_cast<uint4 *>(lk + k_place<D>(row, chunk)) = rk[k];
-            // 4 keys x 4 dims, keys 4sb .. 4sb+3: quarter q of its group of
-            // 16 is part q/2 of the chunk that half q%2 reads
-            const int dg = it % (D / 4), sb = it / (D / 4), q = sb & 3;
-            uint32_t u[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                u[e] = rv[k][e] ^ 0x80808080u;
-            const int chunk_v = 2 * (sb >> 2) + (q & 1), part = 8 * (q >> 1);
-            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg, chunk_v) + part) =
-                make_uint2(codes_f16<0>(u[0], u[1]), codes_f16<0>(u[2], u[3]));
-            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg + 1, chunk_v) + part) =
-                make_uint2(codes_f16<1>(u[0], u[1]), codes_f16<1>(u[2], u[3]));
-            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg + 2, chunk_v) + part) =
-                make_uint2(codes_f16<2>(u[0], u[1]), codes_f16<2>(u[2], u[3]));
-            *reinterpret_cast<uint2 *>(lv + v_place(4 * dg + 3, chunk_v) + part) =
-                make_uint2(codes_f16<3>(u[0], u[1]), codes_f16<3>(u[2], u[3]));
-        }
-        if (tid < 4) {
-            s_sc[buf][0][tid] = rok ? rks : -1.0f;
-            s_sc[buf][1][tid] = rok && rvs > 0.0f ? 1.0f / rvs : 0.0f;
-            s_sc[buf][2][tid] = rok ? log2f(rvs) : -INFINITY;
-            s_sc[buf][3][tid] = rok ? rvs : 0.0f;
+        for (int e = 0; e < 4; e++)
+            u[e] = rv[e] ^ 0x80808080u;
+        *reinterpret_cast<uint2 *>(smem + (at + vput)) =
+            make_uint2(codes_f16<0>(u[0], u[1]), codes_f16<0>(u[2], u[3]));
+        *reinterpret_cast<uint2 *>(smem + ((at + vput) ^ 16) + 128) =
+            make_uint2(codes_f16<1>(u[0], u[1]), codes_f16<1>(u[2], u[3]));
+        *reinterpret_cast<uint2 *>(smem + ((at + vput) ^ 32) + 256) =
+            make_uint2(codes_f16<2>(u[0], u[1]), codes_f16<2>(u[2], u[3]));
+        *reinterpret_cast<uint2 *>(smem + ((at + vput) ^ 48) + 384) =
+            make_uint2(codes_f16<3>(u[0], u[1]), codes_f16<3>(u[2], u[3]));
+        if (lane == 0) {   // (the waves of a group write the same)
+            // no such page: a factor of 0, and -inf added to every score
+            *reinterpret_cast<v4f *>(s_sc[buf][group]) =
+                rok ? v4f{rks, __builtin_amdgcn_logf(rvs), 0.0f, 0.0f} : v4f{0.0f, -INFINITY, -INFINITY, 0.0f};
         }
     };
 
-    v16f acc[DB] = {};
-    float m = kNone, l = 0.0f, vref = 0.0f, lref = kNone;   // lref: log2 of vref
+    // The wave's part of the steps: those that any of its columns sees.
     const int steps = ts < te ? (te - ts + kTileKeys - 1) / kTileKeys : 0;
-    if (steps > 0) {
-        load(ts);
-        store(0);
-        load(ts + kTileKeys);
-    }
-    __syncthreads();
-    for (int i = 0; i < steps; i++) {
-        const int t0 = ts + kTileKeys * i;
-        const char *lk = smem + (i & 1) * L::stage, *lv = lk + L::K;
-        if (i + 1 < steps) {
-            store((i + 1) & 1);
-            load(t0 + 2 * kTileKeys);
+    const bool some = !idle && seen.hi > seen.lo && seen.hi > ts;
+    const int first = some ? max(seen.lo - ts, 0) / kTileKeys : steps;
+    const int last = some ? min((seen.hi - ts + kTileKeys - 1) / kTileKeys, steps) : steps;
+
+    // A subtile is 32 keys.  MFMA and VALU work of neighbouring subtiles is
+    // independent and put side by side, instruction by instruction:
+    //   X(j)  O^T += V^T P^T of subtile j - 1  |  the scores of j as floats, their maximum
+    //   Y(j)  S^T of subtile j + 1             |  the probabilities of j
+    // with the rare change of the running maximum between them.  The waves
+    // run in step at the barriers, so what one wave leaves idle the other on
+    // its SIMD leaves idle too; and the compiler, left to itself, puts the
+    // MFMAs of a block in a row and the VALU work behind them.
+    v16f acc[DB] = {};
+    v16i si;
+    float x[16];
+    v8h p[2], vf[DB];
+    v4i kf[KS];
+    v4f sc[2];
+    float m = kNone, l = 0.0f, lref = kNone;   // lref: log2 of the largest value scale so far
+
+    // LDS places: the permutation of the chunks is an exclusive or, so all of
+    // a lane's places follow from one (kept out of the compiler's sight, which
+    // would hold each of them in a register of its own).
+    int kplace = k_place<D>(col, half), vplace = L::K + v_place(col, half);
+    auto read_k = [&](int buf, int tt) {
+        asm("" : "+v"(kplace));
+        const int at = kplace + buf * L::stage;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+            kf[ks] = *reinterpret_cast<const v4i *>(smem + (at ^ (32 * ks)) + 32 * D * tt);
+    };
+    auto read_v1 = [&](int buf, int tt, int gi, int n) {
+        vf[n] = *reinterpret_cast<const v8h *>(smem + ((vplace + buf * L::stage) ^ (64 * (tt ^ (n & 1)) + 32 * gi)) +
+                                               4096 * n);
+    };
+    auto read_v = [&](int buf, int tt, int gi) {
+        asm("" : "+v"(vplace));
+#pragma unroll
+        for (int n = 0; n < DB; n++)
+            read_v1(buf, tt, gi, n);
+    };
+#define LI8_FENCE __builtin_amdgcn_sched_barrier(0)
+    auto mfma_k = [&](int ks, const v4i (&q)[KS]) {
+        si = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf[ks], q[ks], si, 0, 0, 0);
+        LI8_FENCE;
+    };
+    auto mfma_v = [&](int n, int gi) {
+        acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[n], p[gi], acc[n], 0, 0, 0);
+        LI8_FENCE;
+    };
+    auto to_float = [&](int e0) {
+#pragma unroll
+        for (int e = e0; e < e0 + 4; e++)
+            x[e] = (float)si[e];
+        LI8_FENCE;
+    };
+    // Four probabilities.  The value scale goes into the exponent,
+    // 2^(z - m + log2(vs / vref)), and out of the sum again.
+    float bias[2], lv[2];
+    auto exps = [&](int e0) {
+#pragma unroll
+        for (int e = e0; e < e0 + 4; e++)
+            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], sc[e >> 3].x, bias[e >> 3]));
+        LI8_FENCE;
+    };
+    auto to_half = [&](int gi) {
+        const float *y = x + 8 * gi;
+        const float lg = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+        l = fmaf(lg, __builtin_amdgcn_exp2f(-lv[gi]), l);
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            p[gi][e] = (_Float16)y[e];
+        LI8_FENCE;
+    };
+    // X: PV of the subtile before (its first fragments are in vf, each
+    // replaced by its second as soon as it is used), this one's scores as
+    // floats; kf is read on the way.
+    auto part_x = [&](int vbuf, int vtt, int buf, int tt, int kbuf, int ktt) {
+        sc[0] = *reinterpret_cast<const v4f *>(s_sc[buf][2 * tt]);
+        sc[1] = *reinterpret_cast<const v4f *>(s_sc[buf][2 * tt + 1]);
+        asm("" : "+v"(vplace));
+        LI8_FENCE;
+#pragma unroll
+        for (int n = 0; n < DB; n++) {
+            mfma_v(n, 0);
+            read_v1(vbuf, vtt, 1, n);
+            LI8_FENCE;
         }
-        if (!idle && t0 < seen.hi && t0 + kTileKeys > seen.lo) {
-            const v4f ksc = *reinterpret_cast<const v4f *>(s_sc[i & 1][0]);
-            const v4f ivs = *reinterpret_cast<const v4f *>(s_sc[i & 1][1]);
-            const v4f lvs = *reinterpret_cast<const v4f *>(s_sc[i & 1][2]);
-            const v4f vsc = *reinterpret_cast<const v4f *>(s_sc[i & 1][3]);
-            float x[2][16], fk[4], zm = -INFINITY;
 #pragma unroll
-            for (int gi = 0; gi < 4; gi++)
-                fk[gi] = fmaxf(f * ksc[gi], 1.0e-30f);   // (not 0: a masked score is -inf times it)
+        for (int n = 0; n < DB; n++) {
+            to_float(16 / DB * n);
+            if (DB == 2)
+                to_float(8 * n + 4);
+            mfma_v(n, 1);
+        }
+        read_k(kbuf, ktt);
+        LI8_FENCE;
+    };
+    // Y: the next subtile's products with the queries (kf), this one's
+    // probabilities; vf is read on the way.
+    auto part_y = [&](int buf, int tt) {
+        read_v(buf, tt, 0);
+        si = v16i{};
 #pragma unroll
-            for (int tt = 0; tt < 2; tt++) {
-                v16i sh = {}, sl = {};
+        for (int gi = 0; gi < 2; gi++) {
+            lv[gi] = fmaxf(sc[gi].y - lref, kLeast);
+            bias[gi] = lv[gi] - m + sc[gi].z;
+        }
+        LI8_FENCE;
+        if constexpr (KS == 4) {
+            mfma_k(0, qh); exps(0);
+            mfma_k(1, qh); exps(4);
+            mfma_k(2, qh); to_half(0);
+            mfma_k(3, qh); exps(8);
+        } else {
+            mfma_k(0, qh); exps(0); exps(4);
+            mfma_k(1, qh); to_half(0); exps(8);
+        }
+        si <<= 7;
+        LI8_FENCE;
+        if constexpr (KS == 4) {
+            mfma_k(0, ql); exps(12);
+            mfma_k(1, ql); to_half(1);
+            mfma_k(2, ql);
+            mfma_k(3, ql);
+        } else {
+            mfma_k(0, ql); exps(12);
+            mfma_k(1, ql); to_half(1);
+        }
+    };
+    // Masks, the maximum, and what changes with it.
+    auto settle = [&](int t0) {
+        if (t0 < wlo || t0 + 32 > whi) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ks++) {
-                    const v4i kf = *reinterpret_cast<const v4i *>(lk + k_place<D>(32 * tt + col, 2 * ks + half));
-                    sh = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, qh[ks], sh, 0, 0, 0);
-                    sl = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf, ql[ks], sl, 0, 0, 0);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; e++)
-                    x[tt][e] = (float)((sh[e] << 7) + sl[e]);
+            for (int e = 0; e < 16; e++) {
+                const int key = t0 + 8 * (e >> 2) + 4 * half + (e & 3);
+                x[e] = key < chi && key >= clo ? x[e] : -INFINITY;
             }
-            const float kmin = fminf(fminf(ksc[0], ksc[1]), fminf(ksc[2], ksc[3]));
-            const bool whole = t0 >= wlo && t0 + kTileKeys <= whi &&
-                               __builtin_amdgcn_readfirstlane(kmin >= 0.0f ? 1 : 0);
-            if (!whole) {
+        }
+        // the factor of the integers (not 0: a masked score is -inf times it)
+        sc[0].x = fmaxf(f * sc[0].x, 1.0e-30f);
+        sc[1].x = fmaxf(f * sc[1].x, 1.0e-30f);
+        float g[2];
 #pragma unroll
-                for (int tt = 0; tt < 2; tt++)
-#pragma unroll
-                    for (int e = 0; e < 16; e++) {
-                        const int key = t0 + 32 * tt + 8 * (e >> 2) + 4 * half + (e & 3);
-                        const bool see = key < chi && key >= clo && ksc[2 * tt + (e >> 3)] >= 0.0f;
-                        x[tt][e] = see ? x[tt][e] : -INFINITY;
-                    }
-            }
-#pragma unroll
-            for (int gi = 0; gi < 4; gi++) {
-                const float *xs = x[gi >> 1] + 8 * (gi & 1);
-                const float g0 = fmaxf(fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])),
-                                       fmaxf(fmaxf(xs[4], xs[5]), fmaxf(xs[6], xs[7])));
-                zm = fmaxf(zm, g0 * fk[gi]);
-            }
-            if (__any(zm > m + 8.0f)) {
-                zm = fmaxf(zm, __shfl_xor(zm, 32, 64));
-                const float mn = fmaxf(m, zm), al = __builtin_amdgcn_exp2f(m - mn);
-#pragma unroll
-                for (int n = 0; n < DB; n++)
-                    acc[n] *= al;
-                l *= al;
-                m = mn;
-            }
-            const float lm = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(
-                int, fmaxf(fmaxf(lvs[0], lvs[1]), fmaxf(lvs[2], lvs[3])))));
-            if (lm > lref) {
-                const float al = __builtin_amdgcn_exp2f(lref - lm);
-#pragma unroll
-                for (int n = 0; n < DB; n++)
-                    acc[n] *= al;
-                lref = lm;
-                vref = fmaxf(fmaxf(vsc[0], vsc[1]), fmaxf(vsc[2], vsc[3]));
-            }
-            // The value scale goes into the exponent, 2^(z - m + log2(vs / vref)),
-            // and out of the sum again, one factor per group of 16 keys.  A
-            // scale too far below the largest would leave fp16's range there:
-            // it is multiplied in afterwards.
-            const float lmin = fminf(fminf(lvs[0], lvs[1]), fminf(lvs[2], lvs[3]));
-            const bool far = __builtin_amdgcn_readfirstlane(lmin - lref < kFar ? 1 : 0);
-            v8h p[4];
-#pragma unroll
-            for (int gi = 0; gi < 4; gi++) {
-                const float lv = lvs[gi] - lref;
-                const bool fr = lv < kFar;
-                const float bias = (fr ? 0.0f : lv) - m;
-                float pe[8], lg = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    pe[e] = __builtin_amdgcn_exp2f(fmaf(x[gi >> 1][8 * (gi & 1) + e], fk[gi], bias));
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    kv_h2 h;
-                    h.x = (_Float16)pe[2 * e];
-                    h.y = (_Float16)pe[2 * e + 1];
-                    lg = __builtin_amdgcn_fdot2(h, (kv_h2){(_Float16)1.0f, (_Float16)1.0f}, lg, false);
-                    p[gi][2 * e] = h.x;
-                    p[gi][2 * e + 1] = h.y;
-                }
-                l = fmaf(lg, fr ? 1.0f : vref * ivs[gi], l);
-                if (far) {
-                    const float ratio = fr ? __builtin_amdgcn_exp2f(lv) : 1.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        p[gi][e] = (_Float16)(pe[e] * ratio);
-                }
-            }
+        for (int gi = 0; gi < 2; gi++) {
+            const float *y = x + 8 * gi;
+            g[gi] = fmaxf(fmaxf(fmaxf(fmaxf(y[0], y[1]), y[2]), fmaxf(fmaxf(y[3], y[4]), y[5])), fmaxf(y[6], y[7]));
+            g[gi] = fmaf(g[gi], sc[gi].x, sc[gi].z);
+        }
+        float zm = fmaxf(g[0], g[1]);
+        const float lm = fmaxf(sc[0].y, sc[1].y);
+        // The maximum is moved only when a score is 8 above it (in powers of
+        // two): until then the probabilities stay below 2^8.
+        if (__any(zm > m + 8.0f || lm > lref)) {
+            zm = fmaxf(zm, __shfl_xor(zm, 32, 64));
+            const float mn = zm > m + 8.0f ? zm : m, ln = lm > lref ? lm + 0.5f : lref;   // (some room)
+            const float am = __builtin_amdgcn_exp2f(m - mn);
+            const float al = am * __builtin_amdgcn_exp2f(lref - ln);
 #pragma unroll
             for (int n = 0; n < DB; n++)
-#pragma unroll
-                for (int gi = 0; gi < 4; gi++) {
-                    const v8h vf = *reinterpret_cast<const v8h *>(lv + v_place(32 * n + col, 2 * gi + half));
-                    acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[gi], acc[n], 0, 0, 0);
-                }
+                acc[n] *= al;
+            l *= am;
+            m = mn;
+            lref = ln;
         }
-        __syncthreads();
+    };
+
+    if (steps > 0) {
+        pages(ts);
+        load(ts);
+        pages(ts + kTileKeys);
+        store(0);
+        load(ts + kTileKeys);
+        pages(ts + 2 * kTileKeys);
     }
+    __syncthreads();
+    int buf = 0, pbuf = 0, i = 0;
+    // Three buffers: tile i + 1 goes where tile i - 2 was, which every wave
+    // has left behind before the last barrier.
+    auto next = [&]() { return buf == 2 ? 0 : buf + 1; };
+    auto stage = [&]() {
+        if (i + 1 < steps) {
+            store(next());
+            load(ts + kTileKeys * (i + 2));
+            pages(ts + kTileKeys * (i + 3));
+        }
+    };
+    auto leave = [&]() {
+        pbuf = buf;
+        buf = next();
+    };
+    // (three loops, so that the middle one has no other way through it: the
+    // compiler would keep the accumulators twice)
+    for (; i < first; i++) {
+        stage();
+        lds_barrier();
+        leave();
+    }
+    if (first < last) {
+        read_k(buf, 0);
+        si = v16i{};
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+            si = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf[ks], qh[ks], si, 0, 0, 0);
+        si <<= 7;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+            si = __builtin_amdgcn_mfma_i32_32x32x32_i8(kf[ks], ql[ks], si, 0, 0, 0);
+        p[0] = p[1] = v8h{};   // (nothing to add yet)
+#pragma unroll
+        for (int n = 0; n < DB; n++)
+            vf[n] = v8h{};
+        pbuf = buf;
+        for (; i < last; i++) {
+            const int t0 = ts + kTileKeys * i;
+            stage();
+            part_x(pbuf, 1, buf, 0, buf, 1);
+            settle(t0);
+            part_y(buf, 0);
+            part_x(buf, 0, buf, 1, buf, 1);
+            settle(t0 + 32);
+            lds_barrier();
+            read_k(next(), 0);   // (past the last step: of no use, and not used)
+            part_y(buf, 1);
+            leave();
+        }
+#pragma unroll
+        for (int n = 0; n < DB; n++)
+            mfma_v(n, 0);
+        read_v(pbuf, 1, 1);
+#pragma unroll
+        for (int n = 0; n < DB; n++)
+            mfma_v(n, 1);
+    }
+    for (; i < steps; i++) {
+        stage();
+        lds_barrier();
+        leave();
+    }
+#undef LI8_FENCE
     if (qcol >= b.nc)
         return;
     l += __shfl_xor(l, 32, 64);
-    const float s = l > 0.0f ? vref / l : 0.0f;
+    const float s = l > 0.0f ? __builtin_amdgcn_exp2f(lref) / l : 0.0f;
     if (t.splits > 1) {
         const int64_t at = ((int64_t)item * t.splits + sp) * t.used + qcol;
 #pragma unroll
@@ -638,9 +800,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
             t.part_m[at] = l > 0.0f ? m + log2f(l) : kNone;
         return;
     }
-    const int c = b.c0 + qcol, i = c / t.group, g = c - i * t.group;
-    const int64_t row = b.q.q0 + i;
-    const int head = b.h * t.group + g;
+    const int64_t row = b.q.q0 + (pos - b.q.begin);
+    const int head = b.h * t.group + gcol;
     uint16_t *o = t.O + row * t.os + (int64_t)head * D + 4 * half;
 #pragma unroll
     for (int n = 0; n < DB; n++)
@@ -710,7 +871,8 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t)
 #pragma unroll
     for (int k = 0; k < 8; k++)
         o[k] *= inv;
-    const int c = b.c0 + qc, i = c / t.group, g = c - i * t.group;
+    int g;
+    const int i = b.row_of(qc, t, g);
     const int64_t row = b.q.q0 + i;
     const int head = b.h * t.group + g;
     *reinterpret_cast<uint4 *>(t.O + row * t.os + (int64_t)head * D + 8 * cc) = pack8<BF16>(o);
@@ -739,7 +901,7 @@ hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipSt
         // that would leave XCDs without work
         const int lanes = pairs >= 64 ? 8 : (int)std::min<int64_t>(8, pairs & -pairs);
         k_kv_tiled<D, BF16><<<(unsigned)(round_up(pairs, lanes) * t.blocks * t.splits), 64 * kTileWaves, 0, s>>>(
-            a, t, (int)pairs, lanes);
+            a, t, (int)pairs, lanes, !t.causal || a.max_q < a.max_kv / 2);
     } else {
         k_kv_few<D, BF16><<<(unsigned)(items * t.splits), 64 * kFewWaves, 0, s>>>(a, t);
     }
@@ -811,7 +973,7 @@ hipError_t launch_kv_attention(KvTokens Q, bool bf16, int q_heads, float scale, 
     t.part_o = reinterpret_cast<float *>(ws);
     t.part_m = reinterpret_cast<float *>(ws + align_up((size_t)items * p.splits * p.used * 4 * c.head_dim, 256));
     t.scale = scale * kLog2e;
-    t.group = q_heads / c.heads; t.causal = causal; t.window = window;
+    t.group = q_heads / c.heads; t.inv_group = 1.0f / (float)t.group; t.causal = causal; t.window = window;
     t.cols = p.cols; t.blocks = p.blocks; t.used = p.used; t.splits = p.splits; t.chunk = p.chunk;
     if (c.head_dim == 128)
         return bf16 ? attention_go<128, true>(a, t, items, s) : attention_go<128, false>(a, t, items, s);

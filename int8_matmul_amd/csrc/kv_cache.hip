@@ -66,18 +66,25 @@ __global__ __launch_bounds__(THREADS) void k_kv_append(KvArgs a, KvTokens K, KvT
         rr.cos = nullptr;
     const int c = tid % CPR, ra = tid / CPR;
     float x[RPT][8], m = 0.0f;
+    with_rotation(rr, [&](auto rot) {
+        constexpr int ROT = decltype(rot)::value, BATCH = RPT < 4 ? RPT : 4;   // rows in flight
 #pragma unroll
-    for (int k = 0; k < RPT; k++) {
-        const int pos = lo + ra + RA * k;
+        for (int k0 = 0; k0 < RPT; k0 += BATCH) {
+            RowChunk w[BATCH];
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-            x[k][e] = 0.0f;
-        if (pos < hi)
-            load_rotated8<BF16>(src.p + (q.q0 + pos - q.begin) * src.stride + h * D, c, rr, pos, x[k]);
+            for (int k = 0; k < BATCH; k++) {   // (rows past the end: the last one again)
+                const int pos = min(lo + ra + RA * (k0 + k), hi - 1);
+                fetch_row<ROT>(w[k], src.p + (q.q0 + pos - q.begin) * src.stride + h * D, c, rr, pos);
+            }
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-            m = fmaxf(m, fabsf(x[k][e]));
-    }
+            for (int k = 0; k < BATCH; k++) {
+                rotate_row<BF16, ROT>(w[k], c, rr, x[k0 + k]);
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    m = fmaxf(m, fabsf(x[k0 + k][e]));
+            }
+        }
+    });
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1)
         m = fmaxf(m, __shfl_xor(m, o, 64));
