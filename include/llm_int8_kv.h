@@ -159,14 +159,16 @@ li8_status int8_kv_attention(const void *Q, int64_t q_stride, li8_dtype dtype, i
  * How int8_kv_attention runs a batch of this shape (introspection; nothing
  * is enqueued, no pointer is looked at):
  *   *path    LI8_KV_EMPTY   no rows, nothing is launched
- *            LI8_KV_FEW     16 query columns (tokens x heads of a group) per
- *                           workgroup, the keys split over workgroups
- *            LI8_KV_TILED   many query columns per workgroup
- *   *splits  the most parts a sequence is split into (1: one launch)
+ *            LI8_KV_FEW     16 or 32 query columns (tokens x heads of a
+ *                           group) per workgroup
+ *            LI8_KV_TILED   256 query columns per workgroup
+ *   *splits  the most parts that a row's keys are split into (1: one launch,
+ *            else a second one merges the parts)
  */
 enum { LI8_KV_EMPTY = 0, LI8_KV_FEW = 1, LI8_KV_TILED = 2 };
 li8_status int8_kv_attention_plan(const li8_kv_batch *batch, const li8_kv_cache *cache,
-                                  int32_t q_heads, int32_t window, int32_t *path, int32_t *splits);
+                                  int32_t q_heads, int32_t causal, int32_t window, int32_t *path,
+                                  int32_t *splits);
 
 #ifdef __cplusplus
 }

@@ -140,7 +140,7 @@ def load_library() -> ctypes.CDLL:
     L.int8_kv_attention_workspace_bytes.restype = sz
     L.int8_kv_attention_workspace_bytes.argtypes = [vp, vp, i32]
     L.int8_kv_attention_plan.restype = ctypes.c_int
-    L.int8_kv_attention_plan.argtypes = [vp, vp, i32, i32, vp, vp]
+    L.int8_kv_attention_plan.argtypes = [vp, vp, i32, i32, i32, vp, vp]
     L.int8_kv_attention.restype = ctypes.c_int
     L.int8_kv_attention.argtypes = [vp, i64, ctypes.c_int, i32, ctypes.c_float, vp, i32, i32, vp, vp,
                                     vp, i64, vp, vp, sz, vp]
@@ -810,12 +810,13 @@ def new_kv_attention_workspace(batch: KVBatch, cache: KVCache, q_heads: int) -> 
 KV_PATHS = {0: "empty", 1: "few", 2: "tiled"}
 
 
-def kv_attention_plan(batch: KVBatch, cache: KVCache, q_heads: int, window: int = 0) -> dict:
+def kv_attention_plan(batch: KVBatch, cache: KVCache, q_heads: int, causal: bool = True,
+                      window: int = 0) -> dict:
     """How ``kv_attention`` runs a batch of this shape: path, and the most
-    parts that a sequence's keys are split into."""
+    parts that a row's keys are split into."""
     path, splits = ctypes.c_int32(), ctypes.c_int32()
     _check("int8_kv_attention_plan",
-           load_library().int8_kv_attention_plan(batch._ref, cache._ref, q_heads, window,
+           load_library().int8_kv_attention_plan(batch._ref, cache._ref, q_heads, int(bool(causal)), window,
                                                  ctypes.byref(path), ctypes.byref(splits)))
     return dict(path=KV_PATHS[path.value], splits=splits.value)
 

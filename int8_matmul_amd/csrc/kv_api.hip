@@ -89,16 +89,17 @@ li8_status check_rope(const li8_rope *r, const li8_kv_batch *b, const li8_kv_cac
 bool bad_dtype(li8_dtype d) { return d != LI8_F16 && d != LI8_BF16; }
 
 // Query heads and the grid of the attention.
-li8_status check_heads(const li8_kv_batch *b, const li8_kv_cache *c, int32_t q_heads, int32_t window)
+li8_status check_heads(const li8_kv_batch *b, const li8_kv_cache *c, int32_t q_heads, int32_t causal,
+                       int32_t window)
 {
     if (q_heads < 1 || q_heads > (1 << 20) || q_heads % c->heads != 0)
         return LI8_ERR_SHAPE;
-    if (window < 0)
+    if (window < 0 || (causal != 0 && causal != 1))
         return LI8_ERR_INVALID_ARG;
     const int64_t rows = std::min(b->max_q, b->tokens), group = q_heads / c->heads;
     if (rows * group > kMaxGrid)
         return LI8_ERR_SHAPE;
-    const KvPlan p = kv_plan(*b, *c, q_heads, window);
+    const KvPlan p = kv_plan(*b, *c, q_heads, causal != 0, window);
     if (((double)b->seqs * c->heads + 8) * p.blocks * std::max(p.splits, p.used) > (double)kMaxGrid)
         return LI8_ERR_SHAPE;
     return LI8_OK;
@@ -158,19 +159,20 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
 size_t int8_kv_attention_workspace_bytes(const li8_kv_batch *batch, const li8_kv_cache *cache,
                                          int32_t q_heads)
 {
-    if (check_sizes(batch, cache) != LI8_OK || check_heads(batch, cache, q_heads, 0) != LI8_OK)
+    if (check_sizes(batch, cache) != LI8_OK || check_heads(batch, cache, q_heads, 1, 0) != LI8_OK)
         return 0;
     return kv_workspace(*batch, *cache, q_heads);
 }
 
 li8_status int8_kv_attention_plan(const li8_kv_batch *batch, const li8_kv_cache *cache,
-                                  int32_t q_heads, int32_t window, int32_t *path, int32_t *splits)
+                                  int32_t q_heads, int32_t causal, int32_t window, int32_t *path,
+                                  int32_t *splits)
 {
     LI8_TRY(check_sizes(batch, cache));
-    LI8_TRY(check_heads(batch, cache, q_heads, window));
+    LI8_TRY(check_heads(batch, cache, q_heads, causal, window));
     if (!path || !splits)
         return LI8_ERR_INVALID_ARG;
-    const KvPlan p = kv_plan(*batch, *cache, q_heads, window);
+    const KvPlan p = kv_plan(*batch, *cache, q_heads, causal != 0, window);
     *path = p.path;
     *splits = p.splits;
     return LI8_OK;
@@ -183,8 +185,8 @@ li8_status int8_kv_attention(const void *Q, int64_t q_stride, li8_dtype dtype, i
                              size_t workspace_bytes, hipStream_t stream)
 {
     LI8_TRY(check_sizes(batch, cache));
-    LI8_TRY(check_heads(batch, cache, q_heads, window));
-    if (bad_dtype(dtype) || !isfinite(scale) || scale < 0.0f || (causal != 0 && causal != 1))
+    LI8_TRY(check_heads(batch, cache, q_heads, causal, window));
+    if (bad_dtype(dtype) || !isfinite(scale) || scale < 0.0f)
         return LI8_ERR_INVALID_ARG;
     KvRope r;
     LI8_TRY(check_rope(rope, batch, cache, &r));

@@ -34,7 +34,7 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr float kNone = -1.0e30f;      // a running maximum over nothing yet
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kQMax = 16256.0f;      // 127 * 128: the largest 15-bit query integer
-constexpr int kFewWaves = 4;
+constexpr int kFewLeast = 8;           // fewest steps of a workgroup that shares
 
 struct AttnArgs {
     KvTokens Q;
@@ -42,10 +42,13 @@ struct AttnArgs {
     uint16_t *O;
     int64_t os;
     float *lse;
-    float *part_o, *part_m;            // [item][split][used][D], [item][split][used]
+    // partial results: tiled [item][split][used][D] and [item][split][used],
+    // few columns [2 part + k][used][D], k = 0 for the run's first block
+    float *part_o, *part_m;
     float scale, inv_group;            // scale * log2(e), 1 / group
     int group, causal, window;
     int cols, blocks, used, splits, chunk;
+    int seqs, parts;                   // parts: workgroups that share the steps, 0: one per block
 };
 
 // Where a workgroup's columns lie.  Column c of a (sequence, head) is row
@@ -67,14 +70,13 @@ struct Block {
     }
 };
 
-__device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int item, int cols, Block &b)
+// Block cb of sequence s and head h; false where it has no column.
+__device__ __forceinline__ bool place(const AttnArgs &t, const KvSeq &q, int s, int h, int cb, int cols, Block &b)
 {
-    const int cb = item % t.blocks;
-    const int sh = item / t.blocks;
-    b.h = sh % a.heads;
-    b.s = sh / a.heads;
-    b.q = kv_sequence_of(a, b.s);
-    const int64_t ncol = (int64_t)b.q.n * t.group;
+    b.s = s;
+    b.h = h;
+    b.q = q;
+    const int64_t ncol = (int64_t)q.n * t.group;
     if ((int64_t)cb * cols >= ncol)
         return false;
     b.c0 = cb * cols;
@@ -82,9 +84,83 @@ __device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int i
     b.i0 = b.c0 / t.group;
     b.g0 = b.c0 - b.i0 * t.group;
     int g;
-    b.span = kv_span(b.q.begin + b.i0, b.q.begin + b.row_of(b.nc - 1, t, g), b.q.len, t.causal != 0, t.window);
+    b.span = kv_span(q.begin + b.i0, q.begin + b.row_of(b.nc - 1, t, g), q.len, t.causal != 0, t.window);
     return true;
 }
+
+__device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int item, int cols, Block &b)
+{
+    const int cb = item % t.blocks, sh = item / t.blocks, s = sh / a.heads;
+    return place(t, kv_sequence_of(a, s), s, sh % a.heads, cb, cols, b);
+}
+
+// The work of the few-column kernel in steps of 32 keys, one sequence after
+// another, and within it head after head and block after block, each with
+// the sequence's largest number of steps (at least one, so that an empty row
+// is written).  `parts` workgroups take equal runs of steps, whatever the
+// lengths are: a grid over sequences alone leaves most of the chip to the
+// longest one.  Every workgroup, of the merging kernel too, counts the steps
+// itself, a lane for each of 64 sequences at a time.  (All counts are below
+// 2^31: the host shares no more than that.)
+struct Steps {
+    KvSeq q;                           // this lane's sequence
+    int steps, blocks;                 // steps of each of its blocks
+    int all, upto;                     // its steps, and those of the lanes up to it
+    int chunk, base;                   // 64 sequences from 64 chunk on, steps before them
+
+    __device__ __forceinline__ void look(const KvArgs &a, const AttnArgs &t, int c, int lane)
+    {
+        chunk = c;
+        const int s = min(64 * c + lane, t.seqs - 1);
+        q = kv_sequence_of(a, s);
+        blocks = (int)(((int64_t)q.n * t.group + t.cols - 1) / t.cols);
+        int span = q.len;
+        if (t.window > 0)
+            span = (int)min((int64_t)span, (int64_t)t.window + (t.causal ? t.cols : q.n) + 31);
+        steps = max(1, (span + 31) >> 5);
+        all = 64 * c + lane < t.seqs ? a.heads * blocks * steps : 0;
+        upto = all;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(upto, d, 64);
+            upto += lane >= d ? y : 0;
+        }
+    }
+
+    // Steps of a workgroup, and of all; chunk 0 is looked at afterwards.
+    __device__ __forceinline__ int share(const KvArgs &a, const AttnArgs &t, int lane, int &total)
+    {
+        total = 0;
+        for (int c = (t.seqs - 1) >> 6; c >= 0; c--) {
+            look(a, t, c, lane);
+            total += __builtin_amdgcn_readlane(upto, 63);
+        }
+        base = 0;
+        return max(kFewLeast, (total + t.parts - 1) / t.parts);
+    }
+
+    // The lane whose sequence has step `at` (at < total, not before `base`).
+    __device__ __forceinline__ int find(const KvArgs &a, const AttnArgs &t, int at, int lane)
+    {
+        while (true) {
+            const uint64_t over = __ballot(base + upto > at);
+            if (over)
+                return __ffsll((unsigned long long)over) - 1;
+            base += __builtin_amdgcn_readlane(upto, 63);
+            look(a, t, chunk + 1, lane);
+        }
+    }
+
+    __device__ __forceinline__ KvSeq seq_of(int k) const
+    {
+        KvSeq r;
+        r.q0 = __builtin_amdgcn_readlane(q.q0, k);
+        r.n = __builtin_amdgcn_readlane(q.n, k);
+        r.len = __builtin_amdgcn_readlane(q.len, k);
+        r.begin = __builtin_amdgcn_readlane(q.begin, k);
+        return r;
+    }
+};
 
 __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
@@ -123,10 +199,11 @@ __device__ __forceinline__ void split_query(const float x[8], uint2 &hi, uint2 &
 }
 
 // The block's query columns into LDS, COLS rows of LQ bytes with the first
-// parts and as many with the second, and their factors.
-template <int D, bool BF16, int COLS, int NT, int LQ>
+// parts and as many with the second, and their factors.  between() runs once
+// the first rows have been requested.
+template <int D, bool BF16, int COLS, int NT, int LQ, class Between>
 __device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t, const Block &b, char *lds,
-                                              float *factor)
+                                              float *factor, Between between)
 {
     constexpr int CPR = D / 8, PASSES = COLS * CPR / NT > 0 ? COLS * CPR / NT : 1;
     constexpr int BATCH = PASSES < 4 ? PASSES : 4;   // rows of a thread in flight
@@ -144,6 +221,8 @@ __device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t
                 fetch_row<ROT>(w[k], t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D,
                                cc, t.rope, max(b.q.begin + i, 0));
             }
+            if (k0 == 0)
+                between();
 #pragma unroll
             for (int k = 0; k < BATCH; k++) {
                 const int qc = threadIdx.x / CPR + (k0 + k) * (NT / CPR);
@@ -181,143 +260,167 @@ struct Step {
     bool ok[2];
 };
 
+// Read-only data at addresses that are the same for a whole wave: scalar loads.
+typedef const int32_t __attribute__((address_space(4))) *kv_const_i32;
+typedef const float __attribute__((address_space(4))) *kv_const_f32;
+
 template <int D>
-__device__ __forceinline__ void load_step(Step<D> &st, const KvArgs &a, const int32_t *table, int h,
-                                          int t0, int lo, int te, int lane)
+__device__ __forceinline__ void load_step(Step<D> &st, const KvArgs &a, const int (&pid)[2], int h, int t0,
+                                          int lo, int te, uint32_t koff, uint32_t voff)
 {
-    const int r = lane & 15, g = lane >> 4, page = 1 << a.page_shift;
+    const int page = 1 << a.page_shift;
 #pragma unroll
     for (int tt = 0; tt < 2; tt++) {
         const int t = t0 + 16 * tt;
-        const int pid = table[min(t >> a.page_shift, a.table_width - 1)];
         // a tile past the end, before the first key seen or in no page is
         // masked; page 0 is read in its place
-        st.ok[tt] = (unsigned)pid < (unsigned)a.pages && t < te && t + 16 > lo;
-        const int64_t ph = (int64_t)(st.ok[tt] ? pid : 0) * a.heads + h;
+        st.ok[tt] = (unsigned)pid[tt] < (unsigned)a.pages && t < te && t + 16 > lo;
+        const int64_t ph = (int64_t)(st.ok[tt] ? pid[tt] : 0) * a.heads + h;
         const int64_t base = ((ph * D) << a.page_shift) + (t & (page - 1)) * D;
-        const int8_t *kp = a.k + base;
-        const int8_t *vp = a.v + base;
+        const int8_t *kp = a.k + base + koff;
+        const int8_t *vp = a.v + base + voff;
 #pragma unroll
         for (int ks = 0; ks < D / 64; ks++)
-            st.k[tt][ks] = *reinterpret_cast<const v4i *>(kp + r * D + 64 * ks + 16 * g);
+            st.k[tt][ks] = *reinterpret_cast<const v4i *>(kp + 64 * ks);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const int8_t *p = vp + (4 * g + j) * D + r * (D / 16);
             if constexpr (D == 128)
-                *reinterpret_cast<uint2 *>(st.v[4 * tt + j]) = *reinterpret_cast<const uint2 *>(p);
+                *reinterpret_cast<uint2 *>(st.v[4 * tt + j]) = *reinterpret_cast<const uint2 *>(vp + j * D);
             else
-                st.v[4 * tt + j][0] = *reinterpret_cast<const uint32_t *>(p);
+                st.v[4 * tt + j][0] = *reinterpret_cast<const uint32_t *>(vp + j * D);
         }
-        const float ksc = a.ks[ph], vsc = a.vs[ph];
+        const float ksc = ((kv_const_f32)(uintptr_t)a.ks)[ph], vsc = ((kv_const_f32)(uintptr_t)a.vs)[ph];
         st.ks[tt] = st.ok[tt] ? ksc : 0.0f;
         st.vs[tt] = st.ok[tt] ? vsc : 0.0f;
     }
 }
 
 // ---------------------------------------------------------------------------
-// Few columns: 16 columns of one (sequence, head) and one split of its keys
-// per workgroup; the 4 waves take the steps of 32 keys in turn and keep their
-// own maximum, sum and O^T, merged through LDS at the end.
+// Few columns: 16 NC columns of one (sequence, head) and one split of its
+// keys per workgroup; the 4 waves take the steps of 32 keys in turn and keep
+// their own maximum, sum and O^T, merged through LDS at the end.  K and V go
+// from memory into the MFMA operands' registers, V through a byte transpose
+// (4 keys x 4 dims by v_perm), and a step is requested while the one before
+// is computed: the kernel is bound by reading the cache once.
 // ---------------------------------------------------------------------------
-template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kFewWaves) void k_kv_few(KvArgs a, AttnArgs t)
+template <int D, bool BF16, int NC, int NW>
+__device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, const Block &b, int ts, int te,
+                                          int64_t slot, char *smem, float *s_f, float *s_m, float *s_l)
 {
-    constexpr int CPR = D / 8, NB = D / 16, KS = D / 64, LQ = D + 16, LO = D + 4;
-    __shared__ __align__(16) char smem[kFewWaves * kKvCols * LO * 4];
-    __shared__ float s_f[kKvCols], s_m[kFewWaves][kKvCols], s_l[kFewWaves][kKvCols];
+    constexpr int CPR = D / 8, NB = D / 16, KS = D / 64, LQ = D + 16, LO = D + 4, COLS = kKvCols * NC;
+    constexpr int kStride = 32 * NW;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int sp = blockIdx.x % t.splits, item = blockIdx.x / t.splits;
-    Block b;
-    if (!locate(a, t, item, kKvCols, b))
-        return;
-    const int ts = b.span.base + sp * t.chunk;
-    const int te = min(b.span.hi, ts + t.chunk);
-    if (ts >= te && t.splits > 1)
-        return;                        // (the merging kernel knows how many there are)
-    const int qc = tid / CPR, cc = tid % CPR;   // column and chunk of the query and output phases
-
-    split_queries<D, BF16, kKvCols, 64 * kFewWaves, LQ>(a, t, b, smem, s_f);
-    __syncthreads();
+    const kv_const_i32 table = (kv_const_i32)(uintptr_t)(a.table + (int64_t)b.s * a.table_stride);
     const int col = lane & 15, g = lane >> 4;
-    v4i qh[KS], ql[KS];
+    const uint32_t koff = col * D + 16 * g, voff = 4 * g * D + col * (D / 16);
+    auto pages = [&](int (&pid)[2], int t0) {
+        pid[0] = table[min(t0 >> a.page_shift, a.table_width - 1)];
+        pid[1] = table[min((t0 + 16) >> a.page_shift, a.table_width - 1)];
+    };
+    int t0 = ts + 32 * wid, pid[2];
+    Step<D> st[2];
+    const bool any = t0 < te;
+    // the queries and the first step's data are requested together
+    if (any)
+        pages(pid, t0);
+    split_queries<D, BF16, COLS, 64 * NW, LQ>(a, t, b, smem, s_f, [&]() {
+        if (any) {
+            load_step<D>(st[0], a, pid, b.h, t0, b.span.lo, te, koff, voff);
+            pages(pid, t0 + kStride);
+        }
+    });
+    __syncthreads();
+    v4i qh[NC][KS], ql[NC][KS];
+    float f[NC];
+    int chi[NC], clo[NC];              // keys this lane's columns see: [clo, chi)
 #pragma unroll
-    for (int ks = 0; ks < KS; ks++) {
-        qh[ks] = *reinterpret_cast<const v4i *>(smem + col * LQ + 64 * ks + 16 * g);
-        ql[ks] = *reinterpret_cast<const v4i *>(smem + (kKvCols + col) * LQ + 64 * ks + 16 * g);
+    for (int c = 0; c < NC; c++) {
+        const int qc = kKvCols * c + col;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++) {
+            qh[c][ks] = *reinterpret_cast<const v4i *>(smem + qc * LQ + 64 * ks + 16 * g);
+            ql[c][ks] = *reinterpret_cast<const v4i *>(smem + (COLS + qc) * LQ + 64 * ks + 16 * g);
+        }
+        f[c] = s_f[qc];
+        int gcol;
+        const int pos = b.q.begin + b.row_of(qc, t, gcol);
+        chi[c] = qc >= b.nc ? 0 : t.causal ? min(te, pos + 1) : te;
+        clo[c] = t.window > 0 ? max((int64_t)0, (int64_t)pos + 1 - t.window) : 0;
     }
-    const float f = s_f[col];
     __syncthreads();                   // smem is used again below
 
-    // keys this lane's column sees: [clo, chi)
-    int gcol;
-    const int pos = b.q.begin + b.row_of(col, t, gcol);
-    int chi = t.causal ? min(te, pos + 1) : te;
-    const int clo = t.window > 0 ? max((int64_t)0, (int64_t)pos + 1 - t.window) : 0;
-    if (col >= b.nc)
-        chi = 0;
-    const int32_t *table = a.table + (int64_t)b.s * a.table_stride;
-
-    v4f acc[NB] = {};
-    float m = kNone, l = 0.0f, vref = 0.0f;
-    for (int t0 = ts + 32 * wid; t0 < te; t0 += 32 * kFewWaves) {
-        Step<D> st;
-        load_step<D>(st, a, table, b.h, t0, b.span.lo, te, lane);
-        float z[8], zm = -INFINITY;
+    v4f acc[NC][NB] = {};
+    float m[NC], l[NC], vref = 0.0f;
 #pragma unroll
-        for (int tt = 0; tt < 2; tt++) {
-            v4i sh = {0, 0, 0, 0}, sl = {0, 0, 0, 0};
-#pragma unroll
-            for (int ks = 0; ks < KS; ks++) {
-                sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(st.k[tt][ks], qh[ks], sh, 0, 0, 0);
-                sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(st.k[tt][ks], ql[ks], sl, 0, 0, 0);
-            }
-            const float fk = f * st.ks[tt];
-            const int key = t0 + 16 * tt + 4 * g, hi = st.ok[tt] ? chi : 0;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float v = (float)((sh[i] << 7) + sl[i]) * fk;
-                z[4 * tt + i] = key + i < hi && key + i >= clo ? v : -INFINITY;
-                zm = fmaxf(zm, z[4 * tt + i]);
-            }
-        }
-        // The maximum is moved only when some score is 8 above it (in powers
-        // of two): until then the probabilities stay below 2^8, and neither
-        // O^T nor the sum has to be scaled.
-        if (__any(zm > m + 8.0f)) {
-            zm = fmaxf(zm, __shfl_xor(zm, 16, 64));
-            zm = fmaxf(zm, __shfl_xor(zm, 32, 64));
-            const float mn = fmaxf(m, zm), al = exp2f(m - mn);
-#pragma unroll
-            for (int n = 0; n < NB; n++)
-                acc[n] *= al;
-            l *= al;
-            m = mn;
-        }
-        // Value scales relative to the largest so far, so that the operand
-        // stays in fp16's range whatever the scales are.
-        const float vm = fmaxf(st.vs[0], st.vs[1]);
+    for (int c = 0; c < NC; c++) {
+        m[c] = kNone;
+        l[c] = 0.0f;
+    }
+    auto compute = [&](const Step<D> &w, int t0) {
+        // value scales relative to the largest so far, so that the operand
+        // stays in fp16's range whatever the scales are
+        const float vm = fmaxf(w.vs[0], w.vs[1]);
         if (vm > vref) {
             const float al = vref / vm;
 #pragma unroll
-            for (int n = 0; n < NB; n++)
-                acc[n] *= al;
+            for (int c = 0; c < NC; c++)
+#pragma unroll
+                for (int n = 0; n < NB; n++)
+                    acc[c][n] *= al;
             vref = vm;
         }
-        const float vi = vref > 0.0f ? 1.0f / vref : 0.0f;
-        v8h p;
+        const float vi = vref > 0.0f ? __builtin_amdgcn_rcpf(vref) : 0.0f;
+        const float r[2] = {w.vs[0] * vi, w.vs[1] * vi};
+        v8h p[NC];
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const float pe = exp2f(z[e] - m);
-            l += pe;
-            p[e] = (_Float16)(pe * (st.vs[e >> 2] * vi));
+        for (int c = 0; c < NC; c++) {
+            float z[8], zm = -INFINITY;
+#pragma unroll
+            for (int tt = 0; tt < 2; tt++) {
+                v4i sh = {0, 0, 0, 0}, sl = {0, 0, 0, 0};
+#pragma unroll
+                for (int ks = 0; ks < KS; ks++) {
+                    sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(w.k[tt][ks], qh[c][ks], sh, 0, 0, 0);
+                    sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(w.k[tt][ks], ql[c][ks], sl, 0, 0, 0);
+                }
+                const float fk = f[c] * w.ks[tt];
+                const int key = t0 + 16 * tt + 4 * g, hi = w.ok[tt] ? chi[c] : 0;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float v = (float)((sh[i] << 7) + sl[i]) * fk;
+                    z[4 * tt + i] = key + i < hi && key + i >= clo[c] ? v : -INFINITY;
+                    zm = fmaxf(zm, z[4 * tt + i]);
+                }
+            }
+            // The maximum is moved only when some score is 8 above it (in
+            // powers of two): until then the probabilities stay below 2^8,
+            // and neither O^T nor the sum has to be scaled.
+            if (__any(zm > m[c] + 8.0f)) {
+                zm = fmaxf(zm, __shfl_xor(zm, 16, 64));
+                zm = fmaxf(zm, __shfl_xor(zm, 32, 64));
+                const float mn = fmaxf(m[c], zm), al = __builtin_amdgcn_exp2f(m[c] - mn);
+#pragma unroll
+                for (int n = 0; n < NB; n++)
+                    acc[c][n] *= al;
+                l[c] *= al;
+                m[c] = mn;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float pe = __builtin_amdgcn_exp2f(z[e] - m[c]);
+                l[c] += pe;
+                p[c][e] = (_Float16)(pe * r[e >> 2]);
+            }
         }
+        // Lane (col, g) has the bytes col NB .. col NB + NB - 1 of its 8 keys:
+        // operand n is dim col NB + n of all of them.
 #pragma unroll
-        for (int w = 0; w < KS; w++) {
+        for (int d = 0; d < KS; d++) {
             uint32_t u[8];
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                u[j] = st.v[j][w] ^ 0x80808080u;
+                u[j] = w.v[j][d] ^ 0x80808080u;
             v4u x0, x1, x2, x3;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -326,64 +429,129 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_kv_few(KvArgs a, AttnArgs t)
                 x2[j] = codes_f16<2>(u[2 * j], u[2 * j + 1]);
                 x3[j] = codes_f16<3>(u[2 * j], u[2 * j + 1]);
             }
-            acc[4 * w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x0), p, acc[4 * w], 0, 0, 0);
-            acc[4 * w + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x1), p, acc[4 * w + 1], 0, 0, 0);
-            acc[4 * w + 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x2), p, acc[4 * w + 2], 0, 0, 0);
-            acc[4 * w + 3] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x3), p, acc[4 * w + 3], 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < NC; c++) {
+                acc[c][4 * d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x0), p[c], acc[c][4 * d], 0, 0, 0);
+                acc[c][4 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x1), p[c], acc[c][4 * d + 1], 0, 0, 0);
+                acc[c][4 * d + 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x2), p[c], acc[c][4 * d + 2], 0, 0, 0);
+                acc[c][4 * d + 3] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x3), p[c], acc[c][4 * d + 3], 0, 0, 0);
+            }
+        }
+    };
+    // (a step past the end is requested all the same, masked, from page 0)
+    if (any) {
+        while (true) {
+            load_step<D>(st[1], a, pid, b.h, t0 + kStride, b.span.lo, te, koff, voff);
+            pages(pid, t0 + 2 * kStride);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(st[0], t0);
+            t0 += kStride;
+            if (t0 >= te)
+                break;
+            load_step<D>(st[0], a, pid, b.h, t0 + kStride, b.span.lo, te, koff, voff);
+            pages(pid, t0 + 2 * kStride);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(st[1], t0);
+            t0 += kStride;
+            if (t0 >= te)
+                break;
         }
     }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
 
     // Accumulator n of lane (col, g) holds O^T[(4g + i) NB + n][col], i < 4.
-    float *so = reinterpret_cast<float *>(smem) + (wid * kKvCols + col) * LO;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int c = 0; c < NC; c++) {
+        l[c] += __shfl_xor(l[c], 16, 64);
+        l[c] += __shfl_xor(l[c], 32, 64);
+        float *so = reinterpret_cast<float *>(smem) + (wid * COLS + kKvCols * c + col) * LO;
 #pragma unroll
-        for (int n = 0; n < NB; n += 4) {
-            const v4f o = {acc[n][i] * vref, acc[n + 1][i] * vref, acc[n + 2][i] * vref, acc[n + 3][i] * vref};
-            *reinterpret_cast<v4f *>(so + (4 * g + i) * NB + n) = o;
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int n = 0; n < NB; n += 4) {
+                const v4f o = {acc[c][n][i] * vref, acc[c][n + 1][i] * vref, acc[c][n + 2][i] * vref,
+                               acc[c][n + 3][i] * vref};
+                *reinterpret_cast<v4f *>(so + (4 * g + i) * NB + n) = o;
+            }
+        if (g == 0) {
+            s_m[wid * COLS + kKvCols * c + col] = m[c];
+            s_l[wid * COLS + kKvCols * c + col] = l[c];
         }
-    if (g == 0) {
-        s_m[wid][col] = m;
-        s_l[wid][col] = l;
     }
     __syncthreads();
-    if (qc >= b.nc)
-        return;
-    float M = kNone, L = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int qc = tid / CPR; qc < b.nc; qc += 64 * NW / CPR) {
+        const int cc = tid % CPR;
+        float M = kNone, L = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kFewWaves; w++)
-        M = fmaxf(M, s_m[w][qc]);
+        for (int w = 0; w < NW; w++)
+            M = fmaxf(M, s_m[w * COLS + qc]);
 #pragma unroll
-    for (int w = 0; w < kFewWaves; w++) {
-        const float al = exp2f(s_m[w][qc] - M);
-        const float *src = reinterpret_cast<const float *>(smem) + (w * kKvCols + qc) * LO + 8 * cc;
-        L += s_l[w][qc] * al;
+        for (int w = 0; w < NW; w++) {
+            const float al = __builtin_amdgcn_exp2f(s_m[w * COLS + qc] - M);
+            const float *src = reinterpret_cast<const float *>(smem) + (w * COLS + qc) * LO + 8 * cc;
+            L += s_l[w * COLS + qc] * al;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                o[e] += src[e] * al;
+        }
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; e++)
-            o[e] += src[e] * al;
+            o[e] *= inv;
+        if (slot >= 0) {
+            const int64_t at = slot * t.used + qc;
+            float *po = t.part_o + at * D + 8 * cc;
+            *reinterpret_cast<float4 *>(po) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4 *>(po + 4) = make_float4(o[4], o[5], o[6], o[7]);
+            if (cc == 0)
+                t.part_m[at] = L > 0.0f ? M + log2f(L) : kNone;
+            continue;
+        }
+        int gq;
+        const int i = b.row_of(qc, t, gq);
+        const int64_t row = b.q.q0 + i;
+        const int head = b.h * t.group + gq;
+        *reinterpret_cast<uint4 *>(t.O + row * t.os + (int64_t)head * D + 8 * cc) = pack8<BF16>(o);
+        if (t.lse && cc == 0)
+            t.lse[row * (int64_t)(a.heads * t.group) + head] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; e++)
-        o[e] *= inv;
-    if (t.splits > 1) {
-        const int64_t at = ((int64_t)blockIdx.x) * t.used + qc;
-        float *po = t.part_o + at * D + 8 * cc;
-        *reinterpret_cast<float4 *>(po) = make_float4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<float4 *>(po + 4) = make_float4(o[4], o[5], o[6], o[7]);
-        if (cc == 0)
-            t.part_m[at] = L > 0.0f ? M + log2f(L) : kNone;
+}
+
+template <int D, bool BF16, int NC, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
+{
+    constexpr int COLS = kKvCols * NC;
+    __shared__ __align__(16) char smem[NW * COLS * (D + 4) * 4];
+    __shared__ float s_f[COLS], s_m[NW * COLS], s_l[NW * COLS];
+    Block b;
+    if (t.parts == 0) {
+        if (locate(a, t, blockIdx.x, COLS, b))
+            few_block<D, BF16, NC, NW>(a, t, b, b.span.base, b.span.hi, -1, smem, s_f, s_m, s_l);
         return;
     }
-    int gq;
-    const int i = b.row_of(qc, t, gq);
-    const int64_t row = b.q.q0 + i;
-    const int head = b.h * t.group + gq;
-    *reinterpret_cast<uint4 *>(t.O + row * t.os + (int64_t)head * D + 8 * cc) = pack8<BF16>(o);
-    if (t.lse && cc == 0)
-        t.lse[row * (int64_t)(a.heads * t.group) + head] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    const int lane = threadIdx.x & 63;
+    Steps w;
+    int total;
+    const int per = __builtin_amdgcn_readfirstlane(w.share(a, t, lane, total));
+    const int64_t begin64 = (int64_t)blockIdx.x * per;
+    if (begin64 >= total)
+        return;
+    const int begin = (int)begin64, end = (int)min(begin64 + per, (int64_t)total);
+    for (int at = begin; at < end;) {
+        const int k = __builtin_amdgcn_readfirstlane(w.find(a, t, at, lane));
+        const int steps = __builtin_amdgcn_readlane(w.steps, k), blocks = __builtin_amdgcn_readlane(w.blocks, k);
+        const int r = at - w.base - __builtin_amdgcn_readlane(w.upto - w.all, k);
+        const int unit = r / steps, first = r - unit * steps, h = unit / blocks, cb = unit - h * blocks;
+        const int count = min(steps - first, end - at);
+        // a run's first block goes to the run's slot 0, a later one that it
+        // does not finish to slot 1, and one that is all its own to O
+        const int64_t slot = count == steps ? -1 : 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
+        if (place(t, w.seq_of(k), 64 * w.chunk + k, h, cb, COLS, b)) {
+            const int ts = b.span.base + 32 * first;
+            few_block<D, BF16, NC, NW>(a, t, b, ts, min(b.span.hi, ts + 32 * count), slot, smem, s_f, s_m, s_l);
+        }
+        at += count;
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -455,7 +623,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
     if (ts >= te && t.splits > 1)
         return;
 
-    split_queries<D, BF16, kTileCols, NT, L::q_row>(a, t, b, smem, s_f);
+    split_queries<D, BF16, kTileCols, NT, L::q_row>(a, t, b, smem, s_f, []() {});
     __syncthreads();
     const int col = lane & 31, half = lane >> 5, qcol = 32 * wid + col;
     v4i qh[KS], ql[KS];
@@ -817,57 +985,113 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
         t.lse[row * (int64_t)(a.heads * t.group) + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// Merges the splits of one column: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M),
-// m_i the split's log2 of its sum.  256 threads: D/8 chunks x split lanes.
-template <int D, bool BF16>
-__global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t)
+// Merges the partial results of a column: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M),
+// m_i the part's log2 of its sum.  SL lanes of parts x D/8 chunks per column,
+// 256 / (SL D/8) columns per workgroup; four parts are in flight per lane.
+template <int D, bool BF16, int SL>
+__global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int columns)
 {
-    constexpr int CPR = D / 8, SL = 256 / CPR;
-    __shared__ float s_o[SL][D + 4], s_m[SL], s_l[SL];
-    const int tid = threadIdx.x, cc = tid % CPR, sl = tid / CPR;
-    const int qc = blockIdx.x % t.used, item = blockIdx.x / t.used;
+    constexpr int CPR = D / 8, WIDTH = SL * CPR;
+    static_assert(WIDTH == 64 || WIDTH == 256, "a wave has one column");
+    const int cc = threadIdx.x % CPR, sl = threadIdx.x % WIDTH / CPR;
+    const int at_col = blockIdx.x * (256 / WIDTH) + threadIdx.x / WIDTH;
+    const int qc = at_col % t.used, item = min(at_col, columns - 1) / t.used;
     Block b;
-    if (!locate(a, t, item, t.cols, b) || qc >= b.nc)
-        return;
-    const int na = b.span.hi > b.span.lo ? (b.span.hi - b.span.base + t.chunk - 1) / t.chunk : 0;
+    bool mine = locate(a, t, item, t.cols, b) && qc < b.nc && at_col < columns;
+    // part i of the column is at slot first + i * step
+    int64_t first = 0;
+    int na = 0, step = 1;
+    if (t.parts == 0) {
+        first = (int64_t)item * t.splits;
+        na = mine && b.span.hi > b.span.lo ? min((b.span.hi - b.span.base + t.chunk - 1) / t.chunk, t.splits) : 0;
+    } else {
+        // (a wave's columns are of one sequence)
+        const int lane = threadIdx.x & 63;
+        const int cb = item % t.blocks, sh = item / t.blocks, s = sh / a.heads, h = sh % a.heads;
+        Steps w;
+        int total, before = 0;
+        const int per = w.share(a, t, lane, total);
+        for (int c = 0; c < (s >> 6); c++) {
+            before += __shfl(w.upto, 63, 64);
+            w.look(a, t, c + 1, lane);
+        }
+        const int k = s & 63, steps = __shfl(w.steps, k, 64), blocks = __shfl(w.blocks, k, 64);
+        const int u0 = before + __shfl(w.upto - w.all, k, 64) + (h * blocks + cb) * steps, u1 = u0 + steps - 1;
+        const int p0 = u0 / per, p1 = u1 / per;
+        mine = mine && p1 > p0;          // (else its workgroup has written it)
+        // the first part is the last block of its run (slot 1) unless the run
+        // begins with it, the others begin theirs (slot 0)
+        first = u0 == p0 * per ? 2 * p0 : 2 * p0 + 1;
+        na = mine ? p1 - p0 + 1 : 0;
+        step = 2;
+    }
+    auto slot = [&](int i) {
+        const int64_t k = first + (int64_t)step * i;
+        return (step == 2 && i > 0 ? k & ~(int64_t)1 : k) * t.used + qc;
+    };
     float m = kNone, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int i = sl; i < min(na, t.splits); i += SL) {
-        const int64_t at = ((int64_t)item * t.splits + i) * t.used + qc;
-        const float e = t.part_m[at];
-        const float4 x0 = *reinterpret_cast<const float4 *>(t.part_o + at * D + 8 * cc);
-        const float4 x1 = *reinterpret_cast<const float4 *>(t.part_o + at * D + 8 * cc + 4);
-        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        const float mn = fmaxf(m, e), al = exp2f(m - mn), be = e > kNone ? exp2f(e - mn) : 0.0f;
-        l = l * al + be;
+    for (int i = sl; i < na; i += 4 * SL) {
+        float e[4], x[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int64_t at = slot(min(i + k * SL, na - 1));
+            e[k] = t.part_m[at];
+            *reinterpret_cast<float4 *>(x[k]) = *reinterpret_cast<const float4 *>(t.part_o + at * D + 8 * cc);
+            *reinterpret_cast<float4 *>(x[k] + 4) = *reinterpret_cast<const float4 *>(t.part_o + at * D + 8 * cc + 4);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float ek = i + k * SL < na ? e[k] : kNone;
+            const float mn = fmaxf(m, ek), al = __builtin_amdgcn_exp2f(m - mn);
+            const float be = ek > kNone ? __builtin_amdgcn_exp2f(ek - mn) : 0.0f;
+            l = l * al + be;
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                o[j] = o[j] * al + x[k][j] * be;
+            m = mn;
+        }
+    }
+    auto join = [&](float m2, float l2, const float (&o2)[8]) {
+        const float mn = fmaxf(m, m2), al = __builtin_amdgcn_exp2f(m - mn), be = __builtin_amdgcn_exp2f(m2 - mn);
+        l = l * al + l2 * be;
 #pragma unroll
         for (int k = 0; k < 8; k++)
-            o[k] = o[k] * al + x[k] * be;
+            o[k] = o[k] * al + o2[k] * be;
         m = mn;
-    }
+    };
 #pragma unroll
-    for (int k = 0; k < 8; k++)
-        s_o[sl][8 * cc + k] = o[k];
-    if (cc == 0) {
-        s_m[sl] = m;
-        s_l[sl] = l;
-    }
-    __syncthreads();
-    if (sl != 0)
-        return;
-    float M = kNone, L = 0.0f;
-    for (int i = 0; i < SL; i++)
-        M = fmaxf(M, s_m[i]);
-#pragma unroll
-    for (int k = 0; k < 8; k++)
-        o[k] = 0.0f;
-    for (int i = 0; i < SL; i++) {
-        const float al = exp2f(s_m[i] - M);
-        L += s_l[i] * al;
+    for (int d = CPR; d < 64; d *= 2) {
+        float o2[8];
 #pragma unroll
         for (int k = 0; k < 8; k++)
-            o[k] += s_o[i][8 * cc + k] * al;
+            o2[k] = __shfl_xor(o[k], d, 64);
+        join(__shfl_xor(m, d, 64), __shfl_xor(l, d, 64), o2);
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    if constexpr (WIDTH > 64) {
+        constexpr int W = WIDTH / 64;
+        __shared__ float s_o[256 / 64][D], s_m[256 / 64], s_l[256 / 64];
+        const int w = threadIdx.x / 64, w0 = w / W * W;
+        if (threadIdx.x % 64 < CPR) {
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                s_o[w][8 * cc + k] = o[k];
+            s_m[w] = m;
+            s_l[w] = l;
+        }
+        __syncthreads();
+        if (w == w0) {
+            for (int i = 1; i < W; i++) {
+                float o2[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    o2[k] = s_o[w0 + i][8 * cc + k];
+                join(s_m[w0 + i], s_l[w0 + i], o2);
+            }
+        }
+    }
+    if (!mine || sl != 0)
+        return;
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; k++)
         o[k] *= inv;
@@ -877,13 +1101,14 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t)
     const int head = b.h * t.group + g;
     *reinterpret_cast<uint4 *>(t.O + row * t.os + (int64_t)head * D + 8 * cc) = pack8<BF16>(o);
     if (t.lse && cc == 0)
-        t.lse[row * (int64_t)(a.heads * t.group) + head] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+        t.lse[row * (int64_t)(a.heads * t.group) + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-constexpr int kFewTarget = 1024;       // workgroups aimed at: 4 for each CU
 constexpr int kTileTarget = 512;
 constexpr int64_t kTileMinSplit = 1024;
 constexpr int kTileFrom = 64;          // columns from which the tiled kernel is taken
+constexpr int kFewWhole = 40;          // steps up to which a block stays whole
+constexpr int kFewSlots = 512;         // workgroups that share steps: 2 for each CU
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
@@ -903,20 +1128,45 @@ hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipSt
         k_kv_tiled<D, BF16><<<(unsigned)(round_up(pairs, lanes) * t.blocks * t.splits), 64 * kTileWaves, 0, s>>>(
             a, t, (int)pairs, lanes, !t.causal || a.max_q < a.max_kv / 2);
     } else {
-        k_kv_few<D, BF16><<<(unsigned)(items * t.splits), 64 * kFewWaves, 0, s>>>(a, t);
+        const bool wide = t.cols != kKvCols;
+        if (t.parts > 0) {
+            const unsigned grid = (unsigned)t.parts;
+            if (wide)
+                k_kv_few<D, BF16, 2, 4><<<grid, 256, 0, s>>>(a, t);
+            else
+                k_kv_few<D, BF16, 1, 4><<<grid, 256, 0, s>>>(a, t);
+        } else if (items <= 512) {
+            if (wide)
+                k_kv_few<D, BF16, 2, 8><<<(unsigned)items, 512, 0, s>>>(a, t);
+            else
+                k_kv_few<D, BF16, 1, 8><<<(unsigned)items, 512, 0, s>>>(a, t);
+        } else {
+            if (wide)
+                k_kv_few<D, BF16, 2, 4><<<(unsigned)items, 256, 0, s>>>(a, t);
+            else
+                k_kv_few<D, BF16, 1, 4><<<(unsigned)items, 256, 0, s>>>(a, t);
+        }
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || t.splits == 1)
+    if (e != hipSuccess || (t.splits == 1 && t.parts == 0))
         return e;
-    k_kv_merge<D, BF16><<<(unsigned)(items * t.used), 256, 0, s>>>(a, t);
+    const int64_t columns = items * t.used;
+    // lanes for the parts of a column: about as many parts as it can have
+    const int64_t parts = t.parts > 0 ? (int64_t)t.parts / items + 2 : t.splits;
+    if (parts <= 16) {
+        constexpr int per = 256 / (64);
+        k_kv_merge<D, BF16, 64 * 8 / D><<<(unsigned)((columns + per - 1) / per), 256, 0, s>>>(a, t, (int)columns);
+    } else {
+        k_kv_merge<D, BF16, 256 * 8 / D><<<(unsigned)columns, 256, 0, s>>>(a, t, (int)columns);
+    }
     return hipGetLastError();
 }
 
 } // namespace
 
-KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, int window)
+KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, bool causal, int window)
 {
-    KvPlan p = {LI8_KV_EMPTY, kKvCols, 0, 0, 1, 0};
+    KvPlan p = {LI8_KV_EMPTY, kKvCols, 0, 0, 1, 0, 0};
     const int64_t rows = std::min(b.max_q, b.tokens), group = q_heads / c.heads;
     if (rows == 0 || b.seqs == 0)
         return p;
@@ -926,18 +1176,26 @@ KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, int wi
         p.cols = kTileCols;
     } else {
         p.path = LI8_KV_FEW;
+        p.cols = cols > kKvCols ? 2 * kKvCols : kKvCols;
     }
     p.blocks = (int)((cols + p.cols - 1) / p.cols);
     p.used = (int)std::min<int64_t>(p.cols, cols);
     const int64_t items = plan_items(b, c, p);
     // keys from a span's base to its end at most: a window's keys, the other
-    // rows of the block and the rounding of the base
+    // rows of the block (without `causal` the end is the sequence's, so all
+    // rows that follow) and the rounding of the base
     int64_t span = b.max_kv;
     if (window > 0)
-        span = std::min<int64_t>(span, (int64_t)window + p.cols + 31);
-    const int64_t target = p.path == LI8_KV_TILED ? kTileTarget : kFewTarget;
-    const int64_t least = p.path == LI8_KV_TILED ? kTileMinSplit : kKvMinSplit;
-    const int64_t chunk = std::max(least, round_up((items * span + target - 1) / target, 32 * kFewWaves));
+        span = std::min<int64_t>(span, (int64_t)window + (causal ? p.cols : rows) + 31);
+    if (p.path == LI8_KV_FEW) {
+        const int64_t steps = (span + 31) / 32;
+        if (steps > kFewWhole && items < 8 * kFewSlots && items * steps < ((int64_t)1 << 31)) {
+            p.parts = (int)std::min<int64_t>(kFewSlots, (items * steps + kFewLeast - 1) / kFewLeast);
+            p.splits = (int)std::min<int64_t>(p.parts, steps);
+        }
+        return p;
+    }
+    const int64_t chunk = std::max(kTileMinSplit, round_up((items * span + kTileTarget - 1) / kTileTarget, kTileKeys));
     p.chunk = (int)std::min<int64_t>(chunk, INT32_MAX / 2);
     p.splits = (int)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
     return p;
@@ -945,19 +1203,21 @@ KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, int wi
 
 size_t kv_workspace(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads)
 {
-    const KvPlan p = kv_plan(b, c, q_heads, 0);
+    const KvPlan p = kv_plan(b, c, q_heads, true, 0);
     if (p.path == LI8_KV_EMPTY)
         return 0;
-    // splits under any window: a part has at least `least` keys, and there are
-    // at most target / items parts, rounded up
     const int64_t items = plan_items(b, c, p);
-    const int64_t target = p.path == LI8_KV_TILED ? kTileTarget : kFewTarget;
-    const int64_t least = p.path == LI8_KV_TILED ? kTileMinSplit : kKvMinSplit;
-    const int64_t most = std::min<int64_t>((b.max_kv + least - 1) / least, target / items + 1);
-    if (most <= 1)
+    // Few columns: two slots for each sharing workgroup, most without a
+    // window.  Tiled: the splits under any window, since a part has at least
+    // kTileMinSplit keys and there are at most kTileTarget / items, rounded up.
+    int64_t slots = 2 * (int64_t)p.parts;
+    if (p.path == LI8_KV_TILED) {
+        const int64_t most = std::min<int64_t>((b.max_kv + kTileMinSplit - 1) / kTileMinSplit, kTileTarget / items + 1);
+        slots = most > 1 ? items * most : 0;
+    }
+    if (slots == 0)
         return 0;
-    const int64_t parts = items * most * p.used;
-    return align_up((size_t)parts * 4 * c.head_dim, 256) + align_up((size_t)parts * 4, 256);
+    return align_up((size_t)(slots * p.used) * 4 * c.head_dim, 256) + align_up((size_t)(slots * p.used) * 4, 256);
 }
 
 hipError_t launch_kv_attention(KvTokens Q, bool bf16, int q_heads, float scale, KvRope rope,
@@ -965,16 +1225,18 @@ hipError_t launch_kv_attention(KvTokens Q, bool bf16, int q_heads, float scale, 
                                const li8_kv_cache &c, uint16_t *O, int64_t os, float *lse,
                                char *ws, hipStream_t s)
 {
-    const KvPlan p = kv_plan(b, c, q_heads, window);
+    const KvPlan p = kv_plan(b, c, q_heads, causal, window);
     const KvArgs a = kv_args(b, c);
     const int64_t items = plan_items(b, c, p);
+    const int64_t slots = p.path == LI8_KV_FEW ? 2 * (int64_t)p.parts : items * p.splits;
     AttnArgs t;
     t.Q = Q; t.rope = rope; t.O = O; t.os = os; t.lse = lse;
     t.part_o = reinterpret_cast<float *>(ws);
-    t.part_m = reinterpret_cast<float *>(ws + align_up((size_t)items * p.splits * p.used * 4 * c.head_dim, 256));
+    t.part_m = reinterpret_cast<float *>(ws + align_up((size_t)(slots * p.used) * 4 * c.head_dim, 256));
     t.scale = scale * kLog2e;
     t.group = q_heads / c.heads; t.inv_group = 1.0f / (float)t.group; t.causal = causal; t.window = window;
     t.cols = p.cols; t.blocks = p.blocks; t.used = p.used; t.splits = p.splits; t.chunk = p.chunk;
+    t.seqs = b.seqs; t.parts = p.parts;
     if (c.head_dim == 128)
         return bf16 ? attention_go<128, true>(a, t, items, s) : attention_go<128, false>(a, t, items, s);
     return bf16 ? attention_go<64, true>(a, t, items, s) : attention_go<64, false>(a, t, items, s);

@@ -51,18 +51,19 @@ __host__ __device__ inline KvSpan kv_span(int first, int last, int len, bool cau
     return s;
 }
 
-constexpr int kKvCols = 16;        // query columns of a few-column workgroup
-constexpr int kKvMinSplit = 256;   // fewest keys of a split
+constexpr int kKvCols = 16;        // query columns of a few-column workgroup, or twice as many
 
-// Splits: a block's keys from its span's base on in parts of `chunk`.
+// Tiled: a block's keys from its span's base on are split in parts of
+// `chunk`.  Few columns: `parts` workgroups share all blocks' keys (0: one
+// workgroup for each block).
 struct KvPlan {
     int path;       // LI8_KV_*
     int cols;       // query columns of a workgroup
     int blocks;     // column blocks of the longest chunk
     int used;       // columns in use in the fullest block
-    int splits, chunk;
+    int splits, chunk, parts;
 };
-KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, int window);
+KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, bool causal, int window);
 size_t kv_workspace(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads);
 
 // A rotation table, or cos == nullptr for none.
