@@ -116,7 +116,7 @@ struct Steps {
         blocks = (int)(((int64_t)q.n * t.group + t.cols - 1) / t.cols);
         int span = q.len;
         if (t.window > 0)
-            span = (int)min((int64_t)span, (int64_t)t.window + (t.causal ? t.cols : q.n) + 31);
+            span = (int)min((int64_t)span, (int64_t)t.window + (t.causal ? t.cols : (int64_t)q.len - q.begin) + 31);
         steps = max(1, (span + 31) >> 5);
         all = 64 * c + lane < t.seqs ? a.heads * blocks * steps : 0;
         upto = all;
@@ -618,8 +618,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
     Block b;
     if (!locate(a, t, item, kTileCols, b))
         return;
-    const int ts = b.span.base + sp * t.chunk;
-    const int te = min(b.span.hi, ts + t.chunk);
+    // (the last split takes what is left)
+    const int ts = (int)min((int64_t)b.span.hi, b.span.base + (int64_t)sp * t.chunk);
+    const int te = sp == t.splits - 1 ? b.span.hi : min(b.span.hi, ts + t.chunk);
     if (ts >= te && t.splits > 1)
         return;
 
