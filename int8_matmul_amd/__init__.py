@@ -721,16 +721,16 @@ def _kv_tokens(t: torch.Tensor, name: str, batch: KVBatch, heads: int | None, di
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _KV_DTYPES:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != batch.tokens or t.shape[2] != dim or (heads is not None
-                                                                           and t.shape[1] != heads):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != batch.tokens or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have shape ({batch.tokens}, {'heads' if heads is None else heads}, "
-                         f"{dim}), got {tuple(t.shape)}")
+                         f"{dim}), got {tuple(shape)}")
     if t.device != batch.device:
         raise ValueError(f"{name} is on {t.device}, expected {batch.device}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
         raise ValueError(f"{name}'s rows must be dense [heads, head_dim]")
     # a single row has no step: its stride may be anything
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+    return stride[0] if shape[0] > 1 else shape[1] * dim
 
 
 def _kv_place(batch: KVBatch, cache: KVCache, rope: Rope | None = None) -> None:
@@ -745,12 +745,13 @@ def _kv_place(batch: KVBatch, cache: KVCache, rope: Rope | None = None) -> None:
 
 def _kv_call(name: str, device: torch.device, *args) -> None:
     """The library launches on the current device: make it the tensors'."""
-    fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, _stream(device))
+    fn = getattr(_lib or load_library(), name)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, _stream(device))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != 0:
         raise Int8MatmulError(name, status)
 
@@ -785,13 +786,15 @@ def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.float16,
         raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
     if out is None:
         shape = (batch.tokens, cache.heads, cache.head_dim)
-        out = (torch.empty(shape, dtype=dtype, device=cache.device),
-               torch.empty(shape, dtype=dtype, device=cache.device))
-    K, V = out
-    ks = _kv_tokens(K, "out[0]", batch, cache.heads, cache.head_dim)
-    vs = _kv_tokens(V, "out[1]", batch, cache.heads, cache.head_dim)
-    if K.dtype != dtype or V.dtype != dtype:
-        raise TypeError(f"out must be {dtype}, got {K.dtype} and {V.dtype}")
+        K = torch.empty(shape, dtype=dtype, device=cache.device)
+        V = torch.empty(shape, dtype=dtype, device=cache.device)
+        ks = vs = cache.heads * cache.head_dim
+    else:
+        K, V = out
+        ks = _kv_tokens(K, "out[0]", batch, cache.heads, cache.head_dim)
+        vs = _kv_tokens(V, "out[1]", batch, cache.heads, cache.head_dim)
+        if K.dtype != dtype or V.dtype != dtype:
+            raise TypeError(f"out must be {dtype}, got {K.dtype} and {V.dtype}")
     _kv_call("int8_kv_read", batch.device, cache._ref, batch._ref, _KV_DTYPES[dtype], K.data_ptr(), ks,
              V.data_ptr(), vs)
     return K, V

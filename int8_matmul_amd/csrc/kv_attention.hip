@@ -564,6 +564,7 @@ constexpr int kTileWaves = 8;
 constexpr int kTileCols = 32 * kTileWaves;
 constexpr int kTileKeys = 64;
 constexpr float kLeast = -100.0f;      // log2 of the smallest relative value scale
+constexpr float kMost = 8192.0f;       // largest sum of 8 probabilities taken as it is
 
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -719,12 +720,14 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
 
     // A subtile is 32 keys.  MFMA and VALU work of neighbouring subtiles is
     // independent and put side by side, instruction by instruction:
-    //   X(j)  O^T += V^T P^T of subtile j - 1  |  the scores of j as floats, their maximum
+    //   X(j)  O^T += V^T P^T of subtile j - 1  |  the scores of j as floats
     //   Y(j)  S^T of subtile j + 1             |  the probabilities of j
-    // with the rare change of the running maximum between them.  The waves
-    // run in step at the barriers, so what one wave leaves idle the other on
-    // its SIMD leaves idle too; and the compiler, left to itself, puts the
-    // MFMAs of a block in a row and the VALU work behind them.
+    // The kernel is bound by the instructions that its two waves per SIMD
+    // issue, VALU above all, so the running maximum is not computed: the
+    // probabilities are taken against the last one, and only when their sum
+    // shows one that fp16 may not hold (Y's last line) is the maximum moved
+    // and the subtile's probabilities taken again, which is rare after the
+    // first.  PREFILL
     v16f acc[DB] = {};
     v16i si;
     float x[16];
@@ -771,20 +774,26 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
     };
     // Four probabilities.  The value scale goes into the exponent,
     // 2^(z - m + log2(vs / vref)), and out of the sum again.
-    float bias[2], lv[2];
+    float y[16], bias[2], lv[2], lg[2];
+    auto biases = [&]() {
+#pragma unroll
+        for (int gi = 0; gi < 2; gi++) {
+            lv[gi] = fmaxf(sc[gi].y - lref, kLeast);
+            bias[gi] = lv[gi] - m + sc[gi].z;
+        }
+    };
     auto exps = [&](int e0) {
 #pragma unroll
         for (int e = e0; e < e0 + 4; e++)
-            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], sc[e >> 3].x, bias[e >> 3]));
+            y[e] = __builtin_amdgcn_exp2f(fmaf(x[e], sc[e >> 3].x, bias[e >> 3]));
         LI8_FENCE;
     };
     auto to_half = [&](int gi) {
-        const float *y = x + 8 * gi;
-        const float lg = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-        l = fmaf(lg, __builtin_amdgcn_exp2f(-lv[gi]), l);
+        const float *v = y + 8 * gi;
+        lg[gi] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 #pragma unroll
         for (int e = 0; e < 8; e++)
-            p[gi][e] = (_Float16)y[e];
+            p[gi][e] = (_Float16)v[e];
         LI8_FENCE;
     };
     // X: PV of the subtile before (its first fragments are in vf, each
@@ -816,11 +825,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
     auto part_y = [&](int buf, int tt) {
         read_v(buf, tt, 0);
         si = v16i{};
-#pragma unroll
-        for (int gi = 0; gi < 2; gi++) {
-            lv[gi] = fmaxf(sc[gi].y - lref, kLeast);
-            bias[gi] = lv[gi] - m + sc[gi].z;
-        }
+        // the factor of the integers (not 0: a masked score is -inf times it)
+        sc[0].x = fmaxf(f * sc[0].x, 1.0e-30f);
+        sc[1].x = fmaxf(f * sc[1].x, 1.0e-30f);
+        biases();
         LI8_FENCE;
         if constexpr (KS == 4) {
             mfma_k(0, qh); exps(0);
@@ -842,33 +850,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
             mfma_k(0, ql); exps(12);
             mfma_k(1, ql); to_half(1);
         }
-    };
-    // Masks, the maximum, and what changes with it.
-    auto settle = [&](int t0) {
-        if (t0 < wlo || t0 + 32 > whi) {
+        if (__any(fmaxf(lg[0], lg[1]) > kMost)) {
+            float zm = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 16; e++) {
-                const int key = t0 + 8 * (e >> 2) + 4 * half + (e & 3);
-                x[e] = key < chi && key >= clo ? x[e] : -INFINITY;
-            }
-        }
-        // the factor of the integers (not 0: a masked score is -inf times it)
-        sc[0].x = fmaxf(f * sc[0].x, 1.0e-30f);
-        sc[1].x = fmaxf(f * sc[1].x, 1.0e-30f);
-        float g[2];
-#pragma unroll
-        for (int gi = 0; gi < 2; gi++) {
-            const float *y = x + 8 * gi;
-            g[gi] = fmaxf(fmaxf(fmaxf(fmaxf(y[0], y[1]), y[2]), fmaxf(fmaxf(y[3], y[4]), y[5])), fmaxf(y[6], y[7]));
-            g[gi] = fmaf(g[gi], sc[gi].x, sc[gi].z);
-        }
-        float zm = fmaxf(g[0], g[1]);
-        const float lm = fmaxf(sc[0].y, sc[1].y);
-        // The maximum is moved only when a score is 8 above it (in powers of
-        // two): until then the probabilities stay below 2^8.
-        if (__any(zm > m + 8.0f || lm > lref)) {
+            for (int e = 0; e < 16; e++)
+                zm = fmaxf(zm, fmaf(x[e], sc[e >> 3].x, sc[e >> 3].z));
             zm = fmaxf(zm, __shfl_xor(zm, 32, 64));
-            const float mn = zm > m + 8.0f ? zm : m, ln = lm > lref ? lm + 0.5f : lref;   // (some room)
+            const float mn = fmaxf(m, zm), ln = fmaxf(lref, fmaxf(sc[0].y, sc[1].y));
             const float am = __builtin_amdgcn_exp2f(m - mn);
             const float al = am * __builtin_amdgcn_exp2f(lref - ln);
 #pragma unroll
@@ -877,6 +865,23 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
             l *= am;
             m = mn;
             lref = ln;
+            biases();
+#pragma unroll
+            for (int e0 = 0; e0 < 16; e0 += 4)
+                exps(e0);
+            to_half(0);
+            to_half(1);
+        }
+        l = fmaf(lg[0], __builtin_amdgcn_exp2f(-lv[0]), l);
+        l = fmaf(lg[1], __builtin_amdgcn_exp2f(-lv[1]), l);
+    };
+    auto mask = [&](int t0) {
+        if (t0 < wlo || t0 + 32 > whi) {
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                const int key = t0 + 8 * (e >> 2) + 4 * half + (e & 3);
+                x[e] = key < chi && key >= clo ? x[e] : -INFINITY;
+            }
         }
     };
 
@@ -930,10 +935,10 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
             const int t0 = ts + kTileKeys * i;
             stage();
             part_x(pbuf, 1, buf, 0, buf, 1);
-            settle(t0);
+            mask(t0);
             part_y(buf, 0);
             part_x(buf, 0, buf, 1, buf, 1);
-            settle(t0 + 32);
+            mask(t0 + 32);
             lds_barrier();
             read_k(next(), 0);   // (past the last step: of no use, and not used)
             part_y(buf, 1);
