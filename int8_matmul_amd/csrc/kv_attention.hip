@@ -241,12 +241,13 @@ __device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t
     });
 }
 
-// Codes of byte `byte` of two keys' words (already offset by 128: 0..255) as
-// fp16: 0x6400 | u is 1024 + u, and 1024 + u - 1152 is the code, exactly.
+// Codes of one byte of two keys' words as fp16.  0x6400 | u is 1024 + u for a
+// byte u; with the code's sign bit flipped u is code + 128, so 1152 less is the
+// code, exactly.
 template <int BYTE>
 __device__ __forceinline__ uint32_t codes_f16(uint32_t a, uint32_t b)
 {
-    const uint32_t w = __builtin_amdgcn_perm(b, a, 0x0c000c00u | BYTE | ((4 + BYTE) << 16)) | 0x64006400u;
+    const uint32_t w = __builtin_amdgcn_perm(b, a, 0x0c000c00u | BYTE | ((4 + BYTE) << 16)) ^ 0x64806480u;
     const kv_h2 h = __builtin_bit_cast(kv_h2, w) - (kv_h2){(_Float16)1152.0f, (_Float16)1152.0f};
     return __builtin_bit_cast(uint32_t, h);
 }
@@ -417,17 +418,13 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
         // operand n is dim col NB + n of all of them.
 #pragma unroll
         for (int d = 0; d < KS; d++) {
-            uint32_t u[8];
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                u[j] = w.v[j][d] ^ 0x80808080u;
             v4u x0, x1, x2, x3;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                x0[j] = codes_f16<0>(u[2 * j], u[2 * j + 1]);
-                x1[j] = codes_f16<1>(u[2 * j], u[2 * j + 1]);
-                x2[j] = codes_f16<2>(u[2 * j], u[2 * j + 1]);
-                x3[j] = codes_f16<3>(u[2 * j], u[2 * j + 1]);
+                x0[j] = codes_f16<0>(w.v[2 * j][d], w.v[2 * j + 1][d]);
+                x1[j] = codes_f16<1>(w.v[2 * j][d], w.v[2 * j + 1][d]);
+                x2[j] = codes_f16<2>(w.v[2 * j][d], w.v[2 * j + 1][d]);
+                x3[j] = codes_f16<3>(w.v[2 * j][d], w.v[2 * j + 1][d]);
             }
 #pragma unroll
             for (int c = 0; c < NC; c++) {
@@ -693,18 +690,14 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
         const int at = buf * L::stage;
         asm("" : "+v"(vput));
         *reinterpret_cast<uint4 *>(smem + at + kput) = rk;
-        uint32_t u[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            u[e] = rv[e] ^ 0x80808080u;
         *reinterpret_cast<uint2 *>(smem + (at + vput)) =
-            make_uint2(codes_f16<0>(u[0], u[1]), codes_f16<0>(u[2], u[3]));
+            make_uint2(codes_f16<0>(rv[0], rv[1]), codes_f16<0>(rv[2], rv[3]));
         *reinterpret_cast<uint2 *>(smem + ((at + vput) ^ 16) + 128) =
-            make_uint2(codes_f16<1>(u[0], u[1]), codes_f16<1>(u[2], u[3]));
+            make_uint2(codes_f16<1>(rv[0], rv[1]), codes_f16<1>(rv[2], rv[3]));
         *reinterpret_cast<uint2 *>(smem + ((at + vput) ^ 32) + 256) =
-            make_uint2(codes_f16<2>(u[0], u[1]), codes_f16<2>(u[2], u[3]));
+            make_uint2(codes_f16<2>(rv[0], rv[1]), codes_f16<2>(rv[2], rv[3]));
         *reinterpret_cast<uint2 *>(smem + ((at + vput) ^ 48) + 384) =
-            make_uint2(codes_f16<3>(u[0], u[1]), codes_f16<3>(u[2], u[3]));
+            make_uint2(codes_f16<3>(rv[0], rv[1]), codes_f16<3>(rv[2], rv[3]));
         if (lane == 0) {   // (the waves of a group write the same)
             // no such page: a factor of 0, and -inf added to every score
             *reinterpret_cast<v4f *>(s_sc[buf][group]) =
@@ -803,6 +796,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
         sc[0] = *reinterpret_cast<const v4f *>(s_sc[buf][2 * tt]);
         sc[1] = *reinterpret_cast<const v4f *>(s_sc[buf][2 * tt + 1]);
         asm("" : "+v"(vplace));
+        read_k(kbuf, ktt);
         LI8_FENCE;
 #pragma unroll
         for (int n = 0; n < DB; n++) {
@@ -817,8 +811,6 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
                 to_float(8 * n + 4);
             mfma_v(n, 1);
         }
-        read_k(kbuf, ktt);
-        LI8_FENCE;
     };
     // Y: the next subtile's products with the queries (kf), this one's
     // probabilities; vf is read on the way.
@@ -937,10 +929,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
             part_x(pbuf, 1, buf, 0, buf, 1);
             mask(t0);
             part_y(buf, 0);
-            part_x(buf, 0, buf, 1, buf, 1);
-            mask(t0 + 32);
             lds_barrier();
-            read_k(next(), 0);   // (past the last step: of no use, and not used)
+            part_x(buf, 0, buf, 1, next(), 0);   // (past the last step: keys of no use, and not used)
+            mask(t0 + 32);
             part_y(buf, 1);
             leave();
         }
