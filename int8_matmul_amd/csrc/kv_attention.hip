@@ -34,7 +34,7 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr float kNone = -1.0e30f;      // a running maximum over nothing yet
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kQMax = 16256.0f;      // 127 * 128: the largest 15-bit query integer
-constexpr int kFewLeast = 8;           // fewest steps of a workgroup that shares
+constexpr int kLeastSteps = 8;         // fewest steps of a workgroup that shares
 
 struct AttnArgs {
     KvTokens Q;
@@ -42,12 +42,12 @@ struct AttnArgs {
     uint16_t *O;
     int64_t os;
     float *lse;
-    // partial results: tiled [item][split][used][D] and [item][split][used],
-    // few columns [2 part + k][used][D], k = 0 for the run's first block
+    // partial results: [2 part + k][used][D] and [2 part + k][used], k = 0 for
+    // the run's first block
     float *part_o, *part_m;
     float scale, inv_group;            // scale * log2(e), 1 / group
     int group, causal, window;
-    int cols, blocks, used, splits, chunk;
+    int cols, blocks, used;
     int seqs, parts;                   // parts: workgroups that share the steps, 0: one per block
 };
 
@@ -94,14 +94,14 @@ __device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int i
     return place(t, kv_sequence_of(a, s), s, sh % a.heads, cb, cols, b);
 }
 
-// The work of the few-column kernel in steps of 32 keys, one sequence after
-// another, and within it head after head and block after block, each with
+// The work in steps of 2^SHIFT keys, one sequence after another, and within it head after head and block after block, each with
 // the sequence's largest number of steps (at least one, so that an empty row
 // is written).  `parts` workgroups take equal runs of steps, whatever the
 // lengths are: a grid over sequences alone leaves most of the chip to the
 // longest one.  Every workgroup, of the merging kernel too, counts the steps
 // itself, a lane for each of 64 sequences at a time.  (All counts are below
 // 2^31: the host shares no more than that.)
+template <int SHIFT>
 struct Steps {
     KvSeq q;                           // this lane's sequence
     int steps, blocks;                 // steps of each of its blocks
@@ -117,7 +117,7 @@ struct Steps {
         int span = q.len;
         if (t.window > 0)
             span = (int)min((int64_t)span, (int64_t)t.window + (t.causal ? t.cols : (int64_t)q.len - q.begin) + 31);
-        steps = max(1, (span + 31) >> 5);
+        steps = max(1, (span + (1 << SHIFT) - 1) >> SHIFT);
         all = 64 * c + lane < t.seqs ? a.heads * blocks * steps : 0;
         upto = all;
 #pragma unroll
@@ -136,7 +136,7 @@ struct Steps {
             total += __builtin_amdgcn_readlane(upto, 63);
         }
         base = 0;
-        return max(kFewLeast, (total + t.parts - 1) / t.parts);
+        return max(kLeastSteps, (total + t.parts - 1) / t.parts);
     }
 
     // The lane whose sequence has step `at` (at < total, not before `base`).
@@ -159,6 +159,53 @@ struct Steps {
         r.len = __builtin_amdgcn_readlane(q.len, k);
         r.begin = __builtin_amdgcn_readlane(q.begin, k);
         return r;
+    }
+};
+
+// The blocks of one workgroup's run of steps, one after another: block b,
+// steps first .. first + count - 1 of it, and the slot of its partial result.
+// A run's first block goes to the run's slot 0, a later one that it does not
+// finish to slot 1, and one that is all its own to O (-1).
+// Without KEEP the sequences are looked at anew for each block, and the lanes
+// hold nothing of them in between.
+template <int SHIFT, bool KEEP>
+struct Run {
+    Steps<SHIFT> w;
+    int part, begin, at, end, chunk, base;
+
+    __device__ __forceinline__ bool start(const KvArgs &a, const AttnArgs &t, int run, int lane)
+    {
+        int total;
+        part = run;
+        const int per = __builtin_amdgcn_readfirstlane(w.share(a, t, lane, total));
+        const int64_t b = (int64_t)run * per;
+        if (b >= total)
+            return false;
+        begin = at = (int)b;
+        end = (int)min(b + per, (int64_t)total);
+        chunk = base = 0;
+        return true;
+    }
+
+    // false: the block has no column (its steps are passed over)
+    __device__ __forceinline__ bool next(const KvArgs &a, const AttnArgs &t, int cols, int lane, Block &b, int &first,
+                                         int &count, int64_t &slot)
+    {
+        if constexpr (!KEEP) {
+            w.look(a, t, chunk, lane);
+            w.base = base;
+        }
+        const int k = __builtin_amdgcn_readfirstlane(w.find(a, t, at, lane));
+        chunk = __builtin_amdgcn_readfirstlane(w.chunk);
+        base = __builtin_amdgcn_readfirstlane(w.base);
+        const int steps = __builtin_amdgcn_readlane(w.steps, k), blocks = __builtin_amdgcn_readlane(w.blocks, k);
+        const int r = at - base - __builtin_amdgcn_readlane(w.upto - w.all, k);
+        const int unit = r / steps, h = unit / blocks, cb = unit - h * blocks;
+        first = r - unit * steps;
+        count = min(steps - first, end - at);
+        slot = count == steps ? -1 : 2 * (int64_t)part + (at == begin ? 0 : 1);
+        at += count;
+        return place(t, w.seq_of(k), 64 * chunk + k, h, cb, cols, b);
     }
 };
 
@@ -203,11 +250,11 @@ __device__ __forceinline__ void split_query(const float x[8], uint2 &hi, uint2 &
 // the first rows have been requested.
 template <int D, bool BF16, int COLS, int NT, int LQ, class Between>
 __device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t, const Block &b, char *lds,
-                                              float *factor, Between between)
+                                              float *factor, int tid, Between between)
 {
     constexpr int CPR = D / 8, PASSES = COLS * CPR / NT > 0 ? COLS * CPR / NT : 1;
     constexpr int BATCH = PASSES < 4 ? PASSES : 4;   // rows of a thread in flight
-    const int cc = threadIdx.x % CPR;
+    const int cc = tid % CPR;
     with_rotation(t.rope, [&](auto rot) {
         constexpr int ROT = decltype(rot)::value;
 #pragma unroll
@@ -216,7 +263,7 @@ __device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t
 #pragma unroll
             for (int k = 0; k < BATCH; k++) {
                 int g;   // (columns past the last: the last one again)
-                const int qc = min((int)threadIdx.x / CPR + (k0 + k) * (NT / CPR), b.nc - 1);
+                const int qc = min(tid / CPR + (k0 + k) * (NT / CPR), b.nc - 1);
                 const int i = b.row_of(qc, t, g);
                 fetch_row<ROT>(w[k], t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D,
                                cc, t.rope, max(b.q.begin + i, 0));
@@ -225,7 +272,7 @@ __device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t
                 between();
 #pragma unroll
             for (int k = 0; k < BATCH; k++) {
-                const int qc = threadIdx.x / CPR + (k0 + k) * (NT / CPR);
+                const int qc = tid / CPR + (k0 + k) * (NT / CPR);
                 float x[8], f;
                 uint2 hi, lo;
                 rotate_row<BF16, ROT>(w[k], cc, t.rope, x);
@@ -325,7 +372,7 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
     // the queries and the first step's data are requested together
     if (any)
         pages(pid, t0);
-    split_queries<D, BF16, COLS, 64 * NW, LQ>(a, t, b, smem, s_f, [&]() {
+    split_queries<D, BF16, COLS, 64 * NW, LQ>(a, t, b, smem, s_f, tid, [&]() {
         if (any) {
             load_step<D>(st[0], a, pid, b.h, t0, b.span.lo, te, koff, voff);
             pages(pid, t0 + kStride);
@@ -521,32 +568,23 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
     __shared__ float s_f[COLS], s_m[NW * COLS], s_l[NW * COLS];
     Block b;
     if (t.parts == 0) {
-        if (locate(a, t, blockIdx.x, COLS, b))
+        // (a prompt's last blocks, which see the most keys, first)
+        const int cb = blockIdx.x % t.blocks;
+        if (locate(a, t, blockIdx.x - cb + (t.blocks - 1 - cb), COLS, b))
             few_block<D, BF16, NC, NW>(a, t, b, b.span.base, b.span.hi, -1, smem, s_f, s_m, s_l);
         return;
     }
     const int lane = threadIdx.x & 63;
-    Steps w;
-    int total;
-    const int per = __builtin_amdgcn_readfirstlane(w.share(a, t, lane, total));
-    const int64_t begin64 = (int64_t)blockIdx.x * per;
-    if (begin64 >= total)
+    Run<5, true> run;
+    if (!run.start(a, t, blockIdx.x, lane))
         return;
-    const int begin = (int)begin64, end = (int)min(begin64 + per, (int64_t)total);
-    for (int at = begin; at < end;) {
-        const int k = __builtin_amdgcn_readfirstlane(w.find(a, t, at, lane));
-        const int steps = __builtin_amdgcn_readlane(w.steps, k), blocks = __builtin_amdgcn_readlane(w.blocks, k);
-        const int r = at - w.base - __builtin_amdgcn_readlane(w.upto - w.all, k);
-        const int unit = r / steps, first = r - unit * steps, h = unit / blocks, cb = unit - h * blocks;
-        const int count = min(steps - first, end - at);
-        // a run's first block goes to the run's slot 0, a later one that it
-        // does not finish to slot 1, and one that is all its own to O
-        const int64_t slot = count == steps ? -1 : 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
-        if (place(t, w.seq_of(k), 64 * w.chunk + k, h, cb, COLS, b)) {
+    while (run.at < run.end) {
+        int first, count;
+        int64_t slot;
+        if (run.next(a, t, COLS, lane, b, first, count, slot)) {
             const int ts = b.span.base + 32 * first;
             few_block<D, BF16, NC, NW>(a, t, b, ts, min(b.span.hi, ts + 32 * count), slot, smem, s_f, s_m, s_l);
         }
-        at += count;
         __syncthreads();
     }
 }
@@ -589,40 +627,20 @@ struct TileLds {
 };
 
 template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnArgs t, int pairs, int lanes, int deep)
+__device__ __forceinline__ void tile_block(const KvArgs &a, const AttnArgs &t, const Block &b, int ts, int te,
+                                           int64_t slot, char *smem, float *s_f, float (*s_sc)[4][4])
 {
-    constexpr int NT = 64 * kTileWaves, CPR = D / 8, KS = D / 32, DB = D / 32;
+    constexpr int NT = 64 * kTileWaves, KS = D / 32, DB = D / 32;
     constexpr int ITEMS = kTileKeys * D / 16;   // pieces to stage, at most one for each thread
     static_assert(ITEMS <= NT && ITEMS % 256 == 0, "staging");
     using L = TileLds<D>;
-    __shared__ __align__(16) char smem[L::bytes];
-    __shared__ float s_f[kTileCols];
-    __shared__ __align__(16) float s_sc[3][4][4];   // [buffer][group of 16 keys][k scale, log2 v scale, 0 or -inf]
-    const int tid = threadIdx.x, lane = tid & 63;
+    // (read anew for each block: what follows from it would be kept in
+    // registers from block to block, which there are none for)
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // Blocks of one (sequence, head) share its keys: they stay on 8 / lanes
-    // of the XCDs (the hardware deals workgroups to the 8 XCDs in turn).
-    // Where a chunk is most of its sequence (deep == 0) its last blocks see
-    // the most keys and go first, those of all pairs of the lane before any
-    // block that sees fewer: a long block that starts late would run alone at
-    // the end.  Chunks over much longer sequences have blocks alike, and one
-    // pair goes after the other, so that its keys stay in the L2.
-    const int j = blockIdx.x / lanes, ppl = (pairs + lanes - 1) / lanes, per = t.blocks * t.splits;
-    const int pair = (deep ? j / per : j % ppl) * lanes + blockIdx.x % lanes;
-    if (pair >= pairs)
-        return;
-    const int rest = deep ? j % per : j / ppl, sp = rest % t.splits;
-    const int item = pair * t.blocks + (t.blocks - 1 - rest / t.splits);
-    Block b;
-    if (!locate(a, t, item, kTileCols, b))
-        return;
-    // (the last split takes what is left)
-    const int ts = (int)min((int64_t)b.span.hi, b.span.base + (int64_t)sp * t.chunk);
-    const int te = sp == t.splits - 1 ? b.span.hi : min(b.span.hi, ts + t.chunk);
-    if (ts >= te && t.splits > 1)
-        return;
-
-    split_queries<D, BF16, kTileCols, NT, L::q_row>(a, t, b, smem, s_f, []() {});
+    split_queries<D, BF16, kTileCols, NT, L::q_row>(a, t, b, smem, s_f, tid, []() {});
     __syncthreads();
     const int col = lane & 31, half = lane >> 5, qcol = 32 * wid + col;
     v4i qh[KS], ql[KS];
@@ -953,8 +971,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
         return;
     l += __shfl_xor(l, 32, 64);
     const float s = l > 0.0f ? __builtin_amdgcn_exp2f(lref) / l : 0.0f;
-    if (t.splits > 1) {
-        const int64_t at = ((int64_t)item * t.splits + sp) * t.used + qcol;
+    if (slot >= 0) {
+        const int64_t at = slot * t.used + qcol;
 #pragma unroll
         for (int n = 0; n < DB; n++)
 #pragma unroll
@@ -982,56 +1000,65 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
         t.lse[row * (int64_t)(a.heads * t.group) + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// Merges the partial results of a column: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M),
-// m_i the part's log2 of its sum.  SL lanes of parts x D/8 chunks per column,
-// 256 / (SL D/8) columns per workgroup; four parts are in flight per lane.
+template <int D, bool BF16>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnArgs t, int pairs, int lanes, int deep)
+{
+    __shared__ __align__(16) char smem[TileLds<D>::bytes];
+    __shared__ float s_f[kTileCols];
+    __shared__ __align__(16) float s_sc[3][4][4];   // [buffer][group of 16 keys][k scale, log2 v scale, 0 or -inf]
+    const int lane = threadIdx.x & 63;
+    Run<6, false> run;
+    Block b;
+    int first = 0, count = 0;
+    int64_t slot = -1;
+    bool there;
+    if (t.parts == 0) {
+        // Blocks of one (sequence, head) share its keys: they stay on
+        // 8 / lanes of the XCDs (the hardware deals workgroups to the 8 XCDs
+        // in turn).  Where a chunk is most of its sequence (deep == 0) its
+        // last blocks see the most keys and go first, those of all pairs of
+        // the lane before any block that sees fewer: a long block that starts
+        // late would run alone at the end.  Chunks over much longer sequences
+        // have blocks alike, and one pair goes after the other, so that its
+        // keys stay in the L2.
+        const int j = blockIdx.x / lanes, ppl = (pairs + lanes - 1) / lanes;
+        const int pair = (deep ? j / t.blocks : j % ppl) * lanes + blockIdx.x % lanes;
+        if (pair >= pairs)
+            return;
+        there = locate(a, t, pair * t.blocks + (t.blocks - 1 - (deep ? j % t.blocks : j / ppl)), kTileCols, b);
+        run.at = run.end = 0;
+    } else {
+        // neighbouring runs on one XCD
+        const int per = t.parts >> 3;
+        if (!run.start(a, t, t.parts & 7 ? blockIdx.x : (blockIdx.x & 7) * per + (blockIdx.x >> 3), lane))
+            return;
+        there = run.next(a, t, kTileCols, lane, b, first, count, slot);
+    }
+    while (true) {
+        if (there) {
+            const int ts = min(b.span.base + kTileKeys * first, b.span.hi);
+            const int te = count ? min(b.span.hi, ts + kTileKeys * count) : b.span.hi;
+            tile_block<D, BF16>(a, t, b, ts, te, slot, smem, s_f, s_sc);
+        }
+        if (run.at >= run.end)
+            return;
+        __syncthreads();
+        there = run.next(a, t, kTileCols, lane, b, first, count, slot);
+    }
+}
+
 template <int D, bool BF16, int SL>
-__global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int columns)
+__device__ __forceinline__ void merge_column(const KvArgs &a, const AttnArgs &t, const Block &b, int qc, int na,
+                                             int64_t slot0, int p0, int sl, int cc)
 {
     constexpr int CPR = D / 8, WIDTH = SL * CPR;
-    static_assert(WIDTH == 64 || WIDTH == 256, "a wave has one column");
-    const int cc = threadIdx.x % CPR, sl = threadIdx.x % WIDTH / CPR;
-    const int at_col = blockIdx.x * (256 / WIDTH) + threadIdx.x / WIDTH;
-    const int qc = at_col % t.used, item = min(at_col, columns - 1) / t.used;
-    Block b;
-    bool mine = locate(a, t, item, t.cols, b) && qc < b.nc && at_col < columns;
-    // part i of the column is at slot first + i * step
-    int64_t first = 0;
-    int na = 0, step = 1;
-    if (t.parts == 0) {
-        first = (int64_t)item * t.splits;
-        na = mine && b.span.hi > b.span.lo ? min((b.span.hi - b.span.base + t.chunk - 1) / t.chunk, t.splits) : 0;
-    } else {
-        // (a wave's columns are of one sequence)
-        const int lane = threadIdx.x & 63;
-        const int cb = item % t.blocks, sh = item / t.blocks, s = sh / a.heads, h = sh % a.heads;
-        Steps w;
-        int total, before = 0;
-        const int per = w.share(a, t, lane, total);
-        for (int c = 0; c < (s >> 6); c++) {
-            before += __shfl(w.upto, 63, 64);
-            w.look(a, t, c + 1, lane);
-        }
-        const int k = s & 63, steps = __shfl(w.steps, k, 64), blocks = __shfl(w.blocks, k, 64);
-        const int u0 = before + __shfl(w.upto - w.all, k, 64) + (h * blocks + cb) * steps, u1 = u0 + steps - 1;
-        const int p0 = u0 / per, p1 = u1 / per;
-        mine = mine && p1 > p0;          // (else its workgroup has written it)
-        // the first part is the last block of its run (slot 1) unless the run
-        // begins with it, the others begin theirs (slot 0)
-        first = u0 == p0 * per ? 2 * p0 : 2 * p0 + 1;
-        na = mine ? p1 - p0 + 1 : 0;
-        step = 2;
-    }
-    auto slot = [&](int i) {
-        const int64_t k = first + (int64_t)step * i;
-        return (step == 2 && i > 0 ? k & ~(int64_t)1 : k) * t.used + qc;
-    };
     float m = kNone, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int i = sl; i < na; i += 4 * SL) {
         float e[4], x[4][8];
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const int64_t at = slot(min(i + k * SL, na - 1));
+            const int j = min(i + k * SL, na - 1);
+            const int64_t at = (j == 0 ? slot0 : 2 * (int64_t)(p0 + j)) * t.used + qc;
             e[k] = t.part_m[at];
             *reinterpret_cast<float4 *>(x[k]) = *reinterpret_cast<const float4 *>(t.part_o + at * D + 8 * cc);
             *reinterpret_cast<float4 *>(x[k] + 4) = *reinterpret_cast<const float4 *>(t.part_o + at * D + 8 * cc + 4);
@@ -1057,7 +1084,7 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int colu
         m = mn;
     };
 #pragma unroll
-    for (int d = CPR; d < 64; d *= 2) {
+    for (int d = CPR; d < (WIDTH < 64 ? WIDTH : 64); d *= 2) {
         float o2[8];
 #pragma unroll
         for (int k = 0; k < 8; k++)
@@ -1066,8 +1093,9 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int colu
     }
     if constexpr (WIDTH > 64) {
         constexpr int W = WIDTH / 64;
-        __shared__ float s_o[256 / 64][D], s_m[256 / 64], s_l[256 / 64];
-        const int w = threadIdx.x / 64, w0 = w / W * W;
+        __shared__ float s_o[W][D], s_m[W], s_l[W];
+        const int w = threadIdx.x / 64;
+        __syncthreads();                         // (the column before)
         if (threadIdx.x % 64 < CPR) {
 #pragma unroll
             for (int k = 0; k < 8; k++)
@@ -1076,17 +1104,17 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int colu
             s_l[w] = l;
         }
         __syncthreads();
-        if (w == w0) {
+        if (w == 0) {
             for (int i = 1; i < W; i++) {
                 float o2[8];
 #pragma unroll
                 for (int k = 0; k < 8; k++)
-                    o2[k] = s_o[w0 + i][8 * cc + k];
-                join(s_m[w0 + i], s_l[w0 + i], o2);
+                    o2[k] = s_o[i][8 * cc + k];
+                join(s_m[i], s_l[i], o2);
             }
         }
     }
-    if (!mine || sl != 0)
+    if (sl != 0 || threadIdx.x >= (WIDTH == 256 ? 64 : 256))
         return;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -1101,11 +1129,62 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int colu
         t.lse[row * (int64_t)(a.heads * t.group) + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-constexpr int kTileTarget = 512;
-constexpr int64_t kTileMinSplit = 1024;
-constexpr int kTileFrom = 64;          // columns from which the tiled kernel is taken
-constexpr int kFewWhole = 40;          // steps up to which a block stays whole
+// Merges the partial results of a block's columns: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M),
+// m_i the part's log2 of its sum.  SL lanes of parts x D/8 chunks work on a
+// column: with many parts the workgroup, else a wave, or (SL = 1, where blocks
+// are wide and in few parts) D/8 lanes of it.  A wave has `each` columns of
+// one block; four parts are in flight per lane.
+template <int D, bool BF16, int SL, int SHIFT>
+__global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int items, int each)
+{
+    constexpr int CPR = D / 8, WIDTH = SL * CPR;
+    constexpr int TASK = WIDTH > 64 ? WIDTH : 64;   // threads of a task
+    const int cc = threadIdx.x % CPR, sl = threadIdx.x % WIDTH / CPR, lane = threadIdx.x & 63;
+    const int task = blockIdx.x * (256 / TASK) + threadIdx.x / TASK, tasks = (t.used + each - 1) / each;
+    const int item = min(task / tasks, items - 1);
+    Block b;
+    const bool there = locate(a, t, item, t.cols, b) && task / tasks < items;
+    // steps before the block
+    const int cb = item % t.blocks, sh = item / t.blocks, s = sh / a.heads, h = sh % a.heads;
+    Steps<SHIFT> w;
+    int total, before = 0;
+    const int per = w.share(a, t, lane, total);
+    for (int c = 0; c < (s >> 6); c++) {
+        before += __shfl(w.upto, 63, 64);
+        w.look(a, t, c + 1, lane);
+    }
+    const int k = s & 63, steps = __shfl(w.steps, k, 64), blocks = __shfl(w.blocks, k, 64);
+    const int u0 = before + __shfl(w.upto - w.all, k, 64) + (h * blocks + cb) * steps, u1 = u0 + steps - 1;
+    const int p0 = u0 / per, p1 = u1 / per;
+    if (!there || p1 == p0)                      // (its workgroup has written it)
+        return;
+    // Its first part is the last block of its run (slot 1) unless the run
+    // begins with it; the others begin theirs (slot 0).
+    const int na = p1 - p0 + 1;
+    const int64_t slot0 = u0 == p0 * per ? 2 * (int64_t)p0 : 2 * (int64_t)p0 + 1;
+    const int first = task % tasks * each, stop = min(first + each, b.nc);
+    for (int qc = first + threadIdx.x % TASK / WIDTH; qc < stop; qc += TASK / WIDTH)
+        merge_column<D, BF16, SL>(a, t, b, qc, na, slot0, p0, sl, cc);
+}
+
+// Which kernel, and whether blocks are shared, measured (us):
+//   tiled from 128 columns and 4096 steps (blocks x steps of 64 keys) on: two
+//   chunks' worth of work per CU.  Few columns against tiled at 128 heads x
+//   blocks of a 1024-token prompt with 32 heads (2048 steps) 41 : 42, at 2048
+//   tokens (8192 steps) 164 : 72, 64 tokens x 64 heads over 8192 keys (2048
+//   steps) 45 : 50, 256 tokens x 64 heads over 8192 keys (8192 steps)
+//   127 : 97; 8 tokens x 8 heads of a group, 64 columns, in 16 sequences of
+//   up to 4096 keys 52 : 69, twice as many 83 : 72.
+//   few columns are shared past 40 steps of 32 keys: at 25 steps one launch
+//   took 11.1 against 13.5, at 41 to 4096 sharing is up to 4 times as fast.
+//   tiled blocks are shared where there are fewer than CUs: 64 blocks of 128
+//   steps 97 against 242 unshared, 256 blocks of a 2048-token prompt 77
+//   against 72 (their keys differ, which the count of steps does not know).
+constexpr int kTileColumns = 128;
+constexpr int kTileSteps = 4096;
+constexpr int kFewWhole = 40;
 constexpr int kFewSlots = 512;         // workgroups that share steps: 2 for each CU
+constexpr int kTileSlots = 256;        // tiled: 1 for each CU
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
@@ -1122,8 +1201,9 @@ hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipSt
         // (sequence, head) pairs dealt over the XCDs: 8 lanes, fewer where
         // that would leave XCDs without work
         const int lanes = pairs >= 64 ? 8 : (int)std::min<int64_t>(8, pairs & -pairs);
-        k_kv_tiled<D, BF16><<<(unsigned)(round_up(pairs, lanes) * t.blocks * t.splits), 64 * kTileWaves, 0, s>>>(
-            a, t, (int)pairs, lanes, !t.causal || a.max_q < a.max_kv / 2);
+        const unsigned grid = t.parts > 0 ? (unsigned)t.parts : (unsigned)(round_up(pairs, lanes) * t.blocks);
+        k_kv_tiled<D, BF16><<<grid, 64 * kTileWaves, 0, s>>>(a, t, (int)pairs, lanes,
+                                                                !t.causal || a.max_q < a.max_kv / 2);
     } else {
         const bool wide = t.cols != kKvCols;
         if (t.parts > 0) {
@@ -1145,17 +1225,17 @@ hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipSt
         }
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || (t.splits == 1 && t.parts == 0))
+    if (e != hipSuccess || t.parts == 0)
         return e;
-    const int64_t columns = items * t.used;
-    // lanes for the parts of a column: about as many parts as it can have
-    const int64_t parts = t.parts > 0 ? (int64_t)t.parts / items + 2 : t.splits;
-    if (parts <= 16) {
-        constexpr int per = 256 / (64);
-        k_kv_merge<D, BF16, 64 * 8 / D><<<(unsigned)((columns + per - 1) / per), 256, 0, s>>>(a, t, (int)columns);
-    } else {
-        k_kv_merge<D, BF16, 256 * 8 / D><<<(unsigned)columns, 256, 0, s>>>(a, t, (int)columns);
-    }
+    // about as many lanes as a column can have parts
+    const int each = t.cols == kTileCols ? 16 : 1;
+    const int64_t tasks = items * ((t.used + each - 1) / each);
+    if (t.cols == kTileCols)
+        k_kv_merge<D, BF16, 1, 6><<<(unsigned)((tasks + 3) / 4), 256, 0, s>>>(a, t, (int)items, each);
+    else if (t.parts / items + 2 <= 16)
+        k_kv_merge<D, BF16, 64 * 8 / D, 5><<<(unsigned)((tasks + 3) / 4), 256, 0, s>>>(a, t, (int)items, each);
+    else
+        k_kv_merge<D, BF16, 256 * 8 / D, 5><<<(unsigned)tasks, 256, 0, s>>>(a, t, (int)items, each);
     return hipGetLastError();
 }
 
@@ -1163,58 +1243,58 @@ hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipSt
 
 KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, bool causal, int window)
 {
-    KvPlan p = {LI8_KV_EMPTY, kKvCols, 0, 0, 1, 0, 0};
+    KvPlan p = {LI8_KV_EMPTY, kKvCols, 0, 0, 1, 0};
     const int64_t rows = std::min(b.max_q, b.tokens), group = q_heads / c.heads;
     if (rows == 0 || b.seqs == 0)
         return p;
     const int64_t cols = rows * group;
-    if (cols >= kTileFrom) {
-        p.path = LI8_KV_TILED;
-        p.cols = kTileCols;
-    } else {
-        p.path = LI8_KV_FEW;
-        p.cols = cols > kKvCols ? 2 * kKvCols : kKvCols;
-    }
-    p.blocks = (int)((cols + p.cols - 1) / p.cols);
-    p.used = (int)std::min<int64_t>(p.cols, cols);
-    const int64_t items = plan_items(b, c, p);
     // keys from a span's base to its end at most: a window's keys, the other
     // rows of the block (without `causal` the end is the sequence's, so all
     // rows that follow) and the rounding of the base
-    int64_t span = b.max_kv;
-    if (window > 0)
-        span = std::min<int64_t>(span, (int64_t)window + (causal ? p.cols : rows) + 31);
-    if (p.path == LI8_KV_FEW) {
-        const int64_t steps = (span + 31) / 32;
-        if (steps > kFewWhole && items < 8 * kFewSlots && items * steps < ((int64_t)1 << 31)) {
-            p.parts = (int)std::min<int64_t>(kFewSlots, (items * steps + kFewLeast - 1) / kFewLeast);
-            p.splits = (int)std::min<int64_t>(p.parts, steps);
-        }
-        return p;
+    auto steps_of = [&](int64_t key_step) {
+        int64_t span = b.max_kv;
+        if (window > 0)
+            span = std::min<int64_t>(span, (int64_t)window + (causal ? p.cols : rows) + 31);
+        return (span + key_step - 1) / key_step;
+    };
+    auto items_of = [&]() { return (int64_t)b.seqs * c.heads * ((cols + p.cols - 1) / p.cols); };
+    p.cols = kTileCols;
+    int64_t steps = steps_of(kTileKeys), items = items_of(), slots = kTileSlots;
+    bool whole = items >= slots;
+    if (cols >= kTileColumns && items * steps >= kTileSteps) {
+        p.path = LI8_KV_TILED;
+    } else {
+        p.path = LI8_KV_FEW;
+        p.cols = cols > kKvCols ? 2 * kKvCols : kKvCols;
+        steps = steps_of(32);
+        items = items_of();
+        slots = kFewSlots;
+        whole = steps <= kFewWhole || items >= 8 * slots;
     }
-    const int64_t chunk = std::max(kTileMinSplit, round_up((items * span + kTileTarget - 1) / kTileTarget, kTileKeys));
-    p.chunk = (int)std::min<int64_t>(chunk, INT32_MAX / 2);
-    p.splits = (int)std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk);
+    p.blocks = (int)((cols + p.cols - 1) / p.cols);
+    p.used = (int)std::min<int64_t>(p.cols, cols);
+    if (!whole && items * steps < ((int64_t)1 << 31)) {
+        p.parts = (int)std::min(slots, (items * steps + kLeastSteps - 1) / kLeastSteps);
+        p.splits = (int)std::min<int64_t>(p.parts, steps);
+    }
     return p;
 }
 
 size_t kv_workspace(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads)
 {
+    // The kernel, and with it the columns of a slot, can change with the
+    // window; so the most that either takes: two slots for each workgroup
+    // that shares.
     const KvPlan p = kv_plan(b, c, q_heads, true, 0);
     if (p.path == LI8_KV_EMPTY)
         return 0;
-    const int64_t items = plan_items(b, c, p);
-    // Few columns: two slots for each sharing workgroup, most without a
-    // window.  Tiled: the splits under any window, since a part has at least
-    // kTileMinSplit keys and there are at most kTileTarget / items, rounded up.
-    int64_t slots = 2 * (int64_t)p.parts;
-    if (p.path == LI8_KV_TILED) {
-        const int64_t most = std::min<int64_t>((b.max_kv + kTileMinSplit - 1) / kTileMinSplit, kTileTarget / items + 1);
-        slots = most > 1 ? items * most : 0;
-    }
-    if (slots == 0)
+    const int64_t cols = std::min<int64_t>(kTileCols, (int64_t)std::min(b.max_q, b.tokens) * (q_heads / c.heads));
+    int64_t rows = 2 * (int64_t)p.parts * p.used;
+    if (p.path == LI8_KV_TILED)   // (few columns under a window: at most 32 in each of 512)
+        rows = std::max<int64_t>(p.parts ? 2 * (int64_t)kTileSlots * cols : 0, 2 * (int64_t)kFewSlots * 2 * kKvCols);
+    if (rows == 0)
         return 0;
-    return align_up((size_t)(slots * p.used) * 4 * c.head_dim, 256) + align_up((size_t)(slots * p.used) * 4, 256);
+    return align_up((size_t)rows * 4 * c.head_dim, 256) + align_up((size_t)rows * 4, 256);
 }
 
 hipError_t launch_kv_attention(KvTokens Q, bool bf16, int q_heads, float scale, KvRope rope,
@@ -1225,14 +1305,14 @@ hipError_t launch_kv_attention(KvTokens Q, bool bf16, int q_heads, float scale, 
     const KvPlan p = kv_plan(b, c, q_heads, causal, window);
     const KvArgs a = kv_args(b, c);
     const int64_t items = plan_items(b, c, p);
-    const int64_t slots = p.path == LI8_KV_FEW ? 2 * (int64_t)p.parts : items * p.splits;
+    const int64_t slots = 2 * (int64_t)p.parts;
     AttnArgs t;
     t.Q = Q; t.rope = rope; t.O = O; t.os = os; t.lse = lse;
     t.part_o = reinterpret_cast<float *>(ws);
     t.part_m = reinterpret_cast<float *>(ws + align_up((size_t)(slots * p.used) * 4 * c.head_dim, 256));
     t.scale = scale * kLog2e;
     t.group = q_heads / c.heads; t.inv_group = 1.0f / (float)t.group; t.causal = causal; t.window = window;
-    t.cols = p.cols; t.blocks = p.blocks; t.used = p.used; t.splits = p.splits; t.chunk = p.chunk;
+    t.cols = p.cols; t.blocks = p.blocks; t.used = p.used;
     t.seqs = b.seqs; t.parts = p.parts;
     if (c.head_dim == 128)
         return bf16 ? attention_go<128, true>(a, t, items, s) : attention_go<128, false>(a, t, items, s);

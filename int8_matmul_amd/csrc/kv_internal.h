@@ -35,7 +35,7 @@ __host__ __device__ inline KvSeq kv_sequence(int start, int end, int kv_len, int
 }
 
 // Keys that a block of rows at positions first .. last reaches: [lo, hi).
-// The splits of a block count from lo rounded down to a step of 32 keys.
+// The steps of a block count from base, lo rounded down to 32.
 struct KvSpan {
     int lo, hi, base;
 };
@@ -53,15 +53,14 @@ __host__ __device__ inline KvSpan kv_span(int first, int last, int len, bool cau
 
 constexpr int kKvCols = 16;        // query columns of a few-column workgroup, or twice as many
 
-// Tiled: a block's keys from its span's base on are split in parts of
-// `chunk`.  Few columns: `parts` workgroups share all blocks' keys (0: one
-// workgroup for each block).
+// `parts` workgroups share all blocks' keys (0: one workgroup for each block).
 struct KvPlan {
     int path;       // LI8_KV_*
     int cols;       // query columns of a workgroup
     int blocks;     // column blocks of the longest chunk
     int used;       // columns in use in the fullest block
-    int splits, chunk, parts;
+    int splits;     // most parts of a block
+    int parts;
 };
 KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, bool causal, int window);
 size_t kv_workspace(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads);

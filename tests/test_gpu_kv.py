@@ -1,6 +1,8 @@
 """GPU tests of the int8 key/value cache against the plain forms of
 oracle/kv.py: codes and scales bit for bit, values read back bit for bit,
 attention within a bound derived from what the kernel rounds."""
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -17,6 +19,7 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
 
 
+@functools.lru_cache
 def rope_tables(rows, dims):
     ang = np.arange(rows)[:, None] * (10000.0 ** (-2.0 * np.arange(dims // 2) / dims))
     return np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
@@ -25,15 +28,14 @@ def rope_tables(rows, dims):
 class Setup:
     """A cache with random contents, a table of distinct pages, and a batch."""
 
-    def __init__(self, ns, ls, heads, dim, page, dtype=F16, seed=0, rot=0, inter=False, spare=3, width=None,
-                 max_kv=None, lead=0, tail=0, group=1):
+    def __init__(self, ns, ls, heads, dim, page, dtype=F16, seed=0, rot=0, inter=False, spare=3, max_kv=None, max_q=None, lead=0, tail=0, group=1):
         self.rng = rng = np.random.default_rng(seed)
         self.ns, self.ls, self.heads, self.dim, self.page, self.dtype = ns, ls, heads, dim, page, dtype
         self.group = group
         used = [-(-l // page) for l in ls]
         pages = sum(used) + spare
         order = rng.permutation(pages)
-        self.width = max(max(used), 1) if width is None else width
+        self.width = max(max(used), 1, -(-(max_kv or 0) // page))
         # table entries past a sequence's pages lead nowhere
         self.table = rng.choice([-1, -7, pages, 2**31 - 1], (len(ls), self.width)).astype(np.int32)
         at = 0
@@ -51,7 +53,7 @@ class Setup:
         self.tokens = int(self.q_start[-1]) + tail
         self.max_kv = max(ls) if max_kv is None else max_kv
         self.batch = li8.KVBatch(i32(self.q_start.tolist()), i32(ls), torch.from_numpy(self.table).to(DEV),
-                                 self.tokens, max(ns), self.max_kv)
+                                 self.tokens, max(ns) if max_q is None else max_q, self.max_kv)
         self.rope = self.oracle_rope = None
         if rot:
             c, s = rope_tables(max(self.max_kv, 1), rot)
@@ -250,30 +252,58 @@ def test_attention_shared(ns, ls, heads, group, dim, page, rot, causal, window):
 
 
 TILED = [
-    # ns, ls, heads, group, dim, page, rot, causal, window, split
-    ([64], [64], 1, 1, 128, 16, 128, True, 0, False),
-    ([65, 1, 130], [65, 400, 1000], 2, 1, 64, 16, 64, True, 0, False),
-    ([257, 300], [257, 777], 1, 1, 128, 64, 0, True, 0, False),
-    ([33, 100, 0, 7], [700, 100, 5, 3], 2, 8, 128, 32, 64, True, 0, False),
-    ([100, 64], [900, 64], 1, 3, 64, 128, 64, True, 70, False),
-    ([100, 64], [900, 64], 1, 3, 128, 16, 0, True, 1, False),
-    ([100, 70], [130, 64], 2, 1, 128, 64, 32, False, 0, False),
-    ([90, 200], [900, 210], 1, 2, 64, 32, 0, False, 50, False),
-    ([70, 80], [30, 0], 1, 1, 64, 16, 64, True, 0, False),              # rows before the first token
-    ([70, 80], [30, 0], 1, 1, 128, 16, 0, False, 0, False),
-    ([64, 3], [3000, 2100], 1, 2, 128, 64, 128, True, 0, True),
-    ([20, 30], [5000, 70], 1, 5, 64, 16, 0, True, 0, True),
-    ([64, 100], [2500, 1200], 1, 1, 64, 128, 0, True, 1500, True),
-    ([64, 100], [2500, 1200], 1, 1, 128, 32, 0, False, 1100, True),
-    ([1100], [1100], 1, 1, 64, 64, 0, False, 0, True),
+    # ns, ls, heads, group, dim, page, rot, causal, window
+    ([1], [1], 1, 1, 64, 16, 64, True, 0),
+    ([64], [64], 1, 1, 128, 16, 128, True, 0),
+    ([65, 1, 130], [65, 400, 1000], 2, 1, 64, 16, 64, True, 0),
+    ([257, 300], [257, 777], 1, 1, 128, 64, 0, True, 0),
+    ([33, 100, 0, 7], [500, 100, 5, 3], 2, 8, 128, 32, 64, True, 0),
+    ([100, 64], [900, 64], 1, 3, 64, 128, 64, True, 70),
+    ([100, 64], [900, 64], 1, 3, 128, 16, 0, True, 1),
+    ([100, 70], [130, 64], 2, 1, 128, 64, 32, False, 0),
+    ([90, 200], [900, 210], 1, 2, 64, 32, 0, False, 50),
+    ([70, 80], [30, 0], 1, 1, 64, 16, 64, True, 0),                     # rows before the first token
+    ([70, 80], [30, 0], 1, 1, 128, 16, 0, False, 0),
+    ([64, 3], [3000, 2100], 1, 2, 128, 64, 128, True, 0),
+    ([20, 30], [5000, 70], 1, 5, 64, 16, 0, True, 0),
+    ([64, 100], [2500, 1200], 1, 1, 64, 128, 0, True, 1500),
+    ([64, 100], [2500, 1200], 1, 1, 128, 32, 0, False, 1100),
+    ([1100], [1100], 1, 1, 64, 64, 0, False, 0),
+    ([700, 0, 300], [700, 0, 310], 3, 1, 128, 16, 128, True, 0),        # prompts
+    ([9] * 70, [600 + (61 * i) % 400 for i in range(70)], 1, 8, 64, 16, 0, True, 0),   # past 64 sequences
+    ([150, 9], [90, 1500], 2, 2, 64, 64, 64, True, 0),
 ]
 
 
-@pytest.mark.parametrize("ns, ls, heads, group, dim, page, rot, causal, window, split", TILED)
-def test_attention_tiled(ns, ls, heads, group, dim, page, rot, causal, window, split):
+def tiled_blocks(ns, heads, group, window, shared):
+    """Blocks of each pair of a sequence and a head that the bounds have to allow."""
+    pairs = len(ns) * heads
+    span = min(1 << 14, window + 256 + 31) if window else 1 << 14
+    blocks = max(-(-4096 // (span // 64)), 1 if shared else 256, -(-max(ns) * group // 256) * pairs)
+    return -(-blocks // pairs)
+
+
+# (under a short window as many blocks as the tiled kernel takes go unshared)
+TILED_RUNS = [(*c, shared) for shared in (True, False) for c in TILED
+              if not shared or len(c[0]) * c[2] * tiled_blocks(c[0], c[2], c[3], c[8], True) < 256]
+
+
+@pytest.mark.parametrize("ns, ls, heads, group, dim, page, rot, causal, window, shared", TILED_RUNS)
+def test_attention_tiled(ns, ls, heads, group, dim, page, rot, causal, window, shared):
+    """Small chunks with bounds that call for the tiled kernel: many rows and
+    keys allowed, of which there are few.  It takes 4096 blocks x steps of 64
+    keys, and 256 blocks or more go unshared."""
+    rows = tiled_blocks(ns, heads, group, window, shared) * 256 // group
     for dtype in (F16, BF16):
-        t = Setup(ns, ls, heads, dim, page, dtype, seed=page + group, rot=rot, inter=page == 32, lead=1, tail=2)
-        check_attention(t, heads * group, causal=causal, window=window, expect=("tiled", split), q_scale=2.0)
+        t = Setup(ns, ls, heads, dim, page, dtype, seed=page + group, rot=rot, inter=page == 32, lead=1,
+                  max_kv=1 << 14, max_q=rows, tail=max(0, rows - sum(ns)))
+        check_attention(t, heads * group, causal=causal, window=window, q_scale=2.0, expect=("tiled", shared))
+
+
+def test_attention_tiled_many_blocks():
+    """A prompt with two rounds of blocks for the chip: unshared, longest first."""
+    t = Setup([530], [530], 172, 64, 64)
+    check_attention(t, 172, expect=("tiled", False))
 
 
 @pytest.mark.parametrize("ns, ls, group", [([1, 1], [90, 300], 2), ([1], [3000], 4), ([70, 64], [700, 90], 2)])

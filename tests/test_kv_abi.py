@@ -176,8 +176,10 @@ def test_plan(lib):
     assert plan(lib, batch(max_q=1, seqs=1, max_kv=131072, **wide), c, 64)[0] == 1
     assert plan(lib, batch(max_q=1, seqs=1, max_kv=131072, **wide), c, 64)[1] > 100
     assert plan(lib, batch(max_q=1, seqs=1, max_kv=131072, **wide), c, 64, 1, 256) == (1, 1)
-    assert plan(lib, batch(max_q=512, tokens=512, max_kv=512, **wide), c, 64)[0] == 2
-    assert plan(lib, batch(max_q=512, tokens=4, max_kv=512, **wide), c, 8)[0] == 1   # 4 rows at most
+    assert plan(lib, batch(max_q=512, tokens=512, max_kv=8192, **wide), c, 64) == (2, 1)
+    assert plan(lib, batch(max_q=512, tokens=4, max_kv=8192, **wide), c, 8)[0] == 1     # 4 rows at most
+    assert plan(lib, batch(max_q=64, tokens=512, max_kv=512, **wide), c, 64)[0] == 1    # little work
+    assert plan(lib, batch(max_q=256, tokens=512, seqs=1, max_kv=8192, **wide), c, 64) == (2, 128)
     assert lib.int8_kv_attention_plan(ref(batch()), ref(c), 64, 1, 0, None, None) == INVALID
     # the workspace covers every window and both masks
     for q in (1, 5, 40, 700):
