@@ -142,10 +142,13 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  *           does it see anything) is rotated as position 0
  *   lse     [tokens][q_heads] or NULL
  *   workspace  int8_kv_attention_workspace_bytes(...) bytes; NULL is
- *           accepted where that is 0; its contents do not matter
- * Results do not depend on the other sequences' contents, and repeat bit for
- * bit; they depend on max_q and max_kv through the way a long sequence is
- * split.
+ *           accepted where that is 0; its contents do not matter.  Calls that
+ *           may run at once (two streams, two graphs) need one each.
+ * The same call repeats bit for bit.  A long sequence's keys are divided over
+ * workgroups by the lengths of the whole batch, max_q and max_kv, so a row's
+ * last bits can differ between batches.  Value scales of a sequence and head
+ * more than 2^10 apart cost the pages with the small ones precision: their
+ * probabilities are held in fp16 relative to the largest scale so far.
  */
 size_t int8_kv_attention_workspace_bytes(const li8_kv_batch *batch, const li8_kv_cache *cache,
                                          int32_t q_heads);

@@ -30,6 +30,7 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr float kNone = -1.0e30f;      // a running maximum over nothing yet
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
@@ -100,7 +101,7 @@ __device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int i
 // lengths are: a grid over sequences alone leaves most of the chip to the
 // longest one.  Every workgroup, of the merging kernel too, counts the steps
 // itself, a lane for each of 64 sequences at a time.  (All counts are below
-// 2^31: the host shares no more than that.)
+// 2^30: the host shares no more than that.)
 template <int SHIFT>
 struct Steps {
     KvSeq q;                           // this lane's sequence
@@ -312,7 +313,15 @@ struct Step {
 typedef const int32_t __attribute__((address_space(4))) *kv_const_i32;
 typedef const float __attribute__((address_space(4))) *kv_const_f32;
 
-template <int D>
+template <class T, bool NT>
+__device__ __forceinline__ T load_as(const int8_t *p)
+{
+    if constexpr (NT)
+        return __builtin_nontemporal_load(reinterpret_cast<const T *>(p));
+    return *reinterpret_cast<const T *>(p);
+}
+
+template <int D, bool NT>
 __device__ __forceinline__ void load_step(Step<D> &st, const KvArgs &a, const int (&pid)[2], int h, int t0,
                                           int lo, int te, uint32_t koff, uint32_t voff)
 {
@@ -329,13 +338,16 @@ __device__ __forceinline__ void load_step(Step<D> &st, const KvArgs &a, const in
         const int8_t *vp = a.v + base + voff;
 #pragma unroll
         for (int ks = 0; ks < D / 64; ks++)
-            st.k[tt][ks] = *reinterpret_cast<const v4i *>(kp + 64 * ks);
+            st.k[tt][ks] = load_as<v4i, NT>(kp + 64 * ks);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            if constexpr (D == 128)
-                *reinterpret_cast<uint2 *>(st.v[4 * tt + j]) = *reinterpret_cast<const uint2 *>(vp + j * D);
-            else
-                st.v[4 * tt + j][0] = *reinterpret_cast<const uint32_t *>(vp + j * D);
+            if constexpr (D == 128) {
+                const v2u w = load_as<v2u, NT>(vp + j * D);
+                st.v[4 * tt + j][0] = w.x;
+                st.v[4 * tt + j][D / 64 - 1] = w.y;
+            } else {
+                st.v[4 * tt + j][0] = load_as<uint32_t, NT>(vp + j * D);
+            }
         }
         const float ksc = ((kv_const_f32)(uintptr_t)a.ks)[ph], vsc = ((kv_const_f32)(uintptr_t)a.vs)[ph];
         st.ks[tt] = st.ok[tt] ? ksc : 0.0f;
@@ -351,7 +363,7 @@ __device__ __forceinline__ void load_step(Step<D> &st, const KvArgs &a, const in
 // (4 keys x 4 dims by v_perm), and a step is requested while the one before
 // is computed: the kernel is bound by reading the cache once.
 // ---------------------------------------------------------------------------
-template <int D, bool BF16, int NC, int NW>
+template <int D, bool BF16, int NC, int NW, bool NT>
 __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, const Block &b, int ts, int te,
                                           int64_t slot, char *smem, float *s_f, float *s_m, float *s_l)
 {
@@ -374,7 +386,7 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
         pages(pid, t0);
     split_queries<D, BF16, COLS, 64 * NW, LQ>(a, t, b, smem, s_f, tid, [&]() {
         if (any) {
-            load_step<D>(st[0], a, pid, b.h, t0, b.span.lo, te, koff, voff);
+            load_step<D, NT>(st[0], a, pid, b.h, t0, b.span.lo, te, koff, voff);
             pages(pid, t0 + kStride);
         }
     });
@@ -485,14 +497,14 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
     // (a step past the end is requested all the same, masked, from page 0)
     if (any) {
         while (true) {
-            load_step<D>(st[1], a, pid, b.h, t0 + kStride, b.span.lo, te, koff, voff);
+            load_step<D, NT>(st[1], a, pid, b.h, t0 + kStride, b.span.lo, te, koff, voff);
             pages(pid, t0 + 2 * kStride);
             __builtin_amdgcn_sched_barrier(0);
             compute(st[0], t0);
             t0 += kStride;
             if (t0 >= te)
                 break;
-            load_step<D>(st[0], a, pid, b.h, t0 + kStride, b.span.lo, te, koff, voff);
+            load_step<D, NT>(st[0], a, pid, b.h, t0 + kStride, b.span.lo, te, koff, voff);
             pages(pid, t0 + 2 * kStride);
             __builtin_amdgcn_sched_barrier(0);
             compute(st[1], t0);
@@ -560,7 +572,7 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
     }
 }
 
-template <int D, bool BF16, int NC, int NW>
+template <int D, bool BF16, int NC, int NW, bool NT>
 __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
 {
     constexpr int COLS = kKvCols * NC;
@@ -571,7 +583,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
         // (a prompt's last blocks, which see the most keys, first)
         const int cb = blockIdx.x % t.blocks;
         if (locate(a, t, blockIdx.x - cb + (t.blocks - 1 - cb), COLS, b))
-            few_block<D, BF16, NC, NW>(a, t, b, b.span.base, b.span.hi, -1, smem, s_f, s_m, s_l);
+            few_block<D, BF16, NC, NW, NT>(a, t, b, b.span.base, b.span.hi, -1, smem, s_f, s_m, s_l);
         return;
     }
     const int lane = threadIdx.x & 63;
@@ -583,7 +595,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
         int64_t slot;
         if (run.next(a, t, COLS, lane, b, first, count, slot)) {
             const int ts = b.span.base + 32 * first;
-            few_block<D, BF16, NC, NW>(a, t, b, ts, min(b.span.hi, ts + 32 * count), slot, smem, s_f, s_m, s_l);
+            few_block<D, BF16, NC, NW, NT>(a, t, b, ts, min(b.span.hi, ts + 32 * count), slot, smem, s_f, s_m, s_l);
         }
         __syncthreads();
     }
@@ -1205,23 +1217,25 @@ hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipSt
         k_kv_tiled<D, BF16><<<grid, 64 * kTileWaves, 0, s>>>(a, t, (int)pairs, lanes,
                                                                 !t.causal || a.max_q < a.max_kv / 2);
     } else {
-        const bool wide = t.cols != kKvCols;
+        const bool wide = t.cols != kKvCols, once = t.blocks == 1;
         if (t.parts > 0) {
             const unsigned grid = (unsigned)t.parts;
-            if (wide)
-                k_kv_few<D, BF16, 2, 4><<<grid, 256, 0, s>>>(a, t);
+            if (wide && once)
+                k_kv_few<D, BF16, 2, 4, true><<<grid, 256, 0, s>>>(a, t);
+            else if (wide)
+                k_kv_few<D, BF16, 2, 4, false><<<grid, 256, 0, s>>>(a, t);
             else
-                k_kv_few<D, BF16, 1, 4><<<grid, 256, 0, s>>>(a, t);
+                k_kv_few<D, BF16, 1, 4, true><<<grid, 256, 0, s>>>(a, t);
         } else if (items <= 512) {
             if (wide)
-                k_kv_few<D, BF16, 2, 8><<<(unsigned)items, 512, 0, s>>>(a, t);
+                k_kv_few<D, BF16, 2, 8, false><<<(unsigned)items, 512, 0, s>>>(a, t);
             else
-                k_kv_few<D, BF16, 1, 8><<<(unsigned)items, 512, 0, s>>>(a, t);
+                k_kv_few<D, BF16, 1, 8, false><<<(unsigned)items, 512, 0, s>>>(a, t);
         } else {
             if (wide)
-                k_kv_few<D, BF16, 2, 4><<<(unsigned)items, 256, 0, s>>>(a, t);
+                k_kv_few<D, BF16, 2, 4, false><<<(unsigned)items, 256, 0, s>>>(a, t);
             else
-                k_kv_few<D, BF16, 1, 4><<<(unsigned)items, 256, 0, s>>>(a, t);
+                k_kv_few<D, BF16, 1, 4, false><<<(unsigned)items, 256, 0, s>>>(a, t);
         }
     }
     hipError_t e = hipGetLastError();
@@ -1273,7 +1287,7 @@ KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, bool c
     }
     p.blocks = (int)((cols + p.cols - 1) / p.cols);
     p.used = (int)std::min<int64_t>(p.cols, cols);
-    if (!whole && items * steps < ((int64_t)1 << 31)) {
+    if (!whole && items * steps < ((int64_t)1 << 30)) {
         p.parts = (int)std::min(slots, (items * steps + kLeastSteps - 1) / kLeastSteps);
         p.splits = (int)std::min<int64_t>(p.parts, steps);
     }

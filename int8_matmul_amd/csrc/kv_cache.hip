@@ -14,7 +14,9 @@
 // (lengths, page number, scale and row).
 //
 // Read: one thread per 8 codes, K and V in one launch, 1 byte read and 2
-// written per value.
+// written per value, with non-temporal stores: lines left dirty in the L2 are
+// written back when the kernel ends, and the next one waits for that (four
+// sequences of up to 8191 tokens, 176 MB moved: 41.9 -> 26.9 us, 6.5 TB/s).
 #include <float.h>
 
 #include <algorithm>
@@ -136,6 +138,8 @@ __global__ __launch_bounds__(THREADS) void k_kv_append(KvArgs a, KvTokens K, KvT
     }
 }
 
+typedef uint32_t kv_u4 __attribute__((ext_vector_type(4)));
+
 constexpr int kReadTokens = 64;   // tokens of a read workgroup
 
 template <int D, bool BF16>
@@ -180,7 +184,8 @@ __global__ __launch_bounds__(256) void k_kv_read(KvArgs a, uint16_t *K, int64_t 
 #pragma unroll
         for (int e = 0; e < 8; e++)
             x[e] = byte_value(e < 4 ? w[k].x : w[k].y, e & 3) * f[k];
-        *reinterpret_cast<uint4 *>(out + (q.q0 + i) * stride) = pack8<BF16>(x);
+        const uint4 r = pack8<BF16>(x);
+        __builtin_nontemporal_store(kv_u4{r.x, r.y, r.z, r.w}, reinterpret_cast<kv_u4 *>(out + (q.q0 + i) * stride));
     }
 }
 
