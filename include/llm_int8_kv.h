@@ -135,9 +135,9 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  * the matrix units: q as 15-bit integers of its row's largest magnitude
  * (two int8 parts) times the key codes, exact in int32; the softmax in fp32;
  * the probabilities rounded to fp16 times the value codes, summed in fp32.
- *   scale   >= 0 and finite
+ *   scale   >= 0 and finite, and such that no |z| reaches 10^29
  *   Q, O    [tokens][q_heads][head_dim], rows q_stride, o_stride apart;
- *           O must not alias Q
+ *           O must not alias Q (O == Q is refused)
  *   rope    as for the keys; a negative position (only without `causal`
  *           does it see anything) is rotated as position 0
  *   lse     [tokens][q_heads] or NULL
@@ -149,6 +149,7 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  * last bits can differ between batches.  Value scales of a sequence and head
  * more than 2^10 apart cost the pages with the small ones precision: their
  * probabilities are held in fp16 relative to the largest scale so far.
+ * Value scales below 2^-126 count as 0.
  */
 size_t int8_kv_attention_workspace_bytes(const li8_kv_batch *batch, const li8_kv_cache *cache,
                                          int32_t q_heads);

@@ -195,6 +195,8 @@ li8_status int8_kv_attention(const void *Q, int64_t q_stride, li8_dtype dtype, i
     LI8_TRY(check_pointers(batch, cache));
     LI8_TRY(check_tokens(Q, q_stride, q_heads, cache->head_dim));
     LI8_TRY(check_tokens(O, o_stride, q_heads, cache->head_dim));
+    if (O == Q)   // (workgroups that share a row's keys read its query at different times)
+        return LI8_ERR_INVALID_ARG;
     if (off_by(lse, 4) || off_by(workspace, 16))
         return LI8_ERR_ALIGN;
     const size_t need = kv_workspace(*batch, *cache, q_heads);

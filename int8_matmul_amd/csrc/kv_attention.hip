@@ -430,7 +430,8 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
                     acc[c][n] *= al;
             vref = vm;
         }
-        const float vi = vref > 0.0f ? __builtin_amdgcn_rcpf(vref) : 0.0f;
+        // (below the normal range the reciprocal is infinite: such scales count as 0)
+        const float vi = vref >= FLT_MIN ? __builtin_amdgcn_rcpf(vref) : 0.0f;
         const float r[2] = {w.vs[0] * vi, w.vs[1] * vi};
         v8h p[NC];
 #pragma unroll
@@ -665,7 +666,7 @@ __device__ __forceinline__ void tile_block(const KvArgs &a, const AttnArgs &t, c
     __syncthreads();
 
     // keys this lane's column sees, [clo, chi), and what all columns of the
-    // wave see, [wlo, whi), or any of them, [ulo, uhi)
+    // wave see, [wlo, whi), or any of them (seen)
     int gcol, gdrop;
     const int pos = b.q.begin + b.row_of(qcol, t, gcol);
     int chi = t.causal ? min(te, pos + 1) : te;
@@ -1287,7 +1288,9 @@ KvPlan kv_plan(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads, bool c
     }
     p.blocks = (int)((cols + p.cols - 1) / p.cols);
     p.used = (int)std::min<int64_t>(p.cols, cols);
-    if (!whole && items * steps < ((int64_t)1 << 30)) {
+    // (counted as without a window, so that what is shared, and with it the
+    // workspace, does not depend on it)
+    if (!whole && items * (((int64_t)b.max_kv + 31) / 32) < ((int64_t)1 << 30)) {
         p.parts = (int)std::min(slots, (items * steps + kLeastSteps - 1) / kLeastSteps);
         p.splits = (int)std::min<int64_t>(p.parts, steps);
     }

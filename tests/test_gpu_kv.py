@@ -300,6 +300,54 @@ def test_attention_tiled(ns, ls, heads, group, dim, page, rot, causal, window, s
         check_attention(t, heads * group, causal=causal, window=window, q_scale=2.0, expect=("tiled", shared))
 
 
+def tiled_setup(ns, ls, heads, group, dim, shared, dtype=F16):
+    rows = tiled_blocks(ns, heads, group, 0, shared) * 256 // group
+    return Setup(ns, ls, heads, dim, 16, dtype, max_kv=1 << 14, max_q=rows, tail=max(0, rows - sum(ns)))
+
+
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_tiled_extremes(dim, shared):
+    """The tiled kernel: peaked scores, a zero query, scale 0, zero scales,
+    page numbers that do not exist, no page at all."""
+    t = tiled_setup([70, 64], [700, 90], 1, 2, dim, shared)
+    expect = ("tiled", shared)
+    check_attention(t, 2, q_scale=30.0, scale=0.2, expect=expect)
+    check_attention(t, 2, q_scale=0.0, expect=expect)
+    check_attention(t, 2, scale=0.0, expect=expect)
+    for c, r in ((t.cache.k_scale, t.ref.ks), (t.cache.v_scale, t.ref.vs)):
+        c[t.table[0, 1]] = 0.0
+        r[t.table[0, 1]] = 0.0
+    check_attention(t, 2, expect=expect)
+    for s, b, bad in ((0, 1, -1), (0, 2, t.ref.pages), (1, 0, 2**31 - 1), (1, 2, -2**31), (1, 5, -5)):
+        t.table[s, b] = bad
+    t.batch.table.copy_(torch.from_numpy(t.table))
+    check_attention(t, 2, expect=expect)
+    t.cache.v_scale.zero_()
+    t.ref.vs[:] = 0
+    assert not check_attention(t, 2, expect=expect)[:134].any()
+    t.table[:] = -1
+    t.batch.table.fill_(-1)
+    assert not check_attention(t, 2, expect=expect)[:134].any()
+
+
+@pytest.mark.parametrize("case", ["few", "few shared", "tiled"])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_least_value_scales(case, dtype):
+    """Value scales below fp32's normal range count as 0: what they would give,
+    at most 127 * 2^-126, is below the tolerance's absolute part."""
+    if case == "tiled":
+        t = tiled_setup([70, 64], [700, 90], 1, 2, 64, False, dtype)
+    else:
+        t = Setup([1, 1], [90, 300] if case == "few" else [3000, 1500], 1, 64, 16, dtype)
+    for first, least in ((1, 1.0e-39), (0, 1.0e-45)):
+        for s in range(2):                                # one page of each sequence, then all
+            at = t.table[s, first:first + 1] if first else t.table[s, :-(-t.ls[s] // 16)]
+            t.cache.v_scale[torch.from_numpy(at.astype(np.int64)).to(DEV)] = least
+            t.ref.vs[at] = np.float32(least)
+        check_attention(t, 2, expect=(case.split()[0], case == "few shared"))
+
+
 def test_attention_tiled_many_blocks():
     """A prompt with two rounds of blocks for the chip: unshared, longest first."""
     t = Setup([530], [530], 172, 64, 64)

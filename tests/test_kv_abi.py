@@ -151,6 +151,11 @@ def test_bad_attention(lib):
     assert attend(lib, b=b, wsb=need - 1) == WORKSPACE
 
 
+def test_output_over_the_queries(lib):
+    """Workgroups that share a row's keys read its query at different times."""
+    assert attend(lib, Q=P, O=P) == INVALID
+
+
 def test_empty_calls(lib):
     for kw in (dict(seqs=0), dict(tokens=0), dict(max_q=0)):
         b = batch(**kw, q_start=None, kv_len=None, table=None)
@@ -191,6 +196,24 @@ def test_plan(lib):
                     for causal in (0, 1):
                         if plan(lib, b, c, 64, causal, w)[1] > 1:
                             assert need > 0, (q, kv, s, w, causal)
+
+
+def test_workspace_of_the_largest_batches(lib):
+    """Past 2^30 steps nothing is shared, under a window neither: the
+    workspace is asked for without one."""
+    wide = dict(table_width=1 << 20, table_stride=1 << 20)
+    for heads, rows, seqs, kv in ((4, 1, 512, 1 << 24), (4, 4, 512, 1 << 24), (4, 128, 32, 1 << 30),
+                                  (4, 128, 16, 1 << 26), (8, 300, 2, 1 << 30)):
+        c = cache(heads=heads, head_dim=128, page_size=128, pages=1 << 30)
+        b = batch(max_q=rows, tokens=rows * seqs, seqs=seqs, max_kv=kv, **{**wide, "table_width": kv // 128,
+                                                                           "table_stride": kv // 128})
+        need = lib.int8_kv_attention_workspace_bytes(ref(b), ref(c), heads)
+        for w in (0, 1, 4096, 1 << 20, 1 << 28):
+            for causal in (0, 1):
+                path, splits = plan(lib, b, c, heads, causal, w)
+                # two slots of fp32 rows and a number for each workgroup that shares
+                slots = 2 * 256 * min(rows, 256) if path == 2 else 2 * min(rows, 16)
+                assert splits == 1 or need >= slots * (4 * 128 + 4), (heads, rows, seqs, kv, w, causal)
 
 
 def test_index_arithmetic(tmp_path):
