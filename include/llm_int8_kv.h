@@ -134,7 +134,8 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  * A row that sees nothing gets O = 0 and lse = -inf.  The products run on
  * the matrix units: q as 15-bit integers of its row's largest magnitude
  * (two int8 parts) times the key codes, exact in int32; the softmax in fp32;
- * the probabilities rounded to fp16 times the value codes, summed in fp32.
+ * the probabilities rounded to fp16 (in some kernels in two parts) times the
+ * value codes, summed in fp32.
  *   scale   >= 0 and finite, and such that no |z| reaches 10^29
  *   Q, O    [tokens][q_heads][head_dim], rows q_stride, o_stride apart;
  *           O must not alias Q (O == Q is refused)

@@ -9,7 +9,8 @@
 //                            15-bit integer of its row's largest magnitude,
 //                            q = f (128 qh + ql); the sums are exact
 //   O^T[d, col]  += V^T P^T  fp16 MFMA: the codes are exact in fp16, the
-//                            probabilities are rounded to it (11 bits)
+//                            probabilities are rounded to it (11 bits, or
+//                            22 in two parts)
 // The transposed form leaves a column in the lanes that hold it as the next
 // product's operand: with the keys of a step of 32 numbered so that lane
 // group g has keys 4g..4g+3 and 16+4g..16+4g+3, the scores' accumulator
@@ -369,6 +370,15 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
 {
     constexpr int CPR = D / 8, NB = D / 16, KS = D / 64, LQ = D + 16, LO = D + 4, COLS = kKvCols * NC;
     constexpr int kStride = 32 * NW;
+    // fp16 outputs: the probabilities in two parts, 22 bits, so that only the
+    // output's own rounding shows (error 2.2e-4 of the output's norm against
+    // 2.9e-4, 2.1e-4 of it from that rounding).  One token of 40 heads x 16
+    // sequences takes 89.3 us either way, as reading the cache hides the
+    // second product; one token of 32 heads over 1000 keys 11.9 against 11.3.
+    // With 32 columns a workgroup is bound by its instructions (a prompt of
+    // 1024 tokens 47 us against 41), and bf16 outputs are rounded 8 times as
+    // coarsely: one part.
+    constexpr bool TWO = !BF16 && NC == 1;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const kv_const_i32 table = (kv_const_i32)(uintptr_t)(a.table + (int64_t)b.s * a.table_stride);
@@ -433,7 +443,7 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
         // (below the normal range the reciprocal is infinite: such scales count as 0)
         const float vi = vref >= FLT_MIN ? __builtin_amdgcn_rcpf(vref) : 0.0f;
         const float r[2] = {w.vs[0] * vi, w.vs[1] * vi};
-        v8h p[NC];
+        v8h p[NC], rest[TWO ? NC : 1];
 #pragma unroll
         for (int c = 0; c < NC; c++) {
             float z[8], zm = -INFINITY;
@@ -471,7 +481,10 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
             for (int e = 0; e < 8; e++) {
                 const float pe = __builtin_amdgcn_exp2f(z[e] - m[c]);
                 l[c] += pe;
-                p[c][e] = (_Float16)(pe * r[e >> 2]);
+                const float w = pe * r[e >> 2];
+                p[c][e] = (_Float16)w;
+                if constexpr (TWO)
+                    rest[c][e] = (_Float16)(w - (float)p[c][e]);
             }
         }
         // Lane (col, g) has the bytes col NB .. col NB + NB - 1 of its 8 keys:
@@ -488,10 +501,16 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
             }
 #pragma unroll
             for (int c = 0; c < NC; c++) {
-                acc[c][4 * d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x0), p[c], acc[c][4 * d], 0, 0, 0);
-                acc[c][4 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x1), p[c], acc[c][4 * d + 1], 0, 0, 0);
-                acc[c][4 * d + 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x2), p[c], acc[c][4 * d + 2], 0, 0, 0);
-                acc[c][4 * d + 3] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x3), p[c], acc[c][4 * d + 3], 0, 0, 0);
+                const v8h x[4] = {__builtin_bit_cast(v8h, x0), __builtin_bit_cast(v8h, x1),
+                                  __builtin_bit_cast(v8h, x2), __builtin_bit_cast(v8h, x3)};
+#pragma unroll
+                for (int n = 0; n < 4; n++)
+                    acc[c][4 * d + n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[n], p[c], acc[c][4 * d + n], 0, 0, 0);
+                if constexpr (TWO) {
+#pragma unroll
+                    for (int n = 0; n < 4; n++)
+                        acc[c][4 * d + n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[n], rest[c], acc[c][4 * d + n], 0, 0, 0);
+                }
             }
         }
     };
