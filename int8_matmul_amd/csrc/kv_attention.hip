@@ -96,9 +96,9 @@ __device__ __forceinline__ bool locate(const KvArgs &a, const AttnArgs &t, int i
     return place(t, kv_sequence_of(a, s), s, sh % a.heads, cb, cols, b);
 }
 
-// The work in steps of 2^SHIFT keys, one sequence after another, and within it head after head and block after block, each with
-// the sequence's largest number of steps (at least one, so that an empty row
-// is written).  `parts` workgroups take equal runs of steps, whatever the
+// The work in steps of 2^SHIFT keys, one sequence after another, and within it
+// head after head and block after block, each with the sequence's largest
+// number of steps (at least one, so that an empty row is written).  `parts` workgroups take equal runs of steps, whatever the
 // lengths are: a grid over sequences alone leaves most of the chip to the
 // longest one.  Every workgroup, of the merging kernel too, counts the steps
 // itself, a lane for each of 64 sequences at a time.  (All counts are below
@@ -357,12 +357,17 @@ __device__ __forceinline__ void load_step(Step<D> &st, const KvArgs &a, const in
 }
 
 // ---------------------------------------------------------------------------
-// Few columns: 16 NC columns of one (sequence, head) and one split of its
-// keys per workgroup; the 4 waves take the steps of 32 keys in turn and keep
-// their own maximum, sum and O^T, merged through LDS at the end.  K and V go
-// from memory into the MFMA operands' registers, V through a byte transpose
-// (4 keys x 4 dims by v_perm), and a step is requested while the one before
-// is computed: the kernel is bound by reading the cache once.
+// Few columns: 16 NC columns of one (sequence, head) and a run of its keys per
+// workgroup; the NW waves take the steps of 32 keys in turn and keep their own
+// maximum, sum and O^T, merged through LDS at the end.  K and V go from memory
+// into the MFMA operands' registers, V through a byte transpose (4 keys x 4
+// dims by v_perm), and a step is requested while the one before is computed
+// (two and three steps ahead were slower: registers, and no fewer waits).
+// Bound by reading the cache once: 64 sequences of up to 8192 tokens, 8 heads
+// of a group of 8, one token each, 701 MB: 127 us with the merge, 5.5 TB/s (a
+// copy of 2 GiB moves 4.8); one sequence of 131071 tokens, 268 MB: 51 us.
+// Short calls are bound by the chain of loads (lengths, page number, step) and
+// the launch: one token of 32 heads over 777 keys 11.9 us.
 // ---------------------------------------------------------------------------
 template <int D, bool BF16, int NC, int NW, bool NT>
 __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, const Block &b, int ts, int te,
@@ -626,6 +631,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
 // its keys in steps of 64 that all waves read from LDS.  K stays int8 there
 // (16 MFMAs 32x32x32 i8 per step and wave for the two query parts), V is
 // turned into fp16 and transposed on its way in, once for all waves.
+// A prompt of 4096 tokens, 32 heads, D = 128: 165 us, 830 TFLOP/s by the
+// formula's products; a chunk of 512 tokens in each of 4 sequences of 8192,
+// 8 heads of a group of 8: 548 us, 1000 TFLOP/s.  (Boards differ: 190 us and
+// 660 us on one that held a lower clock.)  The matrix units are busy for a
+// third of the time and the vector ALUs for half of it; with the exponentials
+// left out, or the staging, or the reads of LDS, or the second product, the
+// time falls by 10 to 16 % each, so no one of them alone is the bound.
 // ---------------------------------------------------------------------------
 constexpr int kTileWaves = 8;
 constexpr int kTileCols = 32 * kTileWaves;
@@ -693,7 +705,8 @@ __device__ __forceinline__ void tile_block(const KvArgs &a, const AttnArgs &t, c
     if (qcol >= b.nc)
         chi = clo = 0;
     const int c_first = 32 * wid, c_last = min(32 * wid + 31, b.nc - 1);
-    const int p_first = b.q.begin + b.row_of(c_first, t, gdrop), p_last = b.q.begin + b.row_of(max(c_last, 0), t, gdrop);
+    const int p_first = b.q.begin + b.row_of(c_first, t, gdrop);
+    const int p_last = b.q.begin + b.row_of(max(c_last, 0), t, gdrop);
     const KvSpan seen = kv_span(p_first, p_last, te, t.causal != 0, t.window);
     const bool idle = c_first >= b.nc;
     const int whi = c_last < 32 * wid + 31 ? 0 : t.causal ? min(te, p_first + 1) : te;
@@ -770,7 +783,7 @@ __device__ __forceinline__ void tile_block(const KvArgs &a, const AttnArgs &t, c
     // probabilities are taken against the last one, and only when their sum
     // shows one that fp16 may not hold (Y's last line) is the maximum moved
     // and the subtile's probabilities taken again, which is rare after the
-    // first.  PREFILL
+    // first (171 us against 178 for a 4096-token prompt with 32 heads).
     v16f acc[DB] = {};
     v16i si;
     float x[16];
@@ -1165,7 +1178,9 @@ __device__ __forceinline__ void merge_column(const KvArgs &a, const AttnArgs &t,
 // m_i the part's log2 of its sum.  SL lanes of parts x D/8 chunks work on a
 // column: with many parts the workgroup, else a wave, or (SL = 1, where blocks
 // are wide and in few parts) D/8 lanes of it.  A wave has `each` columns of
-// one block; four parts are in flight per lane.
+// one block; four parts are in flight per lane.  64 sequences' one token each
+// (512 blocks of 8 columns, up to 4 parts) takes 7.8 us, 8 blocks of 64 parts
+// 4.9: the launch and two chains of loads, lengths and then parts.
 template <int D, bool BF16, int SL, int SHIFT>
 __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int items, int each)
 {
@@ -1208,10 +1223,13 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int item
 //   127 : 97; 8 tokens x 8 heads of a group, 64 columns, in 16 sequences of
 //   up to 4096 keys 52 : 69, twice as many 83 : 72.
 //   few columns are shared past 40 steps of 32 keys: at 25 steps one launch
-//   took 11.1 against 13.5, at 41 to 4096 sharing is up to 4 times as fast.
+//   took 11.3 against 18.3, at 41 to 4096 sharing is up to 4 times as fast.
 //   tiled blocks are shared where there are fewer than CUs: 64 blocks of 128
 //   steps 97 against 242 unshared, 256 blocks of a 2048-token prompt 77
 //   against 72 (their keys differ, which the count of steps does not know).
+//   Chunks over long sequences shared from 256 blocks on, 380 and 500 blocks
+//   of up to 128 steps: 415 against 409, 491 against 571; the host does not
+//   see which.
 constexpr int kTileColumns = 128;
 constexpr int kTileSteps = 4096;
 constexpr int kFewWhole = 40;
