@@ -217,18 +217,70 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
     return ab | cd;
 }
 
-// One row's 8 query values (a chunk of D) as two int8 parts; f is the
-// factor of the row's integers, without the softmax scale.  The lanes of a
-// row are D/8 neighbours.
-template <int D>
-__device__ __forceinline__ void split_query(const float x[8], uint2 &hi, uint2 &lo, float &f)
+// Two chunks of 8 values of a row and what their rotation takes.  Rotated by
+// halves a lane has both values of its pairs, so that the tables' numbers and
+// the partners are loaded once; else the chunks are neighbours.
+struct RowPair {
+    uint4 x[2];
+    float4 c[2], s[2];
+};
+
+// The chunks of lane l.
+template <int ROT>
+__device__ __forceinline__ void pair_chunks(int l, const KvRope &r, int (&c)[2])
+{
+    const int hc = r.half >> 3;
+    const bool turned = ROT == ROT_HALVES && l < hc;
+    c[0] = turned ? l : 2 * l;
+    c[1] = turned ? l + hc : 2 * l + 1;
+}
+
+template <int ROT>
+__device__ __forceinline__ void fetch_pair(RowPair &w, const uint16_t *row, int l, const int (&c)[2], const KvRope &r,
+                                           int pos)
+{
+    w.x[0] = load_u4(row + 8 * c[0]);
+    w.x[1] = load_u4(row + 8 * c[1]);
+    if constexpr (ROT != ROT_NONE) {   // (a chunk past the rotated values: the row's first numbers)
+        const int64_t t = (int64_t)pos * r.half + (8 * l < r.half ? 8 * l : 0);
+        const float4 *pc = reinterpret_cast<const float4 *>(r.cos + t);
+        const float4 *ps = reinterpret_cast<const float4 *>(r.sin + t);
+        w.c[0] = pc[0]; w.c[1] = pc[1];
+        w.s[0] = ps[0]; w.s[1] = ps[1];
+    }
+}
+
+// The rotated values; each product and sum is rounded by itself, as the keys' are.
+template <bool BF16, int ROT>
+__device__ __forceinline__ void rotate_pair(const RowPair &w, int l, const KvRope &r, float (&x)[16])
+{
+    unpack8<BF16>(w.x[0], x);
+    unpack8<BF16>(w.x[1], x + 8);
+    if constexpr (ROT != ROT_NONE) {
+        const bool turned = 8 * l < r.half;
+        const float cv[8] = {w.c[0].x, w.c[0].y, w.c[0].z, w.c[0].w, w.c[1].x, w.c[1].y, w.c[1].z, w.c[1].w};
+        const float sv[8] = {w.s[0].x, w.s[0].y, w.s[0].z, w.s[0].w, w.s[1].x, w.s[1].y, w.s[1].z, w.s[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            float &a = x[ROT == ROT_HALVES ? i : 2 * i], &b = x[ROT == ROT_HALVES ? 8 + i : 2 * i + 1];
+            const float za = a * cv[i] - b * sv[i], zb = b * cv[i] + a * sv[i];
+            a = turned ? za : a;
+            b = turned ? zb : b;
+        }
+    }
+}
+
+// N query values of a row as two int8 parts; f is the factor of the row's
+// integers, without the softmax scale.  LANES neighbours have a row.
+template <int LANES, int N>
+__device__ __forceinline__ void split_query(const float (&x)[N], uint2 (&hi)[N / 8], uint2 (&lo)[N / 8], float &f)
 {
     float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; e++)
+    for (int e = 0; e < N; e++)
         m = fmaxf(m, fabsf(x[e]));
 #pragma unroll
-    for (int o = 1; o < D / 8; o <<= 1)
+    for (int o = 1; o < LANES; o <<= 1)
         m = fmaxf(m, __shfl_xor(m, o, 64));
     // x inv in [-16256, 16256] plus 1.5 2^23 is rounded half to even to an
     // integer n in the low bits: n = 128 qh + ql, qh = n >> 7 in -127 .. 127,
@@ -236,56 +288,73 @@ __device__ __forceinline__ void split_query(const float x[8], uint2 &hi, uint2 &
     // holds, which only makes n smaller.)
     const float inv = m > 0.0f ? fminf(kQMax * __builtin_amdgcn_rcpf(m), FLT_MAX) : 0.0f;
     f = inv > 0.0f ? 1.0f / inv : 0.0f;
-    uint32_t b[8];
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-        b[e] = __builtin_bit_cast(uint32_t, fmaf(x[e], inv, 12582912.0f));
-    lo = make_uint2(low_bytes(b[0], b[1], b[2], b[3]) & 0x7f7f7f7fu, low_bytes(b[4], b[5], b[6], b[7]) & 0x7f7f7f7fu);
+    for (int k = 0; k < N / 8; k++) {
+        uint32_t b[8];
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-        b[e] >>= 7;
-    hi = make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
+        for (int e = 0; e < 8; e++)
+            b[e] = __builtin_bit_cast(uint32_t, fmaf(x[8 * k + e], inv, 12582912.0f));
+        lo[k] = make_uint2(low_bytes(b[0], b[1], b[2], b[3]) & 0x7f7f7f7fu,
+                           low_bytes(b[4], b[5], b[6], b[7]) & 0x7f7f7f7fu);
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            b[e] >>= 7;
+        hi[k] = make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
+    }
 }
 
 // The block's query columns into LDS, COLS rows of LQ bytes with the first
 // parts and as many with the second, and their factors.  between() runs once
-// the first rows have been requested.
-template <int D, bool BF16, int COLS, int NT, int LQ, class Between>
+// the rows have been requested.  PAIR: two chunks per lane, which take half
+// the loads of a rotation (256 columns: 8.7 us with one chunk, a 4096-token
+// prompt 168 -> 163 us); with few columns one, as half the lanes would idle
+// (64 sequences' one token each 126 against 128 us).
+template <int D, bool BF16, int COLS, int NT, int LQ, bool PAIR, class Between>
 __device__ __forceinline__ void split_queries(const KvArgs &a, const AttnArgs &t, const Block &b, char *lds,
                                               float *factor, int tid, Between between)
 {
-    constexpr int CPR = D / 8, PASSES = COLS * CPR / NT > 0 ? COLS * CPR / NT : 1;
-    constexpr int BATCH = PASSES < 4 ? PASSES : 4;   // rows of a thread in flight
-    const int cc = tid % CPR;
+    constexpr int N = PAIR ? 16 : 8, LPR = D / N;   // values of a lane, lanes of a row
+    constexpr int PASSES = COLS * LPR / NT > 0 ? COLS * LPR / NT : 1;
+    static_assert(PASSES <= 4, "rows in flight");
+    const int l = tid % LPR;
     with_rotation(t.rope, [&](auto rot) {
         constexpr int ROT = decltype(rot)::value;
+        int c[2] = {l, l};
+        if constexpr (PAIR)
+            pair_chunks<ROT>(l, t.rope, c);
+        std::conditional_t<PAIR, RowPair, RowChunk> w[PASSES];
 #pragma unroll
-        for (int k0 = 0; k0 < PASSES; k0 += BATCH) {
-            RowChunk w[BATCH];
+        for (int k = 0; k < PASSES; k++) {
+            int g;   // (columns past the last: the last one again)
+            const int qc = min(tid / LPR + k * (NT / LPR), b.nc - 1);
+            const int i = b.row_of(qc, t, g), pos = max(b.q.begin + i, 0);
+            const uint16_t *row =
+                t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D;
+            if constexpr (PAIR)
+                fetch_pair<ROT>(w[k], row, l, c, t.rope, pos);
+            else
+                fetch_row<ROT>(w[k], row, l, t.rope, pos);
+        }
+        between();
 #pragma unroll
-            for (int k = 0; k < BATCH; k++) {
-                int g;   // (columns past the last: the last one again)
-                const int qc = min(tid / CPR + (k0 + k) * (NT / CPR), b.nc - 1);
-                const int i = b.row_of(qc, t, g);
-                fetch_row<ROT>(w[k], t.Q.p + (int64_t)(b.q.q0 + i) * t.Q.stride + (int64_t)(b.h * t.group + g) * D,
-                               cc, t.rope, max(b.q.begin + i, 0));
+        for (int k = 0; k < PASSES; k++) {
+            const int qc = tid / LPR + k * (NT / LPR);
+            float x[N], f;
+            uint2 hi[N / 8], lo[N / 8];
+            if constexpr (PAIR)
+                rotate_pair<BF16, ROT>(w[k], l, t.rope, x);
+            else
+                rotate_row<BF16, ROT>(w[k], l, t.rope, x);
+            split_query<LPR, N>(x, hi, lo, f);
+            if (COLS * LPR < NT && qc >= COLS)
+                continue;
+#pragma unroll
+            for (int j = 0; j < N / 8; j++) {
+                *reinterpret_cast<uint2 *>(lds + qc * LQ + 8 * c[j]) = hi[j];
+                *reinterpret_cast<uint2 *>(lds + (COLS + qc) * LQ + 8 * c[j]) = lo[j];
             }
-            if (k0 == 0)
-                between();
-#pragma unroll
-            for (int k = 0; k < BATCH; k++) {
-                const int qc = tid / CPR + (k0 + k) * (NT / CPR);
-                float x[8], f;
-                uint2 hi, lo;
-                rotate_row<BF16, ROT>(w[k], cc, t.rope, x);
-                split_query<D>(x, hi, lo, f);
-                if (COLS * CPR < NT && qc >= COLS)
-                    continue;
-                *reinterpret_cast<uint2 *>(lds + qc * LQ + 8 * cc) = hi;
-                *reinterpret_cast<uint2 *>(lds + (COLS + qc) * LQ + 8 * cc) = lo;
-                if (cc == 0)
-                    factor[qc] = f * t.scale;
-            }
+            if (l == 0)
+                factor[qc] = f * t.scale;
         }
     });
 }
@@ -399,7 +468,7 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
     // the queries and the first step's data are requested together
     if (any)
         pages(pid, t0);
-    split_queries<D, BF16, COLS, 64 * NW, LQ>(a, t, b, smem, s_f, tid, [&]() {
+    split_queries<D, BF16, COLS, 64 * NW, LQ, false>(a, t, b, smem, s_f, tid, [&]() {
         if (any) {
             load_step<D, NT>(st[0], a, pid, b.h, t0, b.span.lo, te, koff, voff);
             pages(pid, t0 + kStride);
@@ -631,10 +700,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
 // its keys in steps of 64 that all waves read from LDS.  K stays int8 there
 // (16 MFMAs 32x32x32 i8 per step and wave for the two query parts), V is
 // turned into fp16 and transposed on its way in, once for all waves.
-// A prompt of 4096 tokens, 32 heads, D = 128: 165 us, 830 TFLOP/s by the
+// A prompt of 4096 tokens, 32 heads, D = 128: 163 us, 843 TFLOP/s by the
 // formula's products; a chunk of 512 tokens in each of 4 sequences of 8192,
-// 8 heads of a group of 8: 548 us, 1000 TFLOP/s.  (Boards differ: 190 us and
-// 660 us on one that held a lower clock.)  The matrix units are busy for a
+// 8 heads of a group of 8: 548 us, 1000 TFLOP/s.  (In bursts of 8 calls, while
+// the clock ramps up, 185 and 670 us.)  The matrix units are busy for a
 // third of the time and the vector ALUs for half of it; with the exponentials
 // left out, or the staging, or the reads of LDS, or the second product, the
 // time falls by 10 to 16 % each, so no one of them alone is the bound.
@@ -684,7 +753,7 @@ __device__ __forceinline__ void tile_block(const KvArgs &a, const AttnArgs &t, c
     asm volatile("" : "+v"(tid));
     const int lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    split_queries<D, BF16, kTileCols, NT, L::q_row>(a, t, b, smem, s_f, tid, []() {});
+    split_queries<D, BF16, kTileCols, NT, L::q_row, true>(a, t, b, smem, s_f, tid, []() {});
     __syncthreads();
     const int col = lane & 31, half = lane >> 5, qcol = 32 * wid + col;
     v4i qh[KS], ql[KS];
