@@ -701,7 +701,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
 // (16 MFMAs 32x32x32 i8 per step and wave for the two query parts), V is
 // turned into fp16 and transposed on its way in, once for all waves.
 // A prompt of 4096 tokens, 32 heads, D = 128: 163 us, 843 TFLOP/s by the
-// formula's products; a chunk of 512 tokens in each of 4 sequences of 8192,
+// formula's products (158 to 167 on four boards); a chunk of 512 tokens in each of 4 sequences of 8192,
 // 8 heads of a group of 8: 548 us, 1000 TFLOP/s.  (In bursts of 8 calls, while
 // the clock ramps up, 185 and 670 us.)  The matrix units are busy for a
 // third of the time and the vector ALUs for half of it; with the exponentials
@@ -719,14 +719,15 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 
 // 16-byte chunks of the LDS tiles are permuted within 128 bytes so that
-// neither the fragment reads (32 rows, one chunk each) nor the writes of V
-// (rows 4 apart) meet in a bank.
+// neither the fragment reads (one chunk of 16 rows at a time) nor the writes
+// of V (rows 4 apart) meet in a bank: a ninth of the LDS's busy cycles are
+// conflicts (a quarter with row & 7 for K: 0.6 % more time).
 template <int D>
 __device__ __forceinline__ int k_place(int row, int chunk)
 {
     if constexpr (D == 128)
-        return row * 128 + 16 * (chunk ^ (row & 7));
-    return row * 64 + 16 * (chunk ^ ((row >> 1) & 3));
+        return row * 128 + 16 * (chunk ^ ((row ^ ((row >> 3) & 1)) & 7));
+    return row * 64 + 16 * (chunk ^ (((row >> 1) ^ (row >> 3)) & 3));
 }
 
 __device__ __forceinline__ int v_place(int d, int chunk) { return d * 128 + 16 * (chunk ^ ((d ^ (d >> 3)) & 7)); }
