@@ -700,13 +700,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
 // its keys in steps of 64 that all waves read from LDS.  K stays int8 there
 // (16 MFMAs 32x32x32 i8 per step and wave for the two query parts), V is
 // turned into fp16 and transposed on its way in, once for all waves.
-// A prompt of 4096 tokens, 32 heads, D = 128: 163 us, 843 TFLOP/s by the
-// formula's products (158 to 167 on four boards); a chunk of 512 tokens in each of 4 sequences of 8192,
-// 8 heads of a group of 8: 548 us, 1000 TFLOP/s.  (In bursts of 8 calls, while
-// the clock ramps up, 185 and 670 us.)  The matrix units are busy for a
-// third of the time and the vector ALUs for half of it; with the exponentials
-// left out, or the staging, or the reads of LDS, or the second product, the
-// time falls by 10 to 16 % each, so no one of them alone is the bound.
+// A prompt of 4096 tokens, 32 heads, D = 128: 167 us, 825 TFLOP/s by the
+// formula's products (158 to 168 on four boards); a chunk of 512 tokens in each
+// of 4 sequences of 8192, 8 heads of a group of 8: 548 us, 1000 TFLOP/s.  (In
+// bursts of 8 calls, while the clock ramps up, 185 and 670 us.)  The matrix
+// units are busy for a third of the time and the vector ALUs for half of it;
+// with the exponentials left out, or the staging, or the reads of LDS, or the
+// second product, the time falls by 5 to 16 % each, so no one of them alone
+// is the bound.
 // ---------------------------------------------------------------------------
 constexpr int kTileWaves = 8;
 constexpr int kTileCols = 32 * kTileWaves;
