@@ -712,7 +712,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
 constexpr int kTileWaves = 8;
 constexpr int kTileCols = 32 * kTileWaves;
 constexpr int kTileKeys = 64;
-constexpr float kLeast = -100.0f;      // log2 of the smallest relative value scale
+// log2 of the smallest relative value scale.  Smaller ones, 0 among them, are
+// taken as it: 2^-60 of the others' values, nothing that fp16 holds.  Their
+// weights come back into the sum from 2^(z - m - 60), so that what the
+// exponential drops below 2^-126 is below 2^-66 of the maximum (from -100 on
+// weights below 2^-26 were lost, 1.4e-3 of a sum over 131071 keys).
+constexpr float kLeast = -60.0f;
 constexpr float kMost = 8192.0f;       // largest sum of 8 probabilities taken as it is
 
 typedef int v16i __attribute__((ext_vector_type(16)));

@@ -1,0 +1,52 @@
+"""GPU tests of the int8 key/value cache at its edges, against plain 64-bit forms."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import int8_matmul_amd as li8
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("least", [0.0, 2.0**-99, 2.0**-110])
+def test_sum_over_pages_without_values(least):
+    """Pages whose value scale is (almost) 0 count in the softmax's sum with
+    their full weight: one key at z = 0 in a page with values, 16383 at
+    2^-26.125 of its weight, all but 15 of them in pages without.  They are
+    2.2e-4 of the sum together.
+
+    Bound: scores are exact to 2^-16 of a weight (queries of one value,
+    integer codes), and a lane adds 2 numbers for each of 512 subtiles of 32
+    keys in fp32, each sum off by half a step: 1024 * 2^-24."""
+    heads, dim, page, n, rows = 256, 64, 128, 16384, 128
+    pages = n // page
+    k = torch.zeros((pages, heads, page, dim), dtype=torch.int8, device=DEV)
+    k[..., 0] = -26
+    k[3, :, 5, 0] = 0
+    v = torch.ones_like(k)
+    ks = torch.ones((pages, heads), dtype=torch.float32, device=DEV)
+    vs = torch.full_like(ks, least)
+    vs[3] = 1.0
+    cache = li8.KVCache(k, v, ks, vs)
+    batch = li8.KVBatch(i32([0, rows]), i32([n]), torch.arange(pages, dtype=torch.int32, device=DEV)[None], rows, rows, n)
+    assert li8.kv_attention_plan(batch, cache, heads, causal=False) == dict(path="tiled", splits=1)
+    Q = torch.zeros((rows, heads, dim), dtype=F16, device=DEV)
+    Q[..., 0] = 1.0
+    lse = torch.empty((rows, heads), dtype=torch.float32, device=DEV)
+    scale = 26.125 / 26 * math.log(2)
+    out = li8.kv_attention(Q, cache, batch, scale=scale, causal=False, lse=lse)
+    w = 2.0**-26.125
+    total = 1 + (n - 1) * w
+    bound = 1024 * 2.0**-24 + n * w * 2.0**-16
+    got = lse.double().cpu().numpy()
+    assert np.abs(got - math.log(total)).max() <= bound, (got.min(), got.max(), math.log(total))
+    want = (1 + 15 * w + (n - 16) * w * least) / total
+    assert np.abs(out.double().cpu().numpy() - want).max() <= 2.0**-11 + bound + 2.0**-24
