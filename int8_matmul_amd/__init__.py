@@ -22,6 +22,7 @@ If the library has not been built, every call raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -609,6 +610,15 @@ def stages(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold: float
 _KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
 
+def _int32(value, name: str) -> int:
+    """``value`` as the library's 32-bit fields and arguments take it: ctypes
+    would cut a larger number to its low bits."""
+    n = operator.index(value)
+    if not -(1 << 31) <= n < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {n}")
+    return n
+
+
 class _CKVCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
@@ -646,8 +656,9 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
         self.device = k.device
-        self._c = _CKVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.pages, self.heads,
-                            self.page_size, self.head_dim)
+        self._c = _CKVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.pages,
+                            _int32(self.heads, "heads"), _int32(self.page_size, "page_size"),
+                            _int32(self.head_dim, "head_dim"))
         self._ref = ctypes.addressof(self._c)
 
 
@@ -687,8 +698,8 @@ class KVBatch:
         self.q_start, self.kv_len, self.table = q_start, kv_len, table
         self.seqs, self.tokens, self.max_q, self.max_kv = S, tokens, max_q, max_kv
         self.device = q_start.device
-        self._c = _CKVBatch(_ptr(q_start), _ptr(kv_len), _ptr(table), stride, width, S, tokens, max_q,
-                            max_kv)
+        self._c = _CKVBatch(_ptr(q_start), _ptr(kv_len), _ptr(table), stride, _int32(width, "table's width"),
+                            _int32(S, "seqs"), tokens, max_q, max_kv)
         self._ref = ctypes.addressof(self._c)
 
 
@@ -704,7 +715,8 @@ class Rope:
             raise ValueError(f"shape mismatch: cos {tuple(cos.shape)}, sin {tuple(sin.shape)}")
         _same_device(cos, sin=sin)
         self.cos, self.sin, self.interleaved, self.device = cos, sin, bool(interleaved), cos.device
-        self._c = _CRope(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(self.interleaved))
+        self._c = _CRope(_ptr(cos), _ptr(sin), _int32(cos.shape[0], "rows"), _int32(2 * cos.shape[1], "dims"),
+                         int(self.interleaved))
         self._ref = ctypes.addressof(self._c)
 
 
@@ -802,7 +814,8 @@ def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.float16,
 
 def kv_attention_workspace_bytes(batch: KVBatch, cache: KVCache, q_heads: int) -> int:
     """Bytes of workspace that ``kv_attention`` needs (0: none)."""
-    return int(load_library().int8_kv_attention_workspace_bytes(batch._ref, cache._ref, q_heads))
+    return int(load_library().int8_kv_attention_workspace_bytes(batch._ref, cache._ref,
+                                                                _int32(q_heads, "q_heads")))
 
 
 def new_kv_attention_workspace(batch: KVBatch, cache: KVCache, q_heads: int) -> torch.Tensor:
@@ -819,7 +832,8 @@ def kv_attention_plan(batch: KVBatch, cache: KVCache, q_heads: int, causal: bool
     parts that a row's keys are split into."""
     path, splits = ctypes.c_int32(), ctypes.c_int32()
     _check("int8_kv_attention_plan",
-           load_library().int8_kv_attention_plan(batch._ref, cache._ref, q_heads, int(bool(causal)), window,
+           load_library().int8_kv_attention_plan(batch._ref, cache._ref, _int32(q_heads, "q_heads"),
+                                                 int(bool(causal)), _int32(window, "window"),
                                                  ctypes.byref(path), ctypes.byref(splits)))
     return dict(path=KV_PATHS[path.value], splits=splits.value)
 
@@ -857,8 +871,8 @@ def kv_attention(Q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float |
         _require(workspace, torch.uint8, "workspace", 1)
         if workspace.device != Q.device:
             raise ValueError(f"workspace is on {workspace.device}, expected {Q.device}")
-    _kv_call("int8_kv_attention", batch.device, Q.data_ptr(), qs, _KV_DTYPES[Q.dtype], Hq,
+    _kv_call("int8_kv_attention", batch.device, Q.data_ptr(), qs, _KV_DTYPES[Q.dtype], _int32(Hq, "q_heads"),
              float(D ** -0.5 if scale is None else scale), None if rope is None else rope._ref,
-             int(bool(causal)), window, batch._ref, cache._ref, out.data_ptr(), os_,
+             int(bool(causal)), _int32(window, "window"), batch._ref, cache._ref, out.data_ptr(), os_,
              _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out

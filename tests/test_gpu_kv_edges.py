@@ -50,3 +50,28 @@ def test_sum_over_pages_without_values(least):
     assert np.abs(got - math.log(total)).max() <= bound, (got.min(), got.max(), math.log(total))
     want = (1 + 15 * w + (n - 16) * w * least) / total
     assert np.abs(out.double().cpu().numpy() - want).max() <= 2.0**-11 + bound + 2.0**-24
+
+
+def small(seqs=1, tokens=1, kv=20):
+    cache = li8.new_kv_cache(4, 2, 64, 16, DEV)
+    return cache, li8.KVBatch(i32([0] + [tokens] * seqs), i32([kv] * seqs), i32([[1, 2]] * seqs), tokens, tokens, kv)
+
+
+def test_numbers_past_32_bits():
+    """Refused, not cut to their low bits."""
+    cache, batch = small()
+    Q = torch.zeros((1, 4, 64), dtype=F16, device=DEV)
+    for window in (2**32 + 1, 2**31, 2**64):
+        with pytest.raises(ValueError):
+            li8.kv_attention(Q, cache, batch, window=window)
+    li8.kv_attention(Q, cache, batch, window=2**31 - 1)
+    none = dict(dtype=torch.int8, device=DEV), dict(dtype=torch.float32, device=DEV)
+    for shape in ((0, 2**32 + 4, 16, 64), (0, 4, 2**32 + 16, 64), (0, 4, 16, 2**32 + 64)):
+        k, s = torch.empty(shape, **none[0]), torch.empty(shape[:2], **none[1])
+        with pytest.raises(ValueError):
+            li8.KVCache(k, k, s, s)
+    for shape in ((2**32 + 20, 0), (0, 2**31 + 32)):
+        with pytest.raises(ValueError):
+            li8.Rope(torch.empty(shape, **none[1]), torch.empty(shape, **none[1]))
+    with pytest.raises(ValueError):
+        li8.KVBatch(i32([0]), i32([]), torch.empty((0, 2**32 + 2), dtype=torch.int32, device=DEV), 0, 0, 0)
