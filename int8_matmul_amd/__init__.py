@@ -637,12 +637,27 @@ class _CRope(ctypes.Structure):
                 ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
-class KVCache:
+class _Described:
+    """An object whose description the library reads at every call: it is made
+    once, so no name can be bound anew (the checks would see the new value and
+    the library the old one)."""
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: make a new object")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} is fixed")
+
+
+class KVCache(_Described):
     """Keys and values in int8, with one scale for each page of tokens and head:
     k, v int8 [pages, heads, page_size, head_dim], k_scale, v_scale fp32 [pages, heads].
 
     Holds the tensors and their description for the library; the checks are
-    made here, once.  The tensors may change in place."""
+    made here, once.  What the tensors hold may change, the tensors and their
+    memory may not (no assignment, no ``resize_`` or ``set_``)."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         _require(k, torch.int8, "k", 4)
@@ -662,7 +677,7 @@ class KVCache:
         self._ref = ctypes.addressof(self._c)
 
 
-class KVBatch:
+class KVBatch(_Described):
     """Sequences and their new rows: q_start int32 [seqs + 1], kv_len int32 [seqs],
     table int32 [seqs, width] of page numbers (rows may be strided).
 
@@ -670,8 +685,9 @@ class KVBatch:
     the last ones of sequence s, which has kv_len[s] tokens with them.
     ``tokens`` is the packed tensors' row count; ``max_q`` and ``max_kv`` are
     at least the longest chunk and the longest sequence (the lengths
-    themselves stay on the GPU).  The tensors may change in place, so one
-    object serves every step of a captured graph."""
+    themselves stay on the GPU).  What the tensors hold may change, so one
+    object serves every step of a captured graph; the tensors, their memory
+    and the numbers are fixed."""
 
     def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, tokens: int,
                  max_q: int, max_kv: int):
@@ -703,7 +719,7 @@ class KVBatch:
         self._ref = ctypes.addressof(self._c)
 
 
-class Rope:
+class Rope(_Described):
     """Rotation of the first 2 * cos.shape[1] values of every head by position:
     cos, sin fp32 [rows, dims / 2]; pairs (i, i + dims/2), or (2i, 2i + 1) if
     ``interleaved``."""

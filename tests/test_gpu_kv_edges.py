@@ -75,3 +75,22 @@ def test_numbers_past_32_bits():
             li8.Rope(torch.empty(shape, **none[1]), torch.empty(shape, **none[1]))
     with pytest.raises(ValueError):
         li8.KVBatch(i32([0]), i32([]), torch.empty((0, 2**32 + 2), dtype=torch.int32, device=DEV), 0, 0, 0)
+
+
+def test_descriptions_are_fixed():
+    """The library reads what was described at construction: a name bound anew
+    would pass the checks and leave the old bounds and pointers in use."""
+    cache, batch = small(tokens=2)
+    rope = li8.Rope(torch.zeros((20, 32), device=DEV), torch.zeros((20, 32), device=DEV))
+    for thing, names in ((cache, ("k", "v", "k_scale", "v_scale", "pages", "heads", "page_size", "head_dim", "device")),
+                         (batch, ("q_start", "kv_len", "table", "seqs", "tokens", "max_q", "max_kv", "device")),
+                         (rope, ("cos", "sin", "interleaved", "device"))):
+        for name in names:
+            was = getattr(thing, name)
+            with pytest.raises(AttributeError):
+                setattr(thing, name, was)
+            with pytest.raises(AttributeError):
+                delattr(thing, name)
+            assert getattr(thing, name) is was
+    with pytest.raises(ValueError):                       # rows of a batch with more of them
+        li8.kv_append(torch.zeros((3, 2, 64), dtype=F16, device=DEV), torch.zeros((3, 2, 64), dtype=F16, device=DEV), cache, batch)

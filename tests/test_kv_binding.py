@@ -56,3 +56,17 @@ def test_numbers_within_32_bits():
         li8.kv_attention_plan(batch(), cache(), 64, window=256.0)
     with pytest.raises(li8.Int8MatmulError):
         li8.kv_attention_plan(batch(), cache(), 64, window=-1)
+
+
+def test_described_objects_are_fixed(monkeypatch):
+    """KVCache and Rope once more without a GPU."""
+    import torch
+    monkeypatch.setattr(li8, "_require", lambda *a: None)
+    k, s = torch.zeros((2, 1, 16, 64), dtype=torch.int8), torch.zeros((2, 1))
+    cache, rope = li8.KVCache(k, k, s, s), li8.Rope(torch.zeros(4, 8), torch.zeros(4, 8))
+    for thing, name in ((cache, "k"), (cache, "pages"), (rope, "cos"), (rope, "extra")):
+        with pytest.raises(AttributeError):
+            setattr(thing, name, None)
+    with pytest.raises(AttributeError):
+        del cache.k
+    assert cache._c.k == cache.k.data_ptr() and rope._c.cos == rope.cos.data_ptr()
