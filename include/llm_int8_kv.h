@@ -29,6 +29,11 @@
  *     chunk longer than max_q has the tokens past it left out, and a page
  *     number outside [0, pages) is never followed: nothing is stored there,
  *     reading gives zeros, and attention treats its tokens as masked.
+ *   - A batch is refused (LI8_ERR_SHAPE) where a grid would have 2^32
+ *     work-items or more.  With q = min(max_q, tokens): append from seqs x
+ *     pages of q tokens of 2^24 on, read from seqs x ceil(q / 64) of 2^24 on,
+ *     attention from seqs x heads x blocks of columns of 2^23 on (at the
+ *     earliest; smaller workgroups go further).
  *   - Inputs must be finite where they are read; the scales of pages with
  *     stored tokens finite and >= 0.  Codes and scales of tokens that no query sees,
  *     and rows outside [q_start[0], q_start[seqs]), may hold anything.

@@ -99,8 +99,12 @@ li8_status check_heads(const li8_kv_batch *b, const li8_kv_cache *c, int32_t q_h
     const int64_t rows = std::min(b->max_q, b->tokens), group = q_heads / c->heads;
     if (rows * group > kMaxGrid)
         return LI8_ERR_SHAPE;
+    // (256 columns and work-items for a workgroup at least: with more, no plan
+    // fits, and the plan's own products need not be looked at)
+    if ((double)b->seqs * c->heads * ((rows * group + 255) / 256) * 256 > kKvMaxItems)
+        return LI8_ERR_SHAPE;
     const KvPlan p = kv_plan(*b, *c, q_heads, causal != 0, window);
-    if (((double)b->seqs * c->heads + 8) * p.blocks * std::max(p.splits, p.used) > (double)kMaxGrid)
+    if (kv_attention_items(*b, *c, p) > kKvMaxItems)
         return LI8_ERR_SHAPE;
     return LI8_OK;
 }
@@ -130,8 +134,7 @@ li8_status int8_kv_append(const void *K, int64_t k_stride, const void *V, int64_
     LI8_TRY(check_pointers(batch, cache));
     LI8_TRY(check_tokens(K, k_stride, cache->heads, cache->head_dim));
     LI8_TRY(check_tokens(V, v_stride, cache->heads, cache->head_dim));
-    const int64_t q = std::min(batch->max_q, batch->tokens);
-    if ((double)batch->seqs * ((q + cache->page_size - 2) / cache->page_size + 1) > (double)kMaxGrid)
+    if (kv_append_items(*batch, *cache) > kKvMaxItems)
         return LI8_ERR_SHAPE;
     return from_hip(launch_kv_append(KvTokens{static_cast<const uint16_t *>(K), k_stride},
                                      KvTokens{static_cast<const uint16_t *>(V), v_stride},
@@ -149,8 +152,7 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
     LI8_TRY(check_pointers(batch, cache));
     LI8_TRY(check_tokens(K, k_stride, cache->heads, cache->head_dim));
     LI8_TRY(check_tokens(V, v_stride, cache->heads, cache->head_dim));
-    const int64_t q = std::min(batch->max_q, batch->tokens);
-    if ((double)batch->seqs * ((q + 15) / 16) > (double)kMaxGrid)
+    if (kv_read_items(*batch) > kKvMaxItems)
         return LI8_ERR_SHAPE;
     return from_hip(launch_kv_read(*cache, *batch, dtype == LI8_BF16, static_cast<uint16_t *>(K),
                                    k_stride, static_cast<uint16_t *>(V), v_stride, stream));

@@ -1319,14 +1319,19 @@ int64_t plan_items(const li8_kv_batch &b, const li8_kv_cache &c, const KvPlan &p
     return (int64_t)b.seqs * c.heads * p.blocks;
 }
 
+// (sequence, head) pairs of the tiled kernel dealt over the XCDs: 8 lanes,
+// fewer where that would leave XCDs without work.
+int tiled_lanes(int64_t pairs) { return pairs >= 64 ? 8 : (int)std::min<int64_t>(8, pairs & -pairs); }
+
+// Work-items of an unshared few-column workgroup.
+int few_items(int64_t items) { return items <= 512 ? 512 : 256; }
+
 template <int D, bool BF16>
 hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipStream_t s)
 {
     if (t.cols == kTileCols) {
         const int64_t pairs = items / t.blocks;
-        // (sequence, head) pairs dealt over the XCDs: 8 lanes, fewer where
-        // that would leave XCDs without work
-        const int lanes = pairs >= 64 ? 8 : (int)std::min<int64_t>(8, pairs & -pairs);
+        const int lanes = tiled_lanes(pairs);
         const unsigned grid = t.parts > 0 ? (unsigned)t.parts : (unsigned)(round_up(pairs, lanes) * t.blocks);
         k_kv_tiled<D, BF16><<<grid, 64 * kTileWaves, 0, s>>>(a, t, (int)pairs, lanes,
                                                                 !t.causal || a.max_q < a.max_kv / 2);
@@ -1340,7 +1345,7 @@ hipError_t attention_go(const KvArgs &a, const AttnArgs &t, int64_t items, hipSt
                 k_kv_few<D, BF16, 2, 4, false><<<grid, 256, 0, s>>>(a, t);
             else
                 k_kv_few<D, BF16, 1, 4, true><<<grid, 256, 0, s>>>(a, t);
-        } else if (items <= 512) {
+        } else if (few_items(items) == 512) {
             if (wide)
                 k_kv_few<D, BF16, 2, 8, false><<<(unsigned)items, 512, 0, s>>>(a, t);
             else
@@ -1425,6 +1430,16 @@ size_t kv_workspace(const li8_kv_batch &b, const li8_kv_cache &c, int q_heads)
     if (rows == 0)
         return 0;
     return align_up((size_t)rows * 4 * c.head_dim, 256) + align_up((size_t)rows * 4, 256);
+}
+
+double kv_attention_items(const li8_kv_batch &b, const li8_kv_cache &c, const KvPlan &p)
+{
+    if (p.path == LI8_KV_EMPTY || p.parts > 0)   // (shared: fewer than 8 kFewSlots blocks, merging them included)
+        return 0;
+    const int64_t pairs = (int64_t)b.seqs * c.heads;
+    if (p.path == LI8_KV_TILED)
+        return (double)round_up(pairs, tiled_lanes(pairs)) * p.blocks * (64 * kTileWaves);
+    return (double)pairs * p.blocks * few_items(plan_items(b, c, p));
 }
 
 hipError_t launch_kv_attention(KvTokens Q, bool bf16, int q_heads, float scale, KvRope rope,

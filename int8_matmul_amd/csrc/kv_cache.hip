@@ -199,16 +199,21 @@ hipError_t append_go(const KvArgs &a, KvTokens K, KvTokens V, KvRope rope, int s
     return hipGetLastError();
 }
 
+// Pages that a chunk of the longest length can touch, and its new rows in one.
+int touched_pages(int q, int page) { return (int)(((int64_t)q + page - 2) / page + 1); }
+int page_rows(int q, int page) { return std::min(page, q); }
+
+// One wave per page and head while its rows fit one pass of the wave: a step
+// of one token per sequence has 4 rows at D = 128 of which one is there, and a
+// larger workgroup would idle.
+bool one_wave(int rows, int dim) { return rows <= 64 / (dim / 8); }
+
 template <int D, bool BF16>
 hipError_t append_d(const KvArgs &a, KvTokens K, KvTokens V, KvRope rope, int seqs, hipStream_t s)
 {
     const int page = 1 << a.page_shift, q = std::min(a.max_q, a.tokens);
-    const int touched = (int)(((int64_t)q + page - 2) / page + 1);
-    const int rows = std::min(page, q);   // new rows of one page at most
-    // One wave per page and head while its rows fit one pass of the wave: a
-    // step of one token per sequence has 4 rows at D = 128 of which one is
-    // there, and a larger workgroup would idle.
-    if (rows <= 64 / (D / 8))
+    const int touched = touched_pages(q, page), rows = page_rows(q, page);
+    if (one_wave(rows, D))
         return append_go<D, 64, 1, BF16>(a, K, V, rope, seqs, touched, s);
     const int rpt = (rows + 256 / (D / 8) - 1) / (256 / (D / 8));
     if (rpt <= 1)
@@ -220,7 +225,21 @@ hipError_t append_d(const KvArgs &a, KvTokens K, KvTokens V, KvRope rope, int se
     return append_go<D, 256, 8, BF16>(a, K, V, rope, seqs, touched, s);
 }
 
+int64_t read_blocks(const li8_kv_batch &b)
+{
+    return ((int64_t)std::min(b.max_q, b.tokens) + kReadTokens - 1) / kReadTokens;
+}
+
 } // namespace
+
+double kv_append_items(const li8_kv_batch &b, const li8_kv_cache &c)
+{
+    const int q = std::min(b.max_q, b.tokens);
+    return (double)b.seqs * touched_pages(q, c.page_size) *
+           (one_wave(page_rows(q, c.page_size), c.head_dim) ? 64 : 256);
+}
+
+double kv_read_items(const li8_kv_batch &b) { return (double)b.seqs * read_blocks(b) * 256; }
 
 hipError_t launch_kv_append(KvTokens K, KvTokens V, bool bf16, KvRope rope, const li8_kv_batch &b,
                             const li8_kv_cache &c, hipStream_t s)
@@ -237,7 +256,7 @@ hipError_t launch_kv_read(const li8_kv_cache &c, const li8_kv_batch &b, bool bf1
                           int64_t ks, uint16_t *V, int64_t vs, hipStream_t s)
 {
     const KvArgs a = kv_args(b, c);
-    const int blocks = (int)(((int64_t)std::min(b.max_q, b.tokens) + kReadTokens - 1) / kReadTokens);
+    const int blocks = (int)read_blocks(b);
     const dim3 grid((unsigned)(b.seqs * blocks), (unsigned)c.heads, 2);
     if (c.head_dim == 128) {
         if (bf16)

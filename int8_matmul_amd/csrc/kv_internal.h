@@ -77,6 +77,14 @@ struct KvTokens {    // strided rows of 16-bit values
     int64_t stride;
 };
 
+// Work-items of a call's largest launch along x (as numbers that no sizes
+// overflow): past 2^32 - 1 the runtime refuses the launch, so the checks refuse
+// the call.
+constexpr double kKvMaxItems = 4294967295.0;
+double kv_append_items(const li8_kv_batch &b, const li8_kv_cache &c);
+double kv_read_items(const li8_kv_batch &b);
+double kv_attention_items(const li8_kv_batch &b, const li8_kv_cache &c, const KvPlan &p);
+
 hipError_t launch_kv_append(KvTokens K, KvTokens V, bool bf16, KvRope rope, const li8_kv_batch &b,
                             const li8_kv_cache &c, hipStream_t s);
 hipError_t launch_kv_read(const li8_kv_cache &c, const li8_kv_batch &b, bool bf16, uint16_t *K,

@@ -94,3 +94,33 @@ def test_descriptions_are_fixed():
             assert getattr(thing, name) is was
     with pytest.raises(ValueError):                       # rows of a batch with more of them
         li8.kv_append(torch.zeros((3, 2, 64), dtype=F16, device=DEV), torch.zeros((3, 2, 64), dtype=F16, device=DEV), cache, batch)
+
+
+def test_largest_grids():
+    """The most workgroups that the checks let through (2^32 work-items less a
+    few), nearly all of them without a row: the last sequence's tokens are
+    stored, read and attended to."""
+    cache = li8.new_kv_cache(3, 16, 64, 16, DEV)
+    x = torch.randn((8192, 16, 64), device=DEV).to(F16)
+
+    def last(seqs, n, max_q):
+        q_start, kv_len = torch.zeros(seqs + 1, dtype=torch.int32, device=DEV), torch.zeros(seqs, dtype=torch.int32, device=DEV)
+        q_start[-1], kv_len[-1] = n, n
+        return li8.KVBatch(q_start, kv_len, i32([[1, 2]]).expand(seqs, 2).contiguous(), max_q, max_q, 32)
+
+    near, one = li8.new_kv_cache(3, 16, 64, 16, DEV), li8.KVBatch(i32([0, 17]), i32([17]), i32([[1, 2]]), 17, 17, 32)
+    li8.kv_append(x[:17], x[:17], near, one)
+    big = last((1 << 23) - 1, 17, 17)
+    li8.kv_append(x[:17], x[:17], cache, big)
+    assert torch.equal(cache.k, near.k) and torch.equal(cache.v, near.v) and torch.equal(cache.k_scale, near.k_scale)
+    del big
+    big = last((1 << 17) - 1, 17, 8192)
+    K, V = li8.kv_read(cache, big)
+    want = li8.kv_read(near, one)
+    assert torch.equal(K[:17], want[0]) and torch.equal(V[:17], want[1])
+    del big
+    big = last((1 << 20) - 1, 1, 1)
+    assert li8.kv_attention_plan(big, cache, 16) == dict(path="few", splits=1)
+    out = li8.kv_attention(x[:1], cache, big)
+    first = li8.KVBatch(i32([0, 1]), i32([1]), i32([[1, 2]]), 1, 1, 32)
+    assert torch.equal(out, li8.kv_attention(x[:1], near, first))

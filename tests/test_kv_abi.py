@@ -298,3 +298,31 @@ def test_oracle_attention_pins():
     assert np.allclose(O1, np.repeat(V, 3, 1))
     O2, l2, _, _ = okv.attention(c, q, 0.1, [0, 20], [12], [[1, 0]])    # 8 rows before the first token
     assert (O2[:8] == 0).all() and np.isneginf(l2[:8]).all() and np.isfinite(l2[8:]).all()
+
+
+def test_more_work_items_than_a_launch_has(lib):
+    """Workgroups x their size stay below 2^32 along a grid's x: sizes past it
+    are refused by the checks, not by the launch."""
+    wide = dict(table_width=1 << 12, table_stride=1 << 12)
+    # read: 64 tokens for each of 2^24 workgroups of 256
+    for seqs, q in ((1 << 17, 8192), (1 << 24, 64), (1 << 30, 1), ((1 << 31) - 1, (1 << 31) - 1)):
+        assert read(lib, b=batch(seqs=seqs, tokens=(1 << 31) - 1, max_q=q)) == SHAPE
+    # append: one wave for a page while its rows fit it, else four
+    for seqs, q in ((1 << 26, 1), (1 << 26, 8), (1 << 22, 64), (1 << 23, 17), ((1 << 31) - 1, (1 << 31) - 1)):
+        assert append(lib, b=batch(seqs=seqs, tokens=(1 << 31) - 1, max_q=q)) == SHAPE
+    # attention: few columns in workgroups of 256, tiled ones of 512
+    for seqs, heads, group, q, kv, path in ((1 << 20, 16, 1, 1, 16, 1), (1 << 22, 4, 9, 2, 100, 1),
+                                            (1 << 15, 256, 16, 10, 100, 2), (1 << 13, 256, 1, 1000, 4096, 2),
+                                            ((1 << 31) - 1, 65535, 1, (1 << 31) - 1, 16, 2)):
+        c = cache(heads=heads)
+        sizes = dict(tokens=(1 << 31) - 1, max_q=q, max_kv=kv, **wide)
+        b = batch(seqs=seqs, **sizes)
+        stride = heads * group * 64
+        p, s = ctypes.c_int32(), ctypes.c_int32()
+        out = ctypes.byref(p), ctypes.byref(s)
+        assert lib.int8_kv_attention_plan(ref(b), ref(c), heads * group, 1, 0, *out) == SHAPE
+        assert attend(lib, c=c, b=b, heads=heads * group, qs=stride, os_=stride) == SHAPE
+        assert lib.int8_kv_attention_workspace_bytes(ref(b), ref(c), heads * group) == 0
+        if seqs < 1 << 30:                                # one (sequence, head) fewer, or eight, is fine
+            assert lib.int8_kv_attention_plan(ref(batch(seqs=seqs - 1, **sizes)), ref(c), heads * group, 1, 0, *out) == OK
+            assert p.value == path
