@@ -48,3 +48,38 @@ def test_tiled(ns, ls, heads, group, dim, page, rot, causal, window, shared, dty
     t = base.Setup(ns, ls, heads, dim, page, dtype, seed=page + group, rot=rot, inter=page == 32, lead=1,
                    max_kv=1 << 14, max_q=rows, tail=max(0, rows - sum(ns)))
     check(t, heads * group, causal, window, 2.0, "tiled", shared)
+
+
+WIDE_MERGES = [
+    # one block in more than 14 parts: a workgroup merges a column
+    ([1], [20000], 1, 64, 64),
+    ([1], [20000], 8, 64, 16),
+    ([3], [9000], 9, 64, 32),        # 27 columns
+    ([3], [9000], 9, 128, 64),
+    ([4], [6000], 3, 128, 16),
+    ([16], [7000], 1, 64, 128),
+]
+
+
+@pytest.mark.parametrize("ns, ls, group, dim, page", WIDE_MERGES)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_merges_of_many_parts(ns, ls, group, dim, page, dtype):
+    t = base.Setup(ns, ls, 1, dim, page, dtype, seed=group, rot=64, lead=1, tail=1)
+    assert check(t, group, True, 0, 1.0, "few", True)["splits"] > 14
+
+
+@pytest.mark.parametrize("dim, dtype", [(64, F16), (64, BF16), (128, F16), (128, BF16)])
+def test_wide_blocks_past_512(dim, dtype):
+    """20 columns in each of 560 blocks with short contexts: 32-column
+    workgroups of 4 waves, unshared."""
+    t = base.Setup([1] * 70, [(37 * i) % 90 for i in range(70)], 8, dim, 16, dtype, group=20)
+    check(t, 160, True, 0, 2.0, "few", False)
+
+
+@pytest.mark.parametrize("dim, group, dtype", [(64, 1, F16), (128, 1, BF16), (64, 17, F16)])
+def test_blocks_past_sharing(dim, group, dtype):
+    """4096 blocks or more go unshared whatever their lengths: a long sequence
+    of 44 steps among short ones."""
+    heads = 64
+    t = base.Setup([1] * 64, [1400] + [1 + (7 * i) % 50 for i in range(63)], heads, dim, 64, dtype, group=group)
+    check(t, heads * group, True, 0, 1.0, "few", False)
