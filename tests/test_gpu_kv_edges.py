@@ -6,6 +6,9 @@ import pytest
 import torch
 
 import int8_matmul_amd as li8
+import test_gpu_kv as base
+from oracle import kv as okv
+from oracle import kv_error
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -124,3 +127,68 @@ def test_largest_grids():
     out = li8.kv_attention(x[:1], cache, big)
     first = li8.KVBatch(i32([0, 1]), i32([1]), i32([[1, 2]]), 1, 1, 32)
     assert torch.equal(out, li8.kv_attention(x[:1], near, first))
+
+
+def cut(t, q_start, kv_len):
+    """(first row, rows, rows that count, tokens) of each sequence, from the
+    header: rows lie in the packed tensors, a sequence is cut to max_kv tokens,
+    of which its rows are the last, and rows past max_q are left out."""
+    out = []
+    for s, length in enumerate(kv_len):
+        q0 = min(max(q_start[s], 0), t.tokens)
+        rows = min(max(q_start[s + 1], q0), t.tokens) - q0
+        out.append((q0, rows, min(rows, t.batch.max_q), min(max(length, 0), t.max_kv)))
+    return out
+
+
+CUTS = [
+    # ns, ls, heads, group, dim, page, max_q, max_kv, what the GPU finds: q_start, kv_len
+    ([3, 2], [20, 30], 1, 1, 64, 16, None, None, [0, 3, 2**31 - 1], [20, 2**31 - 1]),
+    ([3, 2], [20, 30], 1, 1, 64, 16, None, None, [-5, 2, 1], [-3, 30]),
+    ([3, 2], [20, 30], 1, 1, 64, 16, None, None, [4, 1, 5], [31, 99]),
+    ([3, 2], [20, 30], 1, 1, 64, 16, None, None, [0, 5, 5], [2**31 - 1, -2**31]),
+    ([40, 9, 7], [60, 41, 33], 2, 3, 128, 16, 25, 50, [0, 40, 49, 56], [60, 41, 33]),       # chunks past max_q, tokens past max_kv
+    ([40, 9, 7], [60, 41, 33], 2, 3, 128, 16, 25, 50, [0, 40, 49, 56], [10, 2**30, 3]),
+    ([40, 9, 7], [60, 41, 33], 2, 3, 64, 64, 5, 64, [2, 51, 51, 2**31 - 1], [64, 41, 63]),
+    ([1, 6], [3000, 2000], 1, 4, 64, 64, 3, 2500, [0, 1, 7], [2600, 2000]),                  # keys shared
+    ([200, 300], [210, 400], 8, 1, 64, 16, 150, 1 << 14, [0, 200, 500], [210, 2**31 - 1]),   # tiled
+    ([200, 300], [210, 400], 8, 1, 128, 64, 150, 1 << 14, [-9, 180, 400], [90, 390]),
+]
+
+
+@pytest.mark.parametrize("ns, ls, heads, group, dim, page, max_q, max_kv, q_start, kv_len", CUTS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_numbers_past_the_bounds(ns, ls, heads, group, dim, page, max_q, max_kv, q_start, kv_len, causal):
+    """Lengths on the GPU that the host's bounds do not allow are cut as the
+    header says: codes, scales, values, outputs and the rows left as they were."""
+    t = base.Setup(ns, ls, heads, dim, page, F16, seed=dim, rot=64, max_kv=max_kv, max_q=max_q)
+    t.batch.q_start.copy_(i32(q_start))
+    t.batch.kv_len.copy_(i32(kv_len))
+    seqs = cut(t, q_start, kv_len)
+    K, V, Q = t.rows(heads), t.rows(heads, 2.0), t.rows(heads * group)
+    li8.kv_append(K, V, t.cache, t.batch, rope=t.rope)
+    for s, (q0, rows, n, L) in enumerate(seqs):
+        okv.append(t.ref, base.f32(K), base.f32(V), [q0, q0 + n], [L - rows + n], t.table[s:s + 1], t.oracle_rope)
+    t.same_cache()
+
+    got = tuple(torch.full((t.tokens, heads, dim), 7.0, dtype=F16, device=DEV) for _ in range(2))
+    li8.kv_read(t.cache, t.batch, out=got)
+    want = np.full((2, t.tokens, heads, dim), 7.0, np.float32)
+    for s, (q0, rows, n, L) in enumerate(seqs):
+        kv = okv.read(t.ref, [q0, q0 + n], [L - rows + n], t.table[s:s + 1], t.tokens)
+        want[:, q0:q0 + n] = [x[q0:q0 + n] for x in kv]
+    for g, w in zip(got, want):
+        assert torch.equal(g.cpu(), torch.from_numpy(w).to(F16))
+
+    out = torch.full((t.tokens, heads * group, dim), 7.0, dtype=F16, device=DEV)
+    lse = torch.full((t.tokens, heads * group), 7.0, dtype=torch.float32, device=DEV)
+    li8.kv_attention(Q, t.cache, t.batch, rope=t.rope, causal=causal, out=out, lse=lse)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    left = np.ones(t.tokens, bool)
+    for s, (q0, rows, n, L) in enumerate(seqs):
+        r = kv_error.rows(t.ref, base.f32(Q), dim ** -0.5, [q0, q0 + rows], [L], t.table[s:s + 1], t.oracle_rope, causal)
+        r.lse[q0 + n:] = np.nan                           # rows past max_q
+        wrong = kv_error.check(r, out, lse)
+        assert wrong is None, (s, wrong)
+        left[q0:q0 + n] = False
+    assert (out[left] == 7).all() and (lse[left] == 7).all()
