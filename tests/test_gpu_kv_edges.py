@@ -192,3 +192,133 @@ def test_numbers_past_the_bounds(ns, ls, heads, group, dim, page, max_q, max_kv,
         assert wrong is None, (s, wrong)
         left[q0:q0 + n] = False
     assert (out[left] == 7).all() and (lse[left] == 7).all()
+
+
+def plain(Q, cache, table, kv, scale):
+    """fp64 (O, bound) of one sequence's last rows without a rotation: the bound
+    of a kernel with probabilities in one fp16 part (oracle/kv_error.py, with
+    sum w |v - O| <= 2 sum w |v|)."""
+    rows, Hq, D = Q.shape
+    H, page = cache.heads, cache.page_size
+    at = torch.arange(kv, device=DEV)
+    p, i = table.long()[at // page], at % page
+    kc, vc = cache.k[p, :, i].double(), cache.v[p, :, i].double()
+    k, vs = kc * cache.k_scale[p].double()[..., None], cache.v_scale[p].double()
+    v = vc * vs[..., None]
+    O, B = torch.empty((rows, Hq, D), dtype=torch.float64, device=DEV), torch.empty((rows, Hq, D), dtype=torch.float64, device=DEV)
+    G = Hq // H
+    for r in range(rows):
+        n = kv - rows + r + 1
+        for h in range(H):
+            q = Q[r, h * G:(h + 1) * G].double()
+            kk, vv = k[:n, h].contiguous(), v[:n, h].contiguous()
+            z = scale * (q @ kk.T.contiguous())
+            e = (z - z.amax(1, keepdim=True)).exp()
+            S = e.sum(1, keepdim=True)
+            w = e / S
+            A = w @ vv.abs()
+            O[r, h * G:(h + 1) * G] = o = w @ vv
+            Z = scale * q.abs().amax(1, keepdim=True) / 32512 * kk.abs().sum(1).max()
+            inner = A * (2.0**-11 + 2 * (1 + Z) * Z + 2.0**-21 * (z.abs().amax(1, keepdim=True) + 1) + n * 2.0**-24)
+            inner = inner + 2.0**-25 * vc[:n, h].abs().sum(0) * vs[:, h].max() / S
+            B[r, h * G:(h + 1) * G] = inner + (o.abs() + inner) * 2.0**-11 + 2.0**-25
+    return O, B
+
+
+@pytest.mark.parametrize("heads, group, rows, kv, path", [
+    (1, 1 << 20, 1, 64, "tiled"),          # the most query heads: one row is 4096 blocks
+    (1, 1000003, 2, 20, "tiled"),
+    (1, 1048573, 1, 33, "tiled"),
+    (2, 300, 3, 100, "few"),               # a row of more columns than a block
+    (65535, 1, 1, 40, "few"),              # the most heads
+    (65535, 5, 2, 17, "few"),
+])
+def test_many_heads(heads, group, rows, kv, path):
+    dim, page = 64, 16
+    torch.manual_seed(group)
+    cache = li8.new_kv_cache(8, heads, dim, page, DEV)
+    whole = li8.KVBatch(i32([0, kv]), i32([kv]), i32([[4, 1, 3, 2, 7, 5, 6]]), kv, kv, kv)
+    K, V = (torch.randn((kv, heads, dim), device=DEV).to(F16) for _ in range(2))
+    li8.kv_append(K, V, cache, whole)
+    for x, got in zip((K, V), li8.kv_read(cache, whole)):
+        # half a step of the page's scale, again where a page grew; one append: once
+        half = x.abs().float().amax(dim=(0, 2)) / 127 / 2 + 2.0**-9
+        assert ((x.float() - got.float()).abs() <= half[None, :, None] * 1.001).all()
+    Q = (torch.randn((rows, heads * group, dim), device=DEV) * 2).to(F16)
+    batch = li8.KVBatch(i32([0, rows]), i32([kv]), whole.table, rows, rows, kv)
+    assert li8.kv_attention_plan(batch, cache, heads * group) == dict(path=path, splits=1)
+    out = li8.kv_attention(Q, cache, batch).double()
+    if heads == 1 or heads == 2:
+        O, B = plain(Q, cache, whole.table[0], kv, dim ** -0.5)
+        assert ((out - O).abs() <= B).all(), ((out - O).abs() / B).max()
+    else:
+        for h in (0, 1, 4095, 4096, 32768, 65534):
+            one = li8.KVCache(*(c[:, h:h + 1].contiguous() for c in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+            O, B = plain(Q[:, h * group:(h + 1) * group], one, whole.table[0], kv, dim ** -0.5)
+            assert ((out[:, h * group:(h + 1) * group] - O).abs() <= B).all(), h
+        # (every head: its own, not its neighbour's)
+        first = out[0, ::group] if group > 1 else out[0]
+        assert (first[1:] != first[:-1]).any(1).all()
+
+
+def test_strided_tables():
+    """Rows of a wider table, as a server's slots are."""
+    ns, ls, heads, dim, page = [3, 1, 40], [50, 2000, 90], 2, 64, 16
+    t = base.Setup(ns, ls, heads, dim, page, F16, rot=64)
+    wide = torch.full((7, t.width + 9), -3, dtype=torch.int32, device=DEV)
+    wide[1::2, 4:4 + t.width] = t.batch.table
+    strided = li8.KVBatch(t.batch.q_start, t.batch.kv_len, wide[1::2, 4:4 + t.width], t.tokens, max(ns), t.max_kv)
+    assert strided.table.stride(0) == 2 * (t.width + 9)
+    Q, K = t.rows(6), t.rows(heads)
+    copy = li8.KVCache(*(c.clone() for c in (t.cache.k, t.cache.v, t.cache.k_scale, t.cache.v_scale)))
+    for batch, cache in ((t.batch, t.cache), (strided, copy)):
+        li8.kv_append(K, K, cache, batch, rope=t.rope)
+    assert torch.equal(copy.k, t.cache.k) and torch.equal(copy.v, t.cache.v)
+    assert torch.equal(li8.kv_attention(Q, copy, strided, rope=t.rope), li8.kv_attention(Q, t.cache, t.batch, rope=t.rope))
+    for a, b in zip(li8.kv_read(copy, strided), li8.kv_read(t.cache, t.batch)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_graph_of_a_chunk(shared):
+    """The tiled kernel, its merge and a read captured, the workspace made inside
+    the capture; replayed with other lengths, rows and pages, eager calls in between."""
+    group = 2
+    rows = base.tiled_blocks([70, 64], 1, group, 0, shared) * 256 // group
+    t = base.Setup([70, 64], [700, 300], 1, 64, 16, F16, rot=64, max_kv=1 << 14, max_q=rows, tail=rows - 134)
+    Q, K = t.rows(group), t.rows(1)
+    out = torch.zeros_like(Q)
+    back = torch.zeros_like(K), torch.zeros_like(K)
+
+    def step():
+        li8.kv_append(K, K, t.cache, t.batch, rope=t.rope)
+        li8.kv_attention(Q, t.cache, t.batch, rope=t.rope, out=out)
+        li8.kv_read(t.cache, t.batch, out=back)
+
+    assert (li8.kv_attention_plan(t.batch, t.cache, group)["splits"] > 1) == shared
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i, (lens, starts) in enumerate((([700, 300], [0, 70, 134]), ([90, 299], [3, 20, 100]), ([650, 64], [0, 1, 65]), ([0, 7], [0, 0, 7]),
+                                        ([700, 300], [0, 70, 134]))):
+        Q.copy_(t.rows(group))
+        K.copy_(t.rows(1, 1 + i))
+        t.batch.kv_len.copy_(i32(lens))
+        t.batch.q_start.copy_(i32(starts))
+        before = tuple(c.clone() for c in (t.cache.k, t.cache.v, t.cache.k_scale, t.cache.v_scale))
+        out.zero_()
+        g.replay()
+        got = out.clone(), back[0].clone(), back[1].clone(), t.cache.k.clone(), t.cache.v_scale.clone()
+        torch.cuda.synchronize()
+        for c, b in zip((t.cache.k, t.cache.v, t.cache.k_scale, t.cache.v_scale), before):
+            c.copy_(b)
+        out.zero_()
+        step()
+        for a, b in zip(got, (out, *back, t.cache.k, t.cache.v_scale)):
+            assert torch.equal(a.nan_to_num(-1) if a.is_floating_point() else a, b.nan_to_num(-1) if b.is_floating_point() else b), i
+        torch.cuda.synchronize()
