@@ -141,7 +141,9 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  * (two int8 parts) times the key codes, exact in int32; the softmax in fp32;
  * the probabilities rounded to fp16 (in some kernels in two parts) times the
  * value codes, summed in fp32.
- *   scale   >= 0 and finite, and such that no |z| reaches 10^29
+ *   scale   >= 0 and below 10^29 (else refused), and such that scale sum |q| |k|
+ *           stays below it for any row and key, |k| as large as its page's
+ *           scale allows (127 of it)
  *   Q, O    [tokens][q_heads][head_dim], rows q_stride, o_stride apart;
  *           O must not alias Q (O == Q is refused)
  *   rope    as for the keys; a negative position (only without `causal`

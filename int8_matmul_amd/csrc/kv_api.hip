@@ -1,7 +1,5 @@
 // Host side of the C ABI declared in include/llm_int8_kv.h: argument checks
 // and kernel launches.  No allocation, no host sync.
-#include <math.h>
-
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -11,6 +9,7 @@ using namespace li8;
 namespace {
 
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+constexpr float kMaxScale = 1.0e29f;     // below it the kernels' log2(e) times the scale is finite
 constexpr int32_t kMaxKeys = 1 << 30;   // positions and a step past them stay below 2^31
 
 bool off_by(const void *p, uintptr_t align) { return ((uintptr_t)p & (align - 1)) != 0; }
@@ -188,7 +187,7 @@ li8_status int8_kv_attention(const void *Q, int64_t q_stride, li8_dtype dtype, i
 {
     LI8_TRY(check_sizes(batch, cache));
     LI8_TRY(check_heads(batch, cache, q_heads, causal, window));
-    if (bad_dtype(dtype) || !isfinite(scale) || scale < 0.0f)
+    if (bad_dtype(dtype) || !(scale >= 0.0f && scale < kMaxScale))   // (NaN is refused too)
         return LI8_ERR_INVALID_ARG;
     KvRope r;
     LI8_TRY(check_rope(rope, batch, cache, &r));

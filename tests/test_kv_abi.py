@@ -326,3 +326,11 @@ def test_more_work_items_than_a_launch_has(lib):
         if seqs < 1 << 30:                                # one (sequence, head) fewer, or eight, is fine
             assert lib.int8_kv_attention_plan(ref(batch(seqs=seqs - 1, **sizes)), ref(c), heads * group, 1, 0, *out) == OK
             assert p.value == path
+
+
+def test_scales_past_the_scores(lib):
+    """From 2.4e38 on scale * log2(e) was infinite, and a query of zeros gave NaN."""
+    for s in (1.0e29, 3.0e38):
+        assert attend(lib, scale=s) == INVALID
+    b = batch(tokens=0, q_start=None, kv_len=None, table=None)
+    assert attend(lib, b=b, scale=9.9e28) == OK
