@@ -34,9 +34,13 @@
  *     pages of q tokens of 2^24 on, read from seqs x ceil(q / 64) of 2^24 on,
  *     attention from seqs x heads x blocks of columns of 2^23 on (at the
  *     earliest; smaller workgroups go further).
- *   - Inputs must be finite where they are read; the scales of pages with
- *     stored tokens finite and >= 0.  Codes and scales of tokens that no query sees,
- *     and rows outside [q_start[0], q_start[seqs]), may hold anything.
+ *   - Inputs must be finite where they are read (keys and queries after their
+ *     rotation too); the scales of pages with stored tokens >= 0 and below 2^126
+ *     (append writes none above 2^121).  Codes and scales of tokens that no
+ *     query sees, and rows outside [q_start[0], q_start[seqs]), may hold
+ *     anything.
+ *   - Lengths, starts and page numbers must not change while a call runs (work
+ *     on other streams that changes them has to wait for it).
  */
 #ifndef LLM_INT8_KV_H
 #define LLM_INT8_KV_H
@@ -110,7 +114,8 @@ typedef struct li8_rope {
  *   K, V    [tokens][heads][head_dim], rows k_stride, v_stride apart
  *   rope    NULL: keys are stored as they are
  * Tokens at negative positions (kv_len[s] < n) are left out.  A page must
- * not be written for two sequences of the batch.  Codes of a page behind
+ * not be written twice in a batch, for two sequences or for two places in the
+ * table row of one.  Codes of a page behind
  * the sequence's last token, and pages that hold no new token, keep their
  * contents.  Appending the same tokens twice gives the same cache.
  */
@@ -136,7 +141,8 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  *   z[t] = scale * (rotated q) . (k code * k scale)
  *   O    = sum_t softmax(z)[t] * (v code * v scale)     over the seen keys
  *   lse  = log sum_t exp(z[t])                          (natural logarithm)
- * A row that sees nothing gets O = 0 and lse = -inf.  The products run on
+ * A row that sees nothing gets O = 0 and lse = -inf; rows of no sequence, and
+ * those of a chunk past max_q, are not written.  The products run on
  * the matrix units: q as 15-bit integers of its row's largest magnitude
  * (two int8 parts) times the key codes, exact in int32; the softmax in fp32;
  * the probabilities rounded to fp16 (in some kernels in two parts) times the
@@ -158,6 +164,10 @@ li8_status int8_kv_read(const li8_kv_cache *cache, const li8_kv_batch *batch, li
  * more than 2^10 apart cost the pages with the small ones precision: their
  * probabilities are held in fp16 relative to the largest scale so far.
  * Value scales below 2^-126 count as 0.
+ * One kernel runs for the whole batch, chosen by its longest chunk: single
+ * tokens over long sequences are better put into a call of their own than
+ * beside a prompt's chunk (one of 131071 keys beside a chunk of 512 over 2048:
+ * 3264 us, apart 56 and 65).
  */
 size_t int8_kv_attention_workspace_bytes(const li8_kv_batch *batch, const li8_kv_cache *cache,
                                          int32_t q_heads);

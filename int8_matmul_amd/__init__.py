@@ -864,7 +864,9 @@ def kv_attention(Q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float |
     ``scale`` defaults to 1/sqrt(head_dim); ``rope`` rotates Q on the way;
     ``window`` > 0 lets a row see its own and the window - 1 tokens before;
     ``lse`` fp32 [tokens, q_heads] receives the log of each row's sum (-inf
-    for a row that sees no key; its output is 0)."""
+    for a row that sees no key; its output is 0).  Rows of no sequence, and
+    those of a chunk past max_q, are not written.  Single tokens over long
+    sequences are faster in a call of their own than beside a prompt's chunk."""
     _kv_place(batch, cache, rope)
     D = cache.head_dim
     qs = _kv_tokens(Q, "Q", batch, None, D)

@@ -9,8 +9,9 @@
 //                            15-bit integer of its row's largest magnitude,
 //                            q = f (128 qh + ql); the sums are exact
 //   O^T[d, col]  += V^T P^T  fp16 MFMA: the codes are exact in fp16, the
-//                            probabilities are rounded to it (11 bits, or
-//                            22 in two parts)
+//                            probabilities are rounded to it (11 bits; in
+//                            two parts 22 bits, or 2^-25 of the largest
+//                            where that is more)
 // The transposed form leaves a column in the lanes that hold it as the next
 // product's operand: with the keys of a step of 32 numbered so that lane
 // group g has keys 4g..4g+3 and 16+4g..16+4g+3, the scores' accumulator
@@ -36,7 +37,12 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 constexpr float kNone = -1.0e30f;      // a running maximum over nothing yet
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kQMax = 16256.0f;      // 127 * 128: the largest 15-bit query integer
-constexpr int kLeastSteps = 8;         // fewest steps of a workgroup that shares
+// Fewest steps of a workgroup that shares: a part costs its prologue and its
+// merge.  With 4, 8 and 16 (us): 8 heads of a group of 8, one token over 1500 keys
+// 14.5, 16.1, 18.4, 4000 keys 15.4, 17.3, 19.2, 16000 keys 20.5, 20.6, 19.9; one
+// head of 16 over 20000 keys 14.0, 13.7, 14.7; with more steps than 8 for each
+// workgroup no difference.
+constexpr int kLeastSteps = 8;
 
 struct AttnArgs {
     KvTokens Q;
@@ -434,7 +440,9 @@ __device__ __forceinline__ void load_step(Step<D> &st, const KvArgs &a, const in
 // (two and three steps ahead were slower: registers, and no fewer waits).
 // Bound by reading the cache once: 64 sequences of up to 8192 tokens, 8 heads
 // of a group of 8, one token each, 701 MB: 127 us with the merge, 5.5 TB/s (a
-// copy of 2 GiB moves 4.8); one sequence of 131071 tokens, 268 MB: 51 us.
+// copy of 2 GiB moves 5.0, read and written); one sequence of 131071 tokens,
+// 268 MB: 51 us.  (Several such caches in turn, so that none of it is in the
+// Infinity Cache: 1 % more.  fp16 and bf16 take the same.)
 // Short calls are bound by the chain of loads (lengths, page number, step) and
 // the launch: one token of 32 heads over 777 keys 11.9 us.
 // ---------------------------------------------------------------------------
@@ -444,9 +452,11 @@ __device__ __forceinline__ void few_block(const KvArgs &a, const AttnArgs &t, co
 {
     constexpr int CPR = D / 8, NB = D / 16, KS = D / 64, LQ = D + 16, LO = D + 4, COLS = kKvCols * NC;
     constexpr int kStride = 32 * NW;
-    // fp16 outputs: the probabilities in two parts, 22 bits, so that only the
-    // output's own rounding shows (error 2.2e-4 of the output's norm against
-    // 2.9e-4, 2.1e-4 of it from that rounding).  One token of 40 heads x 16
+    // fp16 outputs: the probabilities in two parts, so that only the output's
+    // own rounding shows (error 2.2e-4 of the output's norm against 2.9e-4,
+    // 2.1e-4 of it from that rounding).  22 bits for probabilities of 2^-3 of
+    // the maximum and more; the second part of smaller ones is subnormal and
+    // off by 2^-25 of it, which leaves 14 bits of a probability of 2^-10.  One token of 40 heads x 16
     // sequences takes 89.3 us either way, as reading the cache hides the
     // second product; one token of 32 heads over 1000 keys 11.9 against 11.3.
     // With 32 columns a workgroup is bound by its instructions (a prompt of
@@ -700,14 +710,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_few(KvArgs a, AttnArgs t)
 // its keys in steps of 64 that all waves read from LDS.  K stays int8 there
 // (16 MFMAs 32x32x32 i8 per step and wave for the two query parts), V is
 // turned into fp16 and transposed on its way in, once for all waves.
-// A prompt of 4096 tokens, 32 heads, D = 128: 167 us, 825 TFLOP/s by the
+// A prompt of 4096 tokens, 32 heads, D = 128: 166 us, 830 TFLOP/s by the
 // formula's products (158 to 168 on four boards); a chunk of 512 tokens in each
 // of 4 sequences of 8192, 8 heads of a group of 8: 548 us, 1000 TFLOP/s.  (In
 // bursts of 8 calls, while the clock ramps up, 185 and 670 us.)  The matrix
 // units are busy for a third of the time and the vector ALUs for half of it;
 // with the exponentials left out, or the staging, or the reads of LDS, or the
-// second product, the time falls by 5 to 16 % each, so no one of them alone
-// is the bound.
+// second product, the time falls by 11, 10, 5 and 10 % at the prompt (by 14, 16,
+// 11 and 15 % at the chunks), so no one of them alone is the bound.
 // ---------------------------------------------------------------------------
 constexpr int kTileWaves = 8;
 constexpr int kTileCols = 32 * kTileWaves;
@@ -1141,7 +1151,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void k_kv_tiled(KvArgs a, AttnA
         // the lane before any block that sees fewer: a long block that starts
         // late would run alone at the end.  Chunks over much longer sequences
         // have blocks alike, and one pair goes after the other, so that its
-        // keys stay in the L2.
+        // keys stay in the L2.  Measured, pair by pair : longest first (us):
+        //   longest first up to half of the sequence: prompts of 4096 with 32
+        //   heads 228 : 167, 4096 of 8000 486 : 428, 8 x 1024 of 1500 193 : 160;
+        //   but 4 x 2048 of 4000, 8 heads of a group of 8, 718 : 823
+        //   pair by pair past it, groups of 8: 4 x 512 of 8192 411 : 477, 1024
+        //   of 4096 387 : 467, 2048 of 4300 783 : 898; but 32 heads of one:
+        //   4096 of 8300 509 : 451, 8 x 512 of 2048 149 : 139
         const int j = blockIdx.x / lanes, ppl = (pairs + lanes - 1) / lanes;
         const int pair = (deep ? j / t.blocks : j % ppl) * lanes + blockIdx.x % lanes;
         if (pair >= pairs)
@@ -1254,7 +1270,9 @@ __device__ __forceinline__ void merge_column(const KvArgs &a, const AttnArgs &t,
 // m_i the part's log2 of its sum.  SL lanes of parts x D/8 chunks work on a
 // column: with many parts the workgroup, else a wave, or (SL = 1, where blocks
 // are wide and in few parts) D/8 lanes of it.  A wave has `each` columns of
-// one block; four parts are in flight per lane.  64 sequences' one token each
+// one block; four parts are in flight per lane.  The workgroup from 15 parts for
+// each block on: with 64 the call takes 53.7 us against 55.5 with a wave, with 1
+// (512 blocks) 155 against 146, between 4 and 16 no difference.  64 sequences' one token each
 // (512 blocks of 8 columns, up to 4 parts) takes 7.8 us, 8 blocks of 64 parts
 // 4.9: the launch and two chains of loads, lengths and then parts.
 template <int D, bool BF16, int SL, int SHIFT>
@@ -1300,6 +1318,11 @@ __global__ __launch_bounds__(256) void k_kv_merge(KvArgs a, AttnArgs t, int item
 //   up to 4096 keys 52 : 69, twice as many 83 : 72.
 //   few columns are shared past 40 steps of 32 keys: at 25 steps one launch
 //   took 11.3 against 18.3, at 41 to 4096 sharing is up to 4 times as fast.
+//   From 4096 blocks on (8 for each workgroup that would share) they are not:
+//   one token each, whole : shared, 128 sequences x 32 heads of 300 to 4000 keys
+//   394 : 461, 512 x 8 heads of a group of 8 406 : 584, of 2000 keys each 390 :
+//   415 (32 heads 370 : 353).  One sequence of 131071 keys among 127 of 1000
+//   then runs alone at the end, 928 : 377; the host does not see the lengths.
 //   tiled blocks are shared where there are fewer than CUs: 64 blocks of 128
 //   steps 97 against 242 unshared, 256 blocks of a 2048-token prompt 77
 //   against 72 (their keys differ, which the count of steps does not know).
@@ -1323,7 +1346,11 @@ int64_t plan_items(const li8_kv_batch &b, const li8_kv_cache &c, const KvPlan &p
 // fewer where that would leave XCDs without work.
 int tiled_lanes(int64_t pairs) { return pairs >= 64 ? 8 : (int)std::min<int64_t>(8, pairs & -pairs); }
 
-// Work-items of an unshared few-column workgroup.
+// Work-items of an unshared few-column workgroup: 8 waves where blocks are few,
+// measured 8 : 4 (us): 5 tokens of 4 heads of a group, D = 64, 1200 keys, in 128
+// blocks 12.7 : 14.6, in 256 14.2 : 15.7; one token of 32 heads over 777 keys
+// 11.5 : 11.5; 768 blocks of 1200 keys 48 : 39.  At 512 blocks 4 are ahead already
+// (34 : 29; a 512-token prompt 22 : 17).
 int few_items(int64_t items) { return items <= 512 ? 512 : 256; }
 
 template <int D, bool BF16>

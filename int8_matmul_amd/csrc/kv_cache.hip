@@ -9,15 +9,18 @@
 // workgroup owns one (page, head): it keeps its rows in registers between the
 // maximum and the codes, and every value is read once (the rotation's partner
 // half comes from the cache line that another lane of the row has fetched).
-// What bounds it: 2 bytes read and 1 written per value, so HBM for a prompt
-// (chunks of 5622 tokens, 40 heads, D = 128: 30 us, 173 MB, 5.7 TB/s); for one
-// token per sequence the launch and one chain of dependent loads (lengths,
-// page number, scale and row): 3.4 us for 8 sequences, 4.4 for 256.
+// What bounds it: 2 bytes read and 1 written per value, so memory for a prompt
+// (chunks of 5622 tokens, 40 heads, D = 128, 173 MB: 39 us, 4.5 TB/s, where a copy
+// has 5.0; 30 us over again on the same tokens, which are in the Infinity Cache
+// then); for one token per sequence the launch and one chain of dependent loads
+// (lengths, page number, scale and row): 3.4 us for 8 sequences, 4.4 for 256.
 //
 // Read: one thread per 8 codes, K and V in one launch, 1 byte read and 2
 // written per value, with non-temporal stores: lines left dirty in the L2 are
 // written back when the kernel ends, and the next one waits for that (four
-// sequences of up to 8191 tokens, 176 MB moved: 41.9 -> 26.9 us, 6.5 TB/s).
+// sequences of up to 8191 tokens, 176 MB moved: 41.9 -> 26.9 us over again on the
+// same pages, whose 59 MB the Infinity Cache holds; on other pages each time
+// 39.6 us, 4.4 TB/s).
 #include <float.h>
 
 #include <algorithm>
