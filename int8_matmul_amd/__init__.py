@@ -38,6 +38,8 @@ __all__ = [
     "gemm_cached", "STATUS",
     "KVCache", "KVBatch", "Rope", "new_kv_cache", "kv_append", "kv_read", "kv_attention",
     "kv_attention_plan", "kv_attention_workspace_bytes", "new_kv_attention_workspace",
+    "linear_epilogue", "gated_linear", "linear_backward", "gated_backward",
+    "backward_workspace_bytes", "new_backward_workspace", "ACTIVATIONS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -145,6 +147,17 @@ def load_library() -> ctypes.CDLL:
     L.int8_kv_attention.restype = ctypes.c_int
     L.int8_kv_attention.argtypes = [vp, i64, ctypes.c_int, i32, ctypes.c_float, vp, i32, i32, vp, vp,
                                     vp, i64, vp, vp, sz, vp]
+    L.llm_int8_linear_epilogue.restype = ctypes.c_int
+    L.llm_int8_linear_epilogue.argtypes = [vp, vp, vp, ctypes.c_float, i64, i64, i64, vp, i32, vp, vp, vp, vp,
+                                           sz, vp]
+    L.llm_int8_gated_linear.restype = ctypes.c_int
+    L.llm_int8_gated_linear.argtypes = [vp, vp, vp, ctypes.c_float, i64, i64, i64, vp, i32, vp, vp, vp, sz, vp]
+    L.llm_int8_backward_workspace_bytes.restype = sz
+    L.llm_int8_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    L.llm_int8_linear_backward.restype = ctypes.c_int
+    L.llm_int8_linear_backward.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    L.llm_int8_gated_backward.restype = ctypes.c_int
+    L.llm_int8_gated_backward.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -894,3 +907,160 @@ def kv_attention(Q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float |
              int(bool(causal)), _int32(window, "window"), batch._ref, cache._ref, out.data_ptr(), os_,
              _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out
+
+
+# ---------------------------------------------------------------------------
+# The feed-forward operators (include/llm_int8_ffn.h)
+# ---------------------------------------------------------------------------
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _fitted(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tuple, device) -> torch.Tensor | None:
+    """Checks an optional tensor of a known shape on a known device."""
+    if t is not None:
+        _require(t, dtype, name, len(shape))
+        if tuple(t.shape) != shape or t.device != device:
+            raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _weight(Wq: torch.Tensor, sW: torch.Tensor, device, gated: bool) -> tuple:
+    _require(Wq, torch.int8, "Wq", 2)
+    N, K = Wq.shape
+    _require(sW, torch.float32, "sW", 1)
+    if sW.shape[0] != N:
+        raise ValueError(f"shape mismatch: Wq {tuple(Wq.shape)}, sW {tuple(sW.shape)}")
+    if gated and N % 2:
+        raise ValueError(f"a gated pair's weight has an even number of rows, got {N}")
+    for name, t in (("Wq", Wq), ("sW", sW)):
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return N, K
+
+
+def _scratch(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _require(workspace, torch.uint8, "workspace", 1)
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    return workspace
+
+
+def linear_epilogue(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold: float = 6.0,
+                    bias: torch.Tensor | None = None, activation: str = "none",
+                    residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    pre: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Y fp16 [T,N] = act(Z + bias) + residual, Z the product of ``linear``, rounded once.
+
+    ``bias`` fp16 [N]; ``activation`` one of ACTIVATIONS; ``residual`` fp16 [T,N],
+    which may be ``out`` itself; ``pre`` fp16 [T,N] receives Z + bias for
+    ``linear_backward``.  The workspace is that of ``linear``."""
+    _require(X, torch.float16, "X", 2)
+    T, K = X.shape
+    dev = X.device
+    N, KW = _weight(Wq, sW, dev, False)
+    if KW != K:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Wq {tuple(Wq.shape)}")
+    act = _activation(activation)
+    _fitted(bias, torch.float16, "bias", (N,), dev)
+    _fitted(residual, torch.float16, "residual", (T, N), dev)
+    _fitted(pre, torch.float16, "pre", (T, N), dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.float16, device=dev)
+    else:
+        _fitted(out, torch.float16, "out", (T, N), dev)
+    ws = _scratch(workspace, 0 if workspace is not None else linear_workspace_bytes(T, K, N), dev)
+    _kv_call("llm_int8_linear_epilogue", dev, X.data_ptr(), Wq.data_ptr(), sW.data_ptr(), float(threshold), T, K, N,
+             _ptr(bias), act, _ptr(residual), out.data_ptr(), _ptr(pre), ws.data_ptr(), ws.numel())
+    return out
+
+
+def gated_linear(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold: float = 6.0,
+                 bias: torch.Tensor | None = None, activation: str = "silu", out: torch.Tensor | None = None,
+                 pre: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """H fp16 [T,F] = act(G) * U, [G | U] = Z + bias with the pair's weight Wq [2F,K]
+    (the gate's F rows, then the up-projection's).
+
+    ``bias`` fp16 [2F]; ``pre`` fp16 [T,2F] receives [G | U] for ``gated_backward``.
+    The workspace is that of ``linear`` for N = 2F."""
+    _require(X, torch.float16, "X", 2)
+    T, K = X.shape
+    dev = X.device
+    N, KW = _weight(Wq, sW, dev, True)
+    if KW != K:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Wq {tuple(Wq.shape)}")
+    F = N // 2
+    act = _activation(activation)
+    _fitted(bias, torch.float16, "bias", (N,), dev)
+    _fitted(pre, torch.float16, "pre", (T, N), dev)
+    if out is None:
+        out = torch.empty((T, F), dtype=torch.float16, device=dev)
+    else:
+        _fitted(out, torch.float16, "out", (T, F), dev)
+    ws = _scratch(workspace, 0 if workspace is not None else linear_workspace_bytes(T, K, N), dev)
+    _kv_call("llm_int8_gated_linear", dev, X.data_ptr(), Wq.data_ptr(), sW.data_ptr(), float(threshold), T, K, F,
+             _ptr(bias), act, out.data_ptr(), _ptr(pre), ws.data_ptr(), ws.numel())
+    return out
+
+
+def backward_workspace_bytes(T: int, K: int, N: int) -> int:
+    """Bytes of workspace for the gradients through a weight [N,K] (N = 2F for a pair)."""
+    return int(load_library().llm_int8_backward_workspace_bytes(T, K, N))
+
+
+def new_backward_workspace(T: int, K: int, N: int, device) -> torch.Tensor:
+    return torch.empty(backward_workspace_bytes(T, K, N), dtype=torch.uint8, device=device)
+
+
+def _backward(name: str, dY, pre, Wq, sW, activation, out, grad_pre, dbias, workspace, gated):
+    _require(dY, torch.float16, "dH" if gated else "dY", 2)
+    dev = dY.device
+    N, K = _weight(Wq, sW, dev, gated)
+    T, F = dY.shape
+    if F * (2 if gated else 1) != N:
+        raise ValueError(f"shape mismatch: {'dH' if gated else 'dY'} {tuple(dY.shape)}, Wq {tuple(Wq.shape)}")
+    act = _activation(activation)
+    if pre is None and (gated or act):
+        raise TypeError("pre must be a torch.Tensor")
+    _fitted(pre, torch.float16, "pre", (T, N), dev)
+    _fitted(grad_pre, torch.float16, "grad_pre", (T, N), dev)
+    _fitted(dbias, torch.float32, "dbias", (N,), dev)
+    if out is None:
+        out = torch.empty((T, K), dtype=torch.float16, device=dev)
+    else:
+        _fitted(out, torch.float16, "out", (T, K), dev)
+    ws = _scratch(workspace, 0 if workspace is not None else backward_workspace_bytes(T, K, N), dev)
+    _kv_call(name, dev, dY.data_ptr(), _ptr(pre), act, Wq.data_ptr(), sW.data_ptr(), T, K, F, out.data_ptr(),
+             _ptr(grad_pre), _ptr(dbias), ws.data_ptr(), ws.numel())
+    return out
+
+
+def linear_backward(dY: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, pre: torch.Tensor | None = None,
+                    activation: str = "none", out: torch.Tensor | None = None, grad_pre: torch.Tensor | None = None,
+                    dbias: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dX fp16 [T,K] of ``linear_epilogue`` (or ``linear``) for dY fp16 [T,N]: the gradient
+    through the dequantized, frozen weight, dX = dZ . (Wq * sW), dZ = dY * act'(pre).
+
+    ``pre`` fp16 [T,N] as the forward call stored it (not read without an
+    activation); ``grad_pre`` fp16 [T,N] receives dZ, ``dbias`` fp32 [N] its column
+    sums.  The residual's gradient is dY itself."""
+    return _backward("llm_int8_linear_backward", dY, pre, Wq, sW, activation, out, grad_pre, dbias, workspace, False)
+
+
+def gated_backward(dH: torch.Tensor, pre: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor,
+                   activation: str = "silu", out: torch.Tensor | None = None, grad_pre: torch.Tensor | None = None,
+                   dbias: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dX fp16 [T,K] of ``gated_linear`` for dH fp16 [T,F]: dG = dH U act'(G), dU = dH act(G),
+    dX = [dG | dU] . (Wq * sW).
+
+    ``pre`` fp16 [T,2F] as the forward call stored it; ``grad_pre`` fp16 [T,2F]
+    receives [dG | dU], ``dbias`` fp32 [2F] their column sums."""
+    return _backward("llm_int8_gated_backward", dH, pre, Wq, sW, activation, out, grad_pre, dbias, workspace, True)

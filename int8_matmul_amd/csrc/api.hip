@@ -41,6 +41,10 @@ __global__ void k_stage_flags_xo(const uint32_t *__restrict__ bits, const int32_
         }
 }
 
+} // namespace
+
+namespace li8 {
+
 li8_status check_shape(int64_t T, int64_t K, int64_t N)
 {
     if (T < 0 || K < 0 || N < 0)
@@ -60,6 +64,10 @@ li8_status check_shape(int64_t T, int64_t K, int64_t N)
     return LI8_OK;
 }
 
+} // namespace li8
+
+namespace {
+
 // Exact value of a binary16 magnitude pattern (0 <= m <= 0x7c00).
 double half_mag_value(uint32_t m)
 {
@@ -70,6 +78,10 @@ double half_mag_value(uint32_t m)
         return INFINITY;
     return ldexp((double)(f | 0x400u), (int)e - 25);
 }
+
+} // namespace
+
+namespace li8 {
 
 // Largest binary16 magnitude pattern H whose value is <= thr (thr >= 0),
 // so that |x| > thr  <=>  (bits(x) & 0x7fff) > H for finite x.
@@ -87,6 +99,10 @@ uint16_t threshold_magnitude(float thr)
     }
     return (uint16_t)lo;
 }
+
+} // namespace li8
+
+namespace {
 
 li8_status from_hip(hipError_t e) { return e == hipSuccess ? LI8_OK : LI8_ERR_HIP; }
 

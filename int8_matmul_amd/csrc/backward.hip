@@ -1,0 +1,692 @@
+// Gradients through the frozen int8 weight, for gfx950.
+//
+//   dZ[t,n] = dY[t,n] act'(Z[t,n])                      (linear)
+//   dZ      = [ dH U act'(G) | dH act(G) ]              (gated pair, N = 2F)
+//   dX[t,k] = sum_n dZ[t,n] sW[n] Wq[n,k],   dbias[n] = sum_t dZ[t,n]
+//
+// 1. k_grad_rows, one workgroup per token row: dZ in fp32 from the fp16 inputs,
+//    the row's largest |dZ sW|, and the product's operand
+//    A[t,n] = fp16(dZ sW 2^(14 - e)) with e that maximum's exponent: the scale sW
+//    sits on the contracted index, so it has to go into one of the operands,
+//    and a power of two for each row costs no rounding and keeps gradients of
+//    any size inside fp16 (values down to 2^-28 of the row's largest keep all
+//    11 bits).  One rounding of each element, 2^-11 at most, is what the matrix
+//    instructions' 16-bit operands need; the codes are exact in fp16.
+// 2. k_grad_gemm: dX = A . Wq on v_mfma_f32_32x32x16_f16 (fp32 sums), codes
+//    converted on the way from LDS to the registers; times 2^(e - 14).
+// 3. k_grad_join where the contraction was split between workgroups.
+// dbias: k_grad_cols and k_cols_join, only where asked for.
+#include <algorithm>
+
+#include "li8_internal.h"
+#include "quant_math.h"
+#include "tile_common.h"
+
+namespace li8 {
+namespace {
+
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------------------
+// Elementwise part: eight features f .. f+7 of a row.
+// ---------------------------------------------------------------------------
+
+// Eight fp16 values at p, as fp32; `n` of them exist (VEC: all or none, and p is
+// 16-byte aligned), the others are 0.
+template <bool VEC>
+__device__ __forceinline__ void load8(const uint16_t *p, int n, float (&v)[8])
+{
+    uint32_t w[4] = {0, 0, 0, 0};
+    if constexpr (VEC) {
+        if (n > 0) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (e < n)
+                w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        v[e] = h2f((w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t *p, int n, const float (&v)[8])
+{
+    const uint32_t w[4] = {pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                           pack_f16x2(v[6], v[7])};
+    if constexpr (VEC) {
+        if (n > 0)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (e < n)
+                p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+struct GradArgs {
+    const uint16_t *dY;    // [T, F] (F = N, or N / 2 for a pair)
+    const uint16_t *pre;   // [T, N], or null (linear: slope 1)
+    const float *sW;
+    uint16_t *grad_pre;    // [T, N], or null
+    ActParams act;
+    int T, N, Np;
+};
+
+// dZ of eight features: z[0] (linear), or z[0] the gate's and z[1] the up
+// projection's (pair).
+template <bool GATED, int KIND, bool VEC>
+__device__ __forceinline__ void grad8(const GradArgs &a, int64_t t, int f, float (&z)[1 + GATED][8])
+{
+    const int F = GATED ? a.N >> 1 : a.N, n = F - f;
+    float d[8], g[8];
+    load8<VEC>(a.dY + t * F + f, n, d);
+    if constexpr (GATED) {
+        float u[8];
+        load8<VEC>(a.pre + t * a.N + f, n, g);
+        load8<VEC>(a.pre + t * a.N + F + f, n, u);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            float v, s;
+            act_value_slope<KIND>(g[e], a.act, v, s);
+            z[0][e] = d[e] * u[e] * s;
+            z[1][e] = d[e] * v;
+        }
+    } else {
+        if (a.pre) {
+            load8<VEC>(a.pre + t * a.N + f, n, g);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                float v, s;
+                act_value_slope<KIND>(g[e], a.act, v, s);
+                z[0][e] = d[e] * s;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                z[0][e] = d[e];
+        }
+    }
+}
+
+constexpr int kRowThreads = 512;   // k_grad_rows: 4096 features a round
+
+// NR > 0: the row's NR rounds stay in registers between the maximum and the
+// conversion; 0: rows of any length, computed a second time.
+template <bool GATED, int KIND, bool VEC, int NR>
+__global__ __launch_bounds__(kRowThreads) void k_grad_rows(GradArgs a, uint16_t *__restrict__ A,
+                                                           float *__restrict__ fac)
+{
+    constexpr int P = 1 + GATED;
+    __shared__ uint32_t wmax[kRowThreads / 64];
+    const int tid = threadIdx.x;
+    const int F = GATED ? a.N >> 1 : a.N;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        float keep[NR > 0 ? NR : 1][P][8];
+        uint32_t m = 0;   // largest magnitude as bits (NaN above all)
+        auto scaled = [&](int f, float (&z)[P][8]) {
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+                float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if constexpr (VEC) {
+                    if (f < F) {
+                        const float4 lo = *reinterpret_cast<const float4 *>(a.sW + p * F + f);
+                        const float4 hi = *reinterpret_cast<const float4 *>(a.sW + p * F + f + 4);
+                        s[0] = lo.x, s[1] = lo.y, s[2] = lo.z, s[3] = lo.w;
+                        s[4] = hi.x, s[5] = hi.y, s[6] = hi.z, s[7] = hi.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (f + e < F)
+                            s[e] = a.sW[p * F + f + e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    z[p][e] *= s[e];
+            }
+        };
+        auto first = [&](int f, float (&z)[P][8]) {
+            grad8<GATED, KIND, VEC>(a, t, f, z);
+            if (a.grad_pre)
+#pragma unroll
+                for (int p = 0; p < P; p++)
+                    store8<VEC>(a.grad_pre + t * a.N + p * F + f, F - f, z[p]);
+            scaled(f, z);
+#pragma unroll
+            for (int p = 0; p < P; p++)
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    m = max(m, __builtin_bit_cast(uint32_t, z[p][e]) & 0x7fffffffu);
+        };
+        if constexpr (NR > 0) {
+#pragma unroll
+            for (int r = 0; r < NR; r++)
+                first(8 * (tid + r * kRowThreads), keep[r]);
+        } else {
+            for (int f = 8 * tid; f < F; f += 8 * kRowThreads)
+                first(f, keep[0]);
+        }
+        m = wave_max(m);
+        if ((tid & 63) == 0)
+            wmax[tid >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kRowThreads / 64; w++)
+            m = max(m, wmax[w]);
+        // biased exponent e of the maximum: the scale 2^(14 - e), its inverse for the
+        // product.  (Below 2^-107 the scale stays at 2^121; an all-zero row and
+        // one with infinities or NaN take 1.)
+        const uint32_t e8 = m >> 23;
+        const bool one = m == 0 || e8 == 255;
+        const uint32_t ec = max(e8, 20u);
+        const float scale = one ? 1.0f : __builtin_bit_cast(float, (268u - ec) << 23);
+        if (tid == 0)
+            fac[t] = one ? 1.0f : __builtin_bit_cast(float, (ec - 14u) << 23);
+        auto put = [&](int f, float (&z)[P][8]) {
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    z[p][e] *= scale;
+                    asm("" : "+v"(z[p][e]));   // (no product and conversion in one: equal on both ways here)
+                }
+                store8<VEC>(A + t * a.Np + p * F + f, F - f, z[p]);
+            }
+        };
+        if constexpr (NR > 0) {
+#pragma unroll
+            for (int r = 0; r < NR; r++)
+                put(8 * (tid + r * kRowThreads), keep[r]);
+        } else {
+            for (int f = 8 * tid; f < F; f += 8 * kRowThreads) {
+                grad8<GATED, KIND, VEC>(a, t, f, keep[0]);
+                scaled(f, keep[0]);
+                put(f, keep[0]);
+            }
+        }
+        if (tid < a.Np - a.N)   // (less than 64)
+            A[t * a.Np + a.N + tid] = 0;
+        __syncthreads();   // (wmax is read)
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dbias: 64 lanes x 8 features a workgroup, its 4 waves and the strips of the
+// grid share the rows; partial sums [strips][N] added in order by k_cols_join.
+// ---------------------------------------------------------------------------
+constexpr int kColThreads = 256;
+
+template <bool GATED, int KIND, bool VEC>
+__global__ __launch_bounds__(kColThreads) void k_grad_cols(GradArgs a, float *__restrict__ part)
+{
+    constexpr int P = 1 + GATED;
+    __shared__ float sum[kColThreads / 64][P][512];
+    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+    const int F = GATED ? a.N >> 1 : a.N, f = (int)blockIdx.x * 512 + 8 * lane;
+    const int strips = gridDim.y;
+    const int t0 = (int)((int64_t)a.T * blockIdx.y / strips), t1 = (int)((int64_t)a.T * (blockIdx.y + 1) / strips);
+    float s[P][8];
+#pragma unroll
+    for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            s[p][e] = 0.0f;
+    if (f < F)
+        for (int t = t0 + wid; t < t1; t += kColThreads / 64) {
+            float z[P][8];
+            grad8<GATED, KIND, VEC>(a, t, f, z);
+#pragma unroll
+            for (int p = 0; p < P; p++)
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    s[p][e] += z[p][e];
+        }
+#pragma unroll
+    for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            sum[wid][p][8 * lane + e] = s[p][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < P * 512; i += kColThreads) {
+        const int p = i >> 9, c = i & 511, n = (int)blockIdx.x * 512 + c;
+        if (n < F) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kColThreads / 64; w++)
+                v += sum[w][p][c];
+            part[(int64_t)blockIdx.y * a.N + p * F + n] = v;
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void k_cols_join(const float *__restrict__ part, int strips, int N,
+                                                   float *__restrict__ dbias)
+{
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= N)
+        return;
+    float v = 0.0f;
+    for (int s = 0; s < strips; s++)
+        v += part[(int64_t)s * N + n];
+    dbias[n] = v;
+}
+
+// ---------------------------------------------------------------------------
+// The product.  BM x 256 tiles of dX [T,K]; the contraction in stages of 64
+// weight rows held in a ring of NS LDS buffers: A rows of 128 bytes, and the
+// weight's 64 rows of 256 codes as they lie in memory.  The matrix
+// instruction wants eight consecutive n of one column k in a lane, so the codes
+// are read with the transposing LDS read (ds_read_b64_tr_b8: 16 lanes read 8 rows
+// of 16 bytes and each gets one column): no second, transposed copy of the weight.
+// Chunks of 16 codes are permuted in a row by twice the row's index so that
+// the 8 rows of a read and its two neighbouring chunks meet all 64 banks once.
+// Stages, waits and the tile order are those of k_gemm (gemm.hip).
+// ---------------------------------------------------------------------------
+constexpr int kGN = 64;    // weight rows per stage
+constexpr int kGK = 256;   // columns of dX per tile
+
+// Eight codes as fp16.  0x6400 | u is 1024 + u for a byte u, and with its sign bit
+// flipped a code is u - 128, so 1152 less is the code, exactly.
+__device__ __forceinline__ v8h codes_to_f16(v2i w)
+{
+    const v2h off = {(_Float16)1152.0f, (_Float16)1152.0f};
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t u = (uint32_t)w[i] ^ 0x80808080u;
+        r[2 * i] = __builtin_bit_cast(
+            int, __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - off);
+        r[2 * i + 1] = __builtin_bit_cast(
+            int, __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - off);
+    }
+    return __builtin_bit_cast(v8h, r);
+}
+
+__device__ __forceinline__ v2i read_codes_tr(const int8_t *p)
+{
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((LI8_LDS v2i *)(uintptr_t)(LI8_LDS int8_t *)p);
+}
+
+template <int BM, int NS, int WM, int WN, int GM, bool SPLIT>
+__global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
+    const uint16_t *__restrict__ A, const int8_t *__restrict__ Wq, const float *__restrict__ fac,
+    int T, int K, int N, int Np, int tiles_m, int tiles_k, int splits, uint16_t *__restrict__ dX,
+    float *__restrict__ part)
+{
+    constexpr int NT = WM * WN * 64, NW = WM * WN;
+    constexpr int FM = BM / (WM * 32), FK = kGK / (WN * 32);
+    constexpr int KS = kGN / 16;                       // MFMA k-steps per stage
+    constexpr int ASZ = BM * kGN * 2, SSZ = ASZ + kGN * kGK;
+    constexpr int CA = BM * 8, CB = kGN * 16;          // 16-byte chunks of a stage
+    constexpr int LA = (CA + NT - 1) / NT, LB = CB / NT;
+    constexpr int CPR = FK * 4;                        // 16-byte chunks per staging row
+    constexpr int STG = NW * FM * 32 * CPR * 16;
+    constexpr int LDSB = NS * SSZ > STG ? NS * SSZ : STG;
+    static_assert(FM * WM * 32 == BM && FK * WN * 32 == kGK, "tile shape");
+    static_assert(LB * NT == CB && (LA * NT == CA || (LA == 1 && NT % CA == 0 && CA % 64 == 0)), "loader shape");
+    static_assert(LDSB <= 160 * 1024 && NS >= 2, "LDS of one workgroup");
+    __shared__ __attribute__((aligned(1024))) int8_t lds[LDSB];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wid / WN, wn = wid % WN;
+
+    // ---- tile and part of the contraction ----
+    int bid = blockIdx.x;
+    const int tiles = tiles_m * tiles_k;
+    {
+        const int nblk = tiles * splits;
+        const int per = nblk / 8, rem = nblk % 8, xcd = bid % 8, loc = bid / 8;
+        bid = (xcd < rem) ? xcd * (per + 1) + loc : rem * (per + 1) + (xcd - rem) * per + loc;
+    }
+    const int sp = bid / tiles;
+    bid -= sp * tiles;
+    const int width = GM * tiles_k;
+    const int first_m = (bid / width) * GM;
+    const int gm = min(tiles_m - first_m, GM);
+    const int m0 = (first_m + (bid % width) % gm) * BM, k0 = (bid % width) / gm * kGK;
+    const int nst = Np / kGN;
+    const int st0 = (int)((int64_t)nst * sp / splits), st1 = (int)((int64_t)nst * (sp + 1) / splits);
+    const int ns = st1 - st0;   // (at least 1: splits <= nst)
+
+    // ---- loaders: load i of this lane fills chunk p = i*NT + tid of A's, or of
+    // the weight's, rows (A: row p / 8, weight: row p / 16); with fewer chunks
+    // of A than threads the waves fill them twice over, with the same bytes, so
+    // that every wave counts the same loads ----
+    const int rows = min(BM, T - m0);
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(A + (int64_t)m0 * Np, 2 * rows * Np);
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(Wq, N * K);
+    int voA[LA], voB[LB], rowB[LB];
+#pragma unroll
+    for (int i = 0; i < LA; i++) {
+        const int p = (i * NT + tid) % CA, row = p >> 3, q = (p & 7) ^ swz<8>(row);
+        voA[i] = min(row, rows - 1) * Np * 2 + q * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < LB; i++) {
+        const int p = i * NT + tid, row = p >> 4, k = k0 + 16 * ((p & 15) ^ (2 * (row & 7)));
+        voB[i] = row * K + k;
+        rowB[i] = k < K ? N - row : 0;   // the row exists while n0 < rowB
+    }
+    auto issue = [&](int it) {
+        const int n0 = (st0 + it) * kGN;
+        int8_t *st = lds + (it % NS) * SSZ;
+#pragma unroll
+        for (int i = 0; i < LA; i++)
+            load_to_lds(rA, st + ((i * NT + wid * 64) % CA) * 16, voA[i], 2 * n0);
+#pragma unroll
+        for (int i = 0; i < LB; i++)
+            load_to_lds(rB, st + ASZ + (i * NT + wid * 64) * 16, n0 < rowB[i] ? voB[i] : kOutOfRange, n0 * K);
+    };
+
+    // ---- fragments ----
+    const int khalf = lane >> 5;
+    int offA[FM][KS], offB[FK];
+#pragma unroll
+    for (int a = 0; a < FM; a++) {
+        const int row = wm * FM * 32 + a * 32 + (lane & 31);
+#pragma unroll
+        for (int kk = 0; kk < KS; kk++)
+            offA[a][kk] = row * 128 + (((kk * 2 + khalf) ^ swz<8>(row)) * 16);
+    }
+    // lane l reads half (l & 1) of the chunk of 16 columns (l >> 4) & 1 in row
+    // 8 (l >> 5) + (l & 15) / 2 of the k-step, and gets column l & 31
+    {
+        const int r = (lane & 15) >> 1;
+#pragma unroll
+        for (int b = 0; b < FK; b++) {
+            const int c = (wn * FK + b) * 2 + ((lane >> 4) & 1);
+            offB[b] = ASZ + (8 * khalf + r) * kGK + ((c ^ (2 * r)) * 16) + 8 * (lane & 1);
+        }
+    }
+    v16f acc[FM][FK];
+#pragma unroll
+    for (int a = 0; a < FM; a++)
+#pragma unroll
+        for (int b = 0; b < FK; b++)
+            acc[a][b] = v16f{};
+
+    v8h fa[2][FM];
+    v2i fb[2][FK];
+    auto lread = [&](int set, int it, int kk) {
+        const int8_t *base = lds + (it % NS) * SSZ;
+#pragma unroll
+        for (int a = 0; a < FM; a++)
+            fa[set][a] = *reinterpret_cast<const v8h *>(base + offA[a][kk]);
+#pragma unroll
+        for (int b = 0; b < FK; b++)
+            fb[set][b] = read_codes_tr(base + offB[b] + kk * 16 * kGK);
+    };
+    auto mfmas = [&](int set) {
+        v8h wf[FK];
+#pragma unroll
+        for (int b = 0; b < FK; b++)
+            wf[b] = codes_to_f16(fb[set][b]);
+#pragma unroll
+        for (int a = 0; a < FM; a++)
+#pragma unroll
+            for (int b = 0; b < FK; b++)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[b], fa[set][a], acc[a][b], 0, 0, 0);
+    };
+    auto stage = [&](int it, auto wait_c, auto issue_c, auto last_c) {
+        constexpr int WAIT = decltype(wait_c)::value;
+        constexpr bool ISSUE = decltype(issue_c)::value;
+        constexpr bool LAST = decltype(last_c)::value;
+#pragma unroll
+        for (int kk = 0; kk < KS; kk++) {
+            const int cur = kk & 1;
+            if (kk + 1 < KS) {
+                lread(cur ^ 1, it, kk + 1);
+                mfmas(cur);
+            } else if constexpr (!LAST) {
+                wait_loads_barrier<WAIT>();   // stage it+1 landed; stage it read by all
+                if constexpr (ISSUE)
+                    issue(it + NS);
+                lread(cur ^ 1, it + 1, 0);
+                mfmas(cur);
+            } else {
+                mfmas(cur);
+            }
+        }
+    };
+    using TF = std::false_type;
+    using TT = std::true_type;
+    using W0 = std::integral_constant<int, 0>;
+    using WS = std::integral_constant<int, (LA + LB) * (NS - 2)>;
+
+    // the rows' factors, in registers from here on
+    const int ltok = wm * FM * 32 + (lane & 31);
+    float fx[FM];
+#pragma unroll
+    for (int a = 0; a < FM; a++)
+        fx[a] = fac[min(m0 + ltok + 32 * a, T - 1)];
+#pragma unroll
+    for (int s = 0; s < NS; s++)
+        if (s < ns)
+            issue(s);
+    if (ns >= NS)
+        wait_loads_barrier<(NS - 1) * (LA + LB)>();   // stage 0 landed
+    else
+        wait_loads_barrier<0>();
+    lread(0, 0, 0);
+    int it = 0;
+    for (; it + NS < ns; it++)      // steady state
+        stage(it, WS{}, TT{}, TF{});
+    for (; it + 1 < ns; it++)       // drain
+        stage(it, W0{}, TF{}, TF{});
+    stage(it, W0{}, TF{}, TT{});
+
+    // ---- epilogue ----
+    // acc[a][b], register r: token ltok + 32a, column 32b + 8 (r/4) + 4 khalf + r%4
+    // of the wave's columns
+    const int col0 = k0 + wn * FK * 32;
+    if constexpr (SPLIT) {   // fp32, in the rows' units
+        float *out = part + (int64_t)sp * T * K;
+#pragma unroll
+        for (int a = 0; a < FM; a++)
+#pragma unroll
+            for (int b = 0; b < FK; b++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const int t = m0 + ltok + 32 * a, k = col0 + 32 * b + 8 * g + 4 * khalf;
+                    if (t < T && k < K)
+                        *reinterpret_cast<v4f *>(out + (int64_t)t * K + k) =
+                            v4f{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
+                }
+        return;
+    }
+    wait_loads_barrier<0>();   // the ring is free
+    int8_t *own = lds + wid * (FM * 32) * CPR * 16;
+#pragma unroll
+    for (int a = 0; a < FM; a++)
+#pragma unroll
+        for (int b = 0; b < FK; b++)
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                float p[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    p[j] = acc[a][b][4 * g + j] * fx[a];
+                    asm("" : "+v"(p[j]));
+                }
+                *reinterpret_cast<uint2 *>(own + stage_off<CPR>(a * 32 + (lane & 31), b * 4 + g) + 8 * khalf) =
+                    make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
+            }
+#pragma unroll
+    for (int i = 0; i < FM * 32 * CPR / 64; i++) {
+        const int id = i * 64 + lane, row = id / CPR, ch = id % CPR;
+        const v4i v = *reinterpret_cast<const v4i *>(own + stage_off<CPR>(row, ch));
+        const int t = m0 + wm * FM * 32 + row, k = col0 + 8 * ch;
+        if (t < T && k < K)   // (K is a multiple of 16)
+            __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(dX + (int64_t)t * K + k));
+    }
+}
+
+// dX = fp16(fac * sum of the parts, in order); no part (N = 0): zeros.
+__global__ __launch_bounds__(256) void k_grad_join(const float *__restrict__ part, const float *__restrict__ fac,
+                                                   int splits, int T, int K, uint16_t *__restrict__ dX)
+{
+    const int64_t n = (int64_t)T * K, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= n)
+        return;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s = 0; s < splits; s++) {
+        const float4 lo = *reinterpret_cast<const float4 *>(part + s * n + i);
+        const float4 hi = *reinterpret_cast<const float4 *>(part + s * n + i + 4);
+        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+    }
+    if (splits) {
+        const float f = fac[i / K];   // (K is a multiple of 16: one row)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            v[e] *= f;
+            asm("" : "+v"(v[e]));
+        }
+    }
+    store8<true>(dX + i, 8, v);
+}
+
+} // namespace
+
+// Tile height and parts of the contraction.  (To be chosen by measurement.)
+BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N)
+{
+    const int64_t nst = (N + kGN - 1) / kGN;
+    const int bm = T > 128 ? 256 : T > 64 ? 128 : T > 32 ? 64 : 32;
+    const int64_t tiles = ((T + bm - 1) / bm) * ((K + kGK - 1) / kGK);
+    const int64_t s = std::min<int64_t>({std::max<int64_t>(1, 256 / std::max<int64_t>(tiles, 1)),
+                                         std::max<int64_t>(1, nst / 4), (int64_t)kMaxGradSplits});
+    return {bm, (int)s};
+}
+
+BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
+{
+    const size_t A = 256;
+    const BackwardPlan p = backward_plan(T, K, N);
+    BackwardLayout L;
+    L.Np = (int)((N + kGN - 1) / kGN * kGN);
+    size_t off = 0;
+    L.A = off;     off = align_up(off + 2 * (size_t)T * (size_t)L.Np, A);
+    L.fac = off;   off = align_up(off + 4 * (size_t)T, A);
+    L.cols = off;  off = align_up(off + 4 * (size_t)kMaxColStrips * (size_t)N, A);
+    L.part = off;  off = align_up(off + (p.splits > 1 ? 4 * (size_t)p.splits * (size_t)T * (size_t)K : 0), A);
+    L.total = off;
+    return L;
+}
+
+namespace {
+
+template <bool GATED, int KIND, bool VEC>
+void launch_rows(const GradArgs &a, uint16_t *A, float *fac, hipStream_t s)
+{
+    const int F = GATED ? a.N / 2 : a.N, rounds = (F + 8 * kRowThreads - 1) / (8 * kRowThreads);
+    const dim3 grid((unsigned)std::min(a.T, 1 << 20)), block(kRowThreads);
+    if (rounds <= 1)
+        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 1>), grid, block, 0, s, a, A, fac);
+    else if (rounds <= 2)
+        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 2>), grid, block, 0, s, a, A, fac);
+    else if (rounds <= 4)
+        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 4>), grid, block, 0, s, a, A, fac);
+    else
+        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 0>), grid, block, 0, s, a, A, fac);
+}
+
+template <bool GATED, int KIND, bool VEC>
+void launch_elementwise(const GradArgs &a, uint16_t *A, float *fac, float *cols, float *dbias, hipStream_t s)
+{
+    if (a.T > 0)
+        launch_rows<GATED, KIND, VEC>(a, A, fac, s);
+    if (!dbias)
+        return;
+    int strips = 0;
+    if (a.T > 0) {
+        const int F = GATED ? a.N / 2 : a.N, blocks = (F + 511) / 512;
+        strips = std::max(1, std::min({kMaxColStrips, (a.T + 31) / 32, 2048 / blocks}));
+        hipLaunchKernelGGL((k_grad_cols<GATED, KIND, VEC>), dim3((unsigned)blocks, (unsigned)strips),
+                           dim3(kColThreads), 0, s, a, cols);
+    }
+    hipLaunchKernelGGL(k_cols_join, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, cols, strips, a.N, dbias);
+}
+
+template <bool GATED, bool VEC>
+void launch_by_kind(const GradArgs &a, uint16_t *A, float *fac, float *cols, float *dbias, hipStream_t s)
+{
+    if (a.act.kind == 0)
+        launch_elementwise<GATED, 0, VEC>(a, A, fac, cols, dbias, s);
+    else if (a.act.kind == 1)
+        launch_elementwise<GATED, 1, VEC>(a, A, fac, cols, dbias, s);
+    else
+        launch_elementwise<GATED, 2, VEC>(a, A, fac, cols, dbias, s);
+}
+
+template <int BM, int NS, int WM, int WN, int GM>
+void launch_tiles(const uint16_t *A, const int8_t *Wq, const float *fac, int T, int K, int N, int Np, int splits,
+                  uint16_t *dX, float *part, hipStream_t s)
+{
+    const int tm = (T + BM - 1) / BM, tk = (K + kGK - 1) / kGK;
+    const dim3 grid((unsigned)(tm * tk * splits)), block(WM * WN * 64);
+    if (splits > 1)
+        hipLaunchKernelGGL((k_grad_gemm<BM, NS, WM, WN, GM, true>), grid, block, 0, s, A, Wq, fac, T, K, N, Np, tm, tk,
+                           splits, dX, part);
+    else
+        hipLaunchKernelGGL((k_grad_gemm<BM, NS, WM, WN, GM, false>), grid, block, 0, s, A, Wq, fac, T, K, N, Np, tm, tk,
+                           splits, dX, part);
+}
+
+void launch_join(const float *part, const float *fac, int splits, int64_t T, int64_t K, uint16_t *dX, hipStream_t s)
+{
+    const int64_t blocks = (T * K / 8 + 255) / 256;
+    hipLaunchKernelGGL(k_grad_join, dim3((unsigned)blocks), dim3(256), 0, s, part, fac, splits, (int)T, (int)K, dX);
+}
+
+} // namespace
+
+hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActParams &act, bool gated, const int8_t *Wq,
+                           const float *sW, int64_t T, int64_t K, int64_t N, uint16_t *dX, uint16_t *grad_pre,
+                           float *dbias, char *ws, hipStream_t s)
+{
+    if (T > 0 && N == 0) {
+        if (K > 0)
+            launch_join(nullptr, nullptr, 0, T, K, dX, s);
+        return hipGetLastError();
+    }
+    const BackwardLayout L = backward_layout(T, K, N);
+    const BackwardPlan p = backward_plan(T, K, N);
+    uint16_t *A = reinterpret_cast<uint16_t *>(ws + L.A);
+    float *fac = reinterpret_cast<float *>(ws + L.fac), *cols = reinterpret_cast<float *>(ws + L.cols);
+    float *part = reinterpret_cast<float *>(ws + L.part);
+    const GradArgs a{dY, pre, sW, grad_pre, act, (int)T, (int)N, L.Np};
+    const bool vec = (gated ? N / 2 : N) % 8 == 0;
+    if (gated)
+        vec ? launch_by_kind<true, true>(a, A, fac, cols, dbias, s) : launch_by_kind<true, false>(a, A, fac, cols, dbias, s);
+    else
+        vec ? launch_by_kind<false, true>(a, A, fac, cols, dbias, s) : launch_by_kind<false, false>(a, A, fac, cols, dbias, s);
+    if (T == 0 || K == 0)
+        return hipGetLastError();
+    const int t = (int)T, k = (int)K, n = (int)N;
+    if (p.bm == 256)
+        launch_tiles<256, 3, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+    else if (p.bm == 128)
+        launch_tiles<128, 4, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+    else if (p.bm == 64)
+        launch_tiles<64, 4, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+    else
+        launch_tiles<32, 4, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+    if (p.splits > 1)
+        launch_join(part, fac, p.splits, T, K, dX, s);
+    return hipGetLastError();
+}
+
+} // namespace li8

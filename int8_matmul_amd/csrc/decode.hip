@@ -47,8 +47,12 @@
 // variants give bit-identical results.  F16W: the outlier columns multiply
 // the original fp16 weight W16 (the fp16-weight variant), and the sum is
 // D = fl32(fl32(acc * sX) * sW) + sum_O X * W16.
+// EPI (the fused variant only; see few_epilogue.h): EPI_LINEAR and EPI_GATED
+// finish z = fl32(D * sW) in wave 0.  A gated pair's row group is 8 features'
+// gate rows and their 8 up rows, whose results meet in wave 0's two halves.
 #include <type_traits>
 
+#include "few_epilogue.h"
 #include "li8_internal.h"
 #include "quant_math.h"
 
@@ -216,7 +220,7 @@ __device__ __forceinline__ uint32_t wave_max_tokens(const uint32_t (&v)[TB], int
 // 12 of the weight loads before the row-maxima barrier and the other 4 before
 // the next, a split at which these waves reach each barrier about when the
 // activation waves do.
-template <int KB>
+template <int KB, int EPI>
 __device__ __forceinline__ void mfma_wave(const int8_t *__restrict__ Wq, int T, int K, int N,
                                           const int8_t *lds, v4i *red, int mw, int lane)
 {
@@ -225,7 +229,7 @@ __device__ __forceinline__ void mfma_wave(const int8_t *__restrict__ Wq, int T, 
     const int S = (K + 63) / 64;
     const int QS = 16 * T + 16;
     const int kg = lane >> 4, tok = lane & 15;
-    const int n = min((int)blockIdx.x * kDRows + (lane & 15), N - 1);
+    const int n = few_row<EPI>(blockIdx.x, lane & 15, N);
     const __amdgpu_buffer_rsrc_t rW = make_rsrc(Wq, N * K);
     v4i wr[NL];
     // load i: share w = 2mw + i / KB, its k-step j = i % KB (zeros past the
@@ -271,15 +275,16 @@ __device__ __forceinline__ void mfma_wave(const int8_t *__restrict__ Wq, int T, 
 // TB: a compile-time bound on T (8 or 16), so that the per-token loops of
 // the activation work run over T <= 8 slots when that suffices.  MW: see the
 // file comment (launched with 8 + MW waves).
-template <bool FUSED, int KB, int TB, bool F16W, bool STORE_ACC, int MW>
+template <bool FUSED, int KB, int TB, bool F16W, bool STORE_ACC, int MW, int EPI>
 __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
     const uint16_t *__restrict__ X, const int8_t *__restrict__ Wq, const float *__restrict__ sW,
     const uint16_t *__restrict__ W16,
     uint32_t thr_mag, int T, int K, int N,
     const int32_t *__restrict__ meta, const int32_t *__restrict__ idx_g,
     const float *__restrict__ sX_g, const int8_t *__restrict__ Xq_g,
-    const uint16_t *__restrict__ XO_g, uint16_t *__restrict__ Y, int32_t *__restrict__ acc_out)
+    const uint16_t *__restrict__ XO_g, uint16_t *Y, int32_t *__restrict__ acc_out, EpiParams epi)
 {
+    static_assert(EPI == EPI_PLAIN || (FUSED && !F16W && !STORE_ACC), "epilogue variants");
     static_assert(KB % 8 == 0, "weight loads per lane come in groups of 8");
     __shared__ __attribute__((aligned(16))) int8_t lds[kLds];
     int8_t *xq = lds;
@@ -301,7 +306,7 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
     static_assert(MW != 8 || TB == 8, "8 MFMA waves: 16 waves of at most 128 registers");
     if constexpr (MW == 4) {
         if (wid >= kDWaves) {
-            mfma_wave<KB>(Wq, T, K, N, lds, red, wid - kDWaves, lane);
+            mfma_wave<KB, EPI>(Wq, T, K, N, lds, red, wid - kDWaves, lane);
             return;
         }
     }
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
     const int kend = min(s1 * 64, K);   // end of this wave's share of K
     // (a row group past the last one, rg >= NRG, reads zeros)
     auto wload = [&](int set, int rg) {
-        const int n = min(rg * kDRows + (lane & 15), N - 1);
+        const int n = few_row<EPI>(rg, lane & 15, N);
         const int kl = rg < NRG ? kend : 0;
 #pragma unroll
         for (int j = 0; j < KB; j++) {
@@ -373,11 +378,14 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
         const int e = gt & 31, r = gt >> 5;
         // a row group past the last one gathers nothing: an empty buffer
         // at the last group's rows (every offset out of range, zeros)
-        const int rows = rgc < NRG ? min(kDRows, N - rgc * kDRows) : 0;
-        const int64_t rbase = (int64_t)min(rgc, NRG - 1) * kDRows * K;
-        const __amdgpu_buffer_rsrc_t rWg =
-            F16W ? make_rsrc(W16 + rbase, 2 * rows * K) : make_rsrc(Wq + rbase, rows * K);
-        const int wo = r * K + col;
+        // (a gated pair's rows lie in two places: all of Wq, by row)
+        const int rows = EPI == EPI_GATED ? (rgc < NRG ? kDRows : 0)
+                                          : (rgc < NRG ? min(kDRows, N - rgc * kDRows) : 0);
+        const int64_t rbase = EPI == EPI_GATED ? 0 : (int64_t)min(rgc, NRG - 1) * kDRows * K;
+        const __amdgpu_buffer_rsrc_t rWg = F16W               ? make_rsrc(W16 + rbase, 2 * rows * K)
+                                           : EPI == EPI_GATED ? make_rsrc(Wq, N * K)
+                                                              : make_rsrc(Wq + rbase, rows * K);
+        const int wo = (EPI == EPI_GATED ? few_row<EPI>(rgc, r, N) : r) * K + col;
         const int woff = (e < nO && r < rows) ? (F16W ? 2 * wo : wo) : kOutOfRange;
         if constexpr (F16W)
             g_w = __builtin_amdgcn_raw_buffer_load_b16(rWg, woff, 0, 0);
@@ -388,7 +396,7 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
         const __amdgpu_buffer_rsrc_t rXg = FUSED ? make_rsrc(X, 2 * T * K) : make_rsrc(XO_g, 2 * T * K);
         g_x = __builtin_amdgcn_raw_buffer_load_b16(rXg, (e < nO && r < T) ? 2 * xo : kOutOfRange, 0, 0);
         g_s = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(sW, 4 * N),
-                                                   gt < kDRows ? 4 * min(rgc * kDRows + gt, N - 1)
+                                                   gt < kDRows ? 4 * few_row<EPI>(rgc, gt, N)
                                                                : kOutOfRange,
                                                    0, 0);
     };
@@ -697,10 +705,11 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
         // weight rows of this row group (at most 16 rows of K elements from
         // its first row, so the offsets stay small), token rows of X / XO
         const int rows = min(kDRows, N - rgc * kDRows);
-        const int wl = min(rgc * kDRows + (lane & 15), N - 1) - rgc * kDRows;   // local weight row
-        const __amdgpu_buffer_rsrc_t rWg =
-            F16W ? make_rsrc(W16 + (int64_t)rgc * kDRows * K, 2 * rows * K)
-                 : make_rsrc(Wq + (int64_t)rgc * kDRows * K, rows * K);
+        const int wl = few_row<EPI>(rgc, lane & 15, N) - (EPI == EPI_GATED ? 0 : rgc * kDRows);   // (local) weight row
+        const __amdgpu_buffer_rsrc_t rWg = F16W ? make_rsrc(W16 + (int64_t)rgc * kDRows * K, 2 * rows * K)
+                                           : EPI == EPI_GATED
+                                               ? make_rsrc(Wq, N * K)
+                                               : make_rsrc(Wq + (int64_t)rgc * kDRows * K, rows * K);
         const int ttok = min(tok, T - 1);
         const __amdgpu_buffer_rsrc_t rXg = FUSED ? make_rsrc(X, 2 * T * K) : make_rsrc(XO_g, 2 * T * K);
 #pragma unroll
@@ -742,6 +751,11 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
         // wait only for the older weight loads.  They go to LDS after the
         // MFMAs, for wave 0 to read after the reduction barrier.
         const int nb = rgc * kDRows + 4 * kg;   // this lane's first feature
+        // (EPI: bias and residual, requested by the wave that uses them)
+        FewOperands<EPI> eo;
+        if constexpr (EPI != EPI_PLAIN)
+            if (wid == 0)
+                eo.load(epi, rgc, kg, tok, T, N);
         uint32_t g_w = 0, g_x = 0, g_s = 0;
         if (!gathered)
             gather_issue(rgc, g_w, g_x, g_s);
@@ -845,6 +859,14 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
             fragments(i0, wr, xr, a, b);
             d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, d, 0, 0, 0);
         }
+        if constexpr (EPI != EPI_PLAIN) {
+            float z[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                z[r] = d[r] * swv[r];
+            eo.finish(epi, z, Y, rgc, kg, tok, T, N);
+            return;
+        }
         if (tok >= T)
             return;
         float p[4];
@@ -900,11 +922,11 @@ __global__ __launch_bounds__(kDThreads + 64 * MW) void k_decode(
     }
 }
 
-template <bool FUSED, int KB, int TB, bool F16W, int MW>
+template <bool FUSED, int KB, int TB, bool F16W, int EPI, int MW>
 hipError_t launch_roles(const uint16_t *X, const int8_t *Wq, const float *sW, const uint16_t *W16,
                         uint32_t thr_mag,
                         int64_t T, int64_t K, int64_t N, uint16_t *Y, int32_t *acc, const char *ws,
-                        const WsLayout &L, hipStream_t s)
+                        const WsLayout &L, const EpiParams &epi, hipStream_t s)
 {
     const int nrg = (int)((N + kDRows - 1) / kDRows);
     const dim3 grid((unsigned)(nrg < kDecodeMaxBlocks ? nrg : kDecodeMaxBlocks));
@@ -915,11 +937,11 @@ hipError_t launch_roles(const uint16_t *X, const int8_t *Wq, const float *sW, co
     const int8_t *Xq = FUSED ? nullptr : reinterpret_cast<const int8_t *>(ws + L.Xq);
     const uint16_t *XO = FUSED ? nullptr : reinterpret_cast<const uint16_t *>(ws + L.XO);
     if (acc)
-        hipLaunchKernelGGL((k_decode<FUSED, KB, TB, F16W, true, MW>), grid, block, 0, s, X, Wq,
-                           sW, W16, thr_mag, (int)T, (int)K, (int)N, meta, idx, sX, Xq, XO, Y, acc);
+        hipLaunchKernelGGL((k_decode<FUSED, KB, TB, F16W, EPI == EPI_PLAIN, MW, EPI>), grid, block, 0, s, X, Wq,
+                           sW, W16, thr_mag, (int)T, (int)K, (int)N, meta, idx, sX, Xq, XO, Y, acc, epi);
     else
-        hipLaunchKernelGGL((k_decode<FUSED, KB, TB, F16W, false, MW>), grid, block, 0, s, X, Wq,
-                           sW, W16, thr_mag, (int)T, (int)K, (int)N, meta, idx, sX, Xq, XO, Y, acc);
+        hipLaunchKernelGGL((k_decode<FUSED, KB, TB, F16W, false, MW, EPI>), grid, block, 0, s, X, Wq,
+                           sW, W16, thr_mag, (int)T, (int)K, (int)N, meta, idx, sX, Xq, XO, Y, acc, epi);
     return hipGetLastError();
 }
 
@@ -927,22 +949,22 @@ hipError_t launch_roles(const uint16_t *X, const int8_t *Wq, const float *sW, co
 // MW = 4 with one row group per workgroup, MW = 8 with more row groups than
 // workgroups and T <= 8.  (MW = 8 at one row group per workgroup measured
 // slower than MW = 4: 6.9 against 5.8 us at 8x4096x4096.)
-template <bool FUSED, int KB, int TB, bool F16W>
+template <bool FUSED, int KB, int TB, bool F16W, int EPI>
 hipError_t launch_kb(const uint16_t *X, const int8_t *Wq, const float *sW, const uint16_t *W16,
                      uint32_t thr_mag,
                      int64_t T, int64_t K, int64_t N, uint16_t *Y, int32_t *acc, const char *ws,
-                     const WsLayout &L, hipStream_t s)
+                     const WsLayout &L, const EpiParams &epi, hipStream_t s)
 {
     if constexpr (FUSED && KB == 8) {
         if ((N + kDRows - 1) / kDRows <= kDecodeMaxBlocks)
-            return launch_roles<FUSED, KB, TB, F16W, 4>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc,
-                                                        ws, L, s);
+            return launch_roles<FUSED, KB, TB, F16W, EPI, 4>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc,
+                                                             ws, L, epi, s);
         if constexpr (TB == 8)
-            return launch_roles<FUSED, KB, TB, F16W, 8>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc,
-                                                        ws, L, s);
+            return launch_roles<FUSED, KB, TB, F16W, EPI, 8>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc,
+                                                             ws, L, epi, s);
     }
-    return launch_roles<FUSED, KB, TB, F16W, 0>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws,
-                                                L, s);
+    return launch_roles<FUSED, KB, TB, F16W, EPI, 0>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws,
+                                                     L, epi, s);
 }
 
 } // namespace
@@ -953,26 +975,41 @@ bool decode_shape(int64_t T, int64_t K)
 }
 
 // KB (weight 16-byte loads per lane and row group) by K, TB by T.
-template <bool FUSED, bool F16W>
+template <bool FUSED, bool F16W, int EPI>
 hipError_t launch_decode(const uint16_t *X, const int8_t *Wq, const float *sW, const uint16_t *W16,
                          uint32_t thr_mag, int64_t T, int64_t K, int64_t N, uint16_t *Y,
-                         int32_t *acc, const char *ws, const WsLayout &L, hipStream_t s)
+                         int32_t *acc, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s)
 {
     if (K <= 4096)
-        return T <= 8 ? launch_kb<FUSED, 8, 8, F16W>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, s)
-                      : launch_kb<FUSED, 8, 16, F16W>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, s);
-    return T <= 8 ? launch_kb<FUSED, 16, 8, F16W>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, s)
-                  : launch_kb<FUSED, 16, 16, F16W>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, s);
+        return T <= 8
+                   ? launch_kb<FUSED, 8, 8, F16W, EPI>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, epi, s)
+                   : launch_kb<FUSED, 8, 16, F16W, EPI>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, epi, s);
+    return T <= 8
+               ? launch_kb<FUSED, 16, 8, F16W, EPI>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, epi, s)
+               : launch_kb<FUSED, 16, 16, F16W, EPI>(X, Wq, sW, W16, thr_mag, T, K, N, Y, acc, ws, L, epi, s);
 }
+
+static const WsLayout kNoLayout{};
 
 hipError_t launch_decode_fused(const uint16_t *X, const int8_t *Wq, const float *sW,
                                const uint16_t *W16, uint16_t thr_mag, int64_t T, int64_t K,
                                int64_t N, uint16_t *Y, hipStream_t s)
 {
-    static const WsLayout none{};
     if (W16)
-        return launch_decode<true, true>(X, Wq, sW, W16, thr_mag, T, K, N, Y, nullptr, nullptr, none, s);
-    return launch_decode<true, false>(X, Wq, sW, nullptr, thr_mag, T, K, N, Y, nullptr, nullptr, none, s);
+        return launch_decode<true, true, EPI_PLAIN>(X, Wq, sW, W16, thr_mag, T, K, N, Y, nullptr, nullptr,
+                                                    kNoLayout, EpiParams{}, s);
+    return launch_decode<true, false, EPI_PLAIN>(X, Wq, sW, nullptr, thr_mag, T, K, N, Y, nullptr, nullptr,
+                                                 kNoLayout, EpiParams{}, s);
+}
+
+hipError_t launch_decode_epi(const uint16_t *X, const int8_t *Wq, const float *sW, uint16_t thr_mag,
+                             int64_t T, int64_t K, int64_t N, uint16_t *Y, const EpiParams &epi, hipStream_t s)
+{
+    if (epi.gated)
+        return launch_decode<true, false, EPI_GATED>(X, Wq, sW, nullptr, thr_mag, T, K, N, Y, nullptr, nullptr,
+                                                     kNoLayout, epi, s);
+    return launch_decode<true, false, EPI_LINEAR>(X, Wq, sW, nullptr, thr_mag, T, K, N, Y, nullptr, nullptr,
+                                                  kNoLayout, epi, s);
 }
 
 hipError_t launch_decode_gemm(const int8_t *Wq, const float *sW, const uint16_t *W16, int64_t T,
@@ -980,8 +1017,10 @@ hipError_t launch_decode_gemm(const int8_t *Wq, const float *sW, const uint16_t 
                               const WsLayout &L, hipStream_t s)
 {
     if (W16)
-        return launch_decode<false, true>(nullptr, Wq, sW, W16, 0, T, K, N, Y, acc, ws, L, s);
-    return launch_decode<false, false>(nullptr, Wq, sW, nullptr, 0, T, K, N, Y, acc, ws, L, s);
+        return launch_decode<false, true, EPI_PLAIN>(nullptr, Wq, sW, W16, 0, T, K, N, Y, acc, ws, L,
+                                                     EpiParams{}, s);
+    return launch_decode<false, false, EPI_PLAIN>(nullptr, Wq, sW, nullptr, 0, T, K, N, Y, acc, ws, L,
+                                                  EpiParams{}, s);
 }
 
 } // namespace li8

@@ -34,8 +34,11 @@
 //     bit-identical outputs.
 // F16W: the outlier columns multiply the fp16 weight W16, and
 // D = fl32(fl32(acc * sX) * sW) + sum_O X * W16.
+// EPI (few_epilogue.h): k_dfinish takes z = fl32(D * sW) further; for a gated
+// pair k_dsplit and k_dfinish take 8 features' gate and up rows as a row group.
 #include <algorithm>
 
+#include "few_epilogue.h"
 #include "li8_internal.h"
 #include "quant_math.h"
 
@@ -139,7 +142,7 @@ struct SplitOut {   // FUSED: where class-0 workgroups write the prepared stages
     uint16_t *XO;
 };
 
-template <bool FUSED, int KB, int TB>
+template <bool FUSED, int KB, int TB, bool GATED>
 __global__ __launch_bounds__(kSThreads) void k_dsplit(
     const uint16_t *__restrict__ X, const int8_t *__restrict__ Wq, int T, int K, int N, int KSL,
     int NRGC, const uint32_t *__restrict__ bits, const int32_t *__restrict__ ocnt,
@@ -172,7 +175,7 @@ __global__ __launch_bounds__(kSThreads) void k_dsplit(
 
     v4i wbuf[2][KB];
     auto wload = [&](int set, int rg) {   // (rg >= NRG reads zeros)
-        const int n = min(rg * 16 + (lane & 15), N - 1);
+        const int n = few_row<GATED ? EPI_GATED : EPI_PLAIN>(rg, lane & 15, N);
         const int kl = rg < NRG ? kend : 0;
 #pragma unroll
         for (int j = 0; j < KB; j++) {
@@ -404,13 +407,14 @@ __global__ __launch_bounds__(kSThreads) void k_dsplit(
 // ---------------------------------------------------------------------------
 // 3. Finish: wave w of workgroup g handles row group rg = 4 g + w.
 // ---------------------------------------------------------------------------
-template <bool F16W, bool STORE_ACC>
+template <bool F16W, bool STORE_ACC, int EPI>
 __global__ __launch_bounds__(kFThreads) void k_dfinish(
     const int8_t *__restrict__ Wq, const float *__restrict__ sW, const uint16_t *__restrict__ W16,
     int T, int K, int N, int KS, const int32_t *__restrict__ part, const int32_t *__restrict__ meta,
     const int32_t *__restrict__ idx_g, const float *__restrict__ sX_g,
-    const uint16_t *__restrict__ XO_g, uint16_t *__restrict__ Y, int32_t *__restrict__ acc_out)
+    const uint16_t *__restrict__ XO_g, uint16_t *Y, int32_t *__restrict__ acc_out, EpiParams epi)
 {
+    static_assert(EPI == EPI_PLAIN || (!F16W && !STORE_ACC), "epilogue variants");
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
     const int NRG = (N + 15) / 16;
     const int rg = blockIdx.x * (kFThreads / 64) + wid;
@@ -429,7 +433,10 @@ __global__ __launch_bounds__(kFThreads) void k_dfinish(
     float swv[4];
 #pragma unroll
     for (int r = 0; r < 4; r++)
-        swv[r] = sW[min(nb + r, N - 1)];
+        swv[r] = sW[few_row<EPI>(rg, 4 * kg + r, N)];
+    FewOperands<EPI> eo;
+    if constexpr (EPI != EPI_PLAIN)
+        eo.load(epi, rg, kg, tok, T, N);
     if constexpr (STORE_ACC) {
         if (tok < T)
 #pragma unroll
@@ -448,9 +455,11 @@ __global__ __launch_bounds__(kFThreads) void k_dfinish(
     // D += X[:, O] . W[:, O]^T, 32 outlier columns per MFMA: lane supplies
     // weight row (lane & 15) and token tok at ranks 32c + 8 kg .. +7
     const int rows = min(16, N - rg * 16);
-    const int wl = min(lane & 15, rows - 1);   // local weight row
-    const __amdgpu_buffer_rsrc_t rWg = F16W ? make_rsrc(W16 + (int64_t)rg * 16 * K, 2 * rows * K)
-                                            : make_rsrc(Wq + (int64_t)rg * 16 * K, rows * K);
+    // (local) weight row: a gated pair's rows lie in two places
+    const int wl = EPI == EPI_GATED ? few_row<EPI>(rg, lane & 15, N) : min(lane & 15, rows - 1);
+    const __amdgpu_buffer_rsrc_t rWg = F16W               ? make_rsrc(W16 + (int64_t)rg * 16 * K, 2 * rows * K)
+                                       : EPI == EPI_GATED ? make_rsrc(Wq, N * K)
+                                                          : make_rsrc(Wq + (int64_t)rg * 16 * K, rows * K);
     const __amdgpu_buffer_rsrc_t rI = make_rsrc(idx_g, 4 * K);
     const __amdgpu_buffer_rsrc_t rXO = make_rsrc(XO_g, 2 * T * K);
     for (int c = 0; c < (nO + 31) / 32; c++) {
@@ -487,6 +496,14 @@ __global__ __launch_bounds__(kFThreads) void k_dfinish(
         }
         d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, d, 0, 0, 0);
     }
+    if constexpr (EPI != EPI_PLAIN) {
+        float z[4];
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+            z[r] = d[r] * swv[r];
+        eo.finish(epi, z, Y, rg, kg, tok, T, N);
+        return;
+    }
     if (tok >= T)
         return;
     float p[4];
@@ -512,27 +529,27 @@ __global__ __launch_bounds__(kFThreads) void k_dfinish(
     }
 }
 
-template <bool FUSED, int KB, int TB>
+template <bool FUSED, int KB, int TB, bool GATED>
 void launch_split_kb(const uint16_t *X, const int8_t *Wq, int64_t T, int64_t K, int64_t N,
                      const SplitPlan &p, const uint32_t *bits, const int32_t *ocnt,
                      const uint32_t *pmax, SplitOut out, const int8_t *Xq, int32_t *part,
                      hipStream_t s)
 {
-    hipLaunchKernelGGL((k_dsplit<FUSED, KB, TB>), dim3((unsigned)(p.KS * p.NRGC)), dim3(kSThreads), 0,
+    hipLaunchKernelGGL((k_dsplit<FUSED, KB, TB, GATED>), dim3((unsigned)(p.KS * p.NRGC)), dim3(kSThreads), 0,
                        s, X, Wq, (int)T, (int)K, (int)N, p.KSL, p.NRGC, bits, ocnt, pmax, out, Xq,
                        part);
 }
 
-template <bool FUSED>
+template <bool FUSED, bool GATED = false>
 void launch_split(const uint16_t *X, const int8_t *Wq, int64_t T, int64_t K, int64_t N,
                   const SplitPlan &p, const uint32_t *bits, const int32_t *ocnt, const uint32_t *pmax,
                   SplitOut out, const int8_t *Xq, int32_t *part, hipStream_t s)
 {
     if (p.KSL <= 8 * 512)
-        return T <= 8 ? launch_split_kb<FUSED, 8, 8>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s)
-                      : launch_split_kb<FUSED, 8, 16>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s);
-    return T <= 8 ? launch_split_kb<FUSED, 16, 8>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s)
-                  : launch_split_kb<FUSED, 16, 16>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s);
+        return T <= 8 ? launch_split_kb<FUSED, 8, 8, GATED>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s)
+                      : launch_split_kb<FUSED, 8, 16, GATED>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s);
+    return T <= 8 ? launch_split_kb<FUSED, 16, 8, GATED>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s)
+                  : launch_split_kb<FUSED, 16, 16, GATED>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, Xq, part, s);
 }
 
 void launch_finish(const int8_t *Wq, const float *sW, const uint16_t *W16, int64_t T, int64_t K,
@@ -543,19 +560,33 @@ void launch_finish(const int8_t *Wq, const float *sW, const uint16_t *W16, int64
     const dim3 grid((unsigned)((NRG + 3) / 4)), block(kFThreads);
     if (W16) {
         if (acc)
-            hipLaunchKernelGGL((k_dfinish<true, true>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
-                               (int)N, KS, part, meta, idx, sX, XO, Y, acc);
+            hipLaunchKernelGGL((k_dfinish<true, true, EPI_PLAIN>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
+                               (int)N, KS, part, meta, idx, sX, XO, Y, acc, EpiParams{});
         else
-            hipLaunchKernelGGL((k_dfinish<true, false>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
-                               (int)N, KS, part, meta, idx, sX, XO, Y, acc);
+            hipLaunchKernelGGL((k_dfinish<true, false, EPI_PLAIN>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
+                               (int)N, KS, part, meta, idx, sX, XO, Y, acc, EpiParams{});
     } else {
         if (acc)
-            hipLaunchKernelGGL((k_dfinish<false, true>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
-                               (int)N, KS, part, meta, idx, sX, XO, Y, acc);
+            hipLaunchKernelGGL((k_dfinish<false, true, EPI_PLAIN>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
+                               (int)N, KS, part, meta, idx, sX, XO, Y, acc, EpiParams{});
         else
-            hipLaunchKernelGGL((k_dfinish<false, false>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
-                               (int)N, KS, part, meta, idx, sX, XO, Y, acc);
+            hipLaunchKernelGGL((k_dfinish<false, false, EPI_PLAIN>), grid, block, 0, s, Wq, sW, W16, (int)T, (int)K,
+                               (int)N, KS, part, meta, idx, sX, XO, Y, acc, EpiParams{});
     }
+}
+
+void launch_finish_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N, int KS,
+                       const int32_t *part, const SplitOut &out, uint16_t *Y, const EpiParams &epi,
+                       hipStream_t s)
+{
+    const int NRG = (int)((N + 15) / 16);
+    const dim3 grid((unsigned)((NRG + 3) / 4)), block(kFThreads);
+    if (epi.gated)
+        hipLaunchKernelGGL((k_dfinish<false, false, EPI_GATED>), grid, block, 0, s, Wq, sW, nullptr, (int)T,
+                           (int)K, (int)N, KS, part, out.meta, out.idx, out.sX, out.XO, Y, nullptr, epi);
+    else
+        hipLaunchKernelGGL((k_dfinish<false, false, EPI_LINEAR>), grid, block, 0, s, Wq, sW, nullptr, (int)T,
+                           (int)K, (int)N, KS, part, out.meta, out.idx, out.sX, out.XO, Y, nullptr, epi);
 }
 
 } // namespace
@@ -623,7 +654,7 @@ size_t split_part_bytes(int64_t T, int64_t K, int64_t N)
 
 hipError_t launch_split_fused(const uint16_t *X, const int8_t *Wq, const float *sW,
                               const uint16_t *W16, uint16_t thr_mag, int64_t T, int64_t K,
-                              int64_t N, uint16_t *Y, char *ws, hipStream_t s)
+                              int64_t N, uint16_t *Y, char *ws, hipStream_t s, const EpiParams *epi)
 {
     const SplitLayout L = split_layout(T, K, N);
     const SplitPlan p = split_plan(T, K, N);
@@ -640,8 +671,14 @@ hipError_t launch_split_fused(const uint16_t *X, const int8_t *Wq, const float *
     else
         hipLaunchKernelGGL((k_dscan<16>), dim3((unsigned)nb1), dim3(64), 0, s, X, (int)T, (int)K,
                            (uint32_t)thr_mag, bits, ocnt, pmax);
-    launch_split<true>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, nullptr, part, s);
-    launch_finish(Wq, sW, W16, T, K, N, p.KS, part, out.meta, out.idx, out.sX, out.XO, Y, nullptr, s);
+    if (epi && epi->gated)
+        launch_split<true, true>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, nullptr, part, s);
+    else
+        launch_split<true>(X, Wq, T, K, N, p, bits, ocnt, pmax, out, nullptr, part, s);
+    if (epi)
+        launch_finish_epi(Wq, sW, T, K, N, p.KS, part, out, Y, *epi, s);
+    else
+        launch_finish(Wq, sW, W16, T, K, N, p.KS, part, out.meta, out.idx, out.sX, out.XO, Y, nullptr, s);
     return hipGetLastError();
 }
 

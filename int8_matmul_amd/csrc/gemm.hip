@@ -39,8 +39,10 @@
 #include <type_traits>
 #include <utility>
 
+#include "act_math.h"
 #include "li8_internal.h"
 #include "quant_math.h"
+#include "tile_common.h"
 
 namespace li8 {
 namespace {
@@ -50,70 +52,21 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
-#define LI8_LDS __attribute__((address_space(3)))
 
-// Buffer resource over `bytes` bytes at p (raw buffer, offsets in bytes).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *p, int bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, bytes, 0x00020000);
-}
+// EPI (EpiParams in li8_internal.h).  For a gated pair the tile's
+// BN weight rows are BN/2 features' gate and up rows in alternating blocks of
+// 32, so that a wave holds both of a feature in the same registers of
+// neighbouring accumulator blocks; H, half as wide as Z, is all that is
+// written unless the caller keeps z.
 
-// 16 bytes per lane from rsrc at voffset + soffset into LDS at lds + 16*lane.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, void *lds, int voffset,
-                                            int soffset)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LI8_LDS void *)lds, 16, voffset, soffset, 0, 0);
-}
-
-// B (4 or 16) bytes per lane from rsrc at voffset into LDS at lds + B*lane.
-// (Called from a device function: the builtin written inside a kernel's
-// lambda makes the host pass drop the kernel's launch stub.)
-template <int B>
-__device__ __forceinline__ void load_to_lds_n(__amdgpu_buffer_rsrc_t r, void *lds, int voffset)
-{
-    static_assert(B == 4 || B == 16, "bytes per lane");
-    if constexpr (B == 4)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LI8_LDS void *)lds, 4, voffset, 0, 0, 0);
-    else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LI8_LDS void *)lds, 16, voffset, 0, 0, 0);
-}
-
-template <int CPR>
-__device__ __forceinline__ int swz(int row)
-{
-    static_assert(CPR == 4 || CPR == 8, "16-byte chunks per LDS row");
-    if constexpr (CPR == 8)
-        return (row ^ (row >> 3)) & 7;
-    else
-        return ((row >> 1) ^ (row >> 3)) & 3;
-}
-
-// Wait until at most N buffer loads of this wave are in flight and all its
-// LDS reads are done, then barrier.  The compiler does not track the LDS
-// writes of buffer_load ... lds, so this wait is what orders them.
-template <int N>
-__device__ __forceinline__ void wait_loads_barrier()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-constexpr int kOutOfRange = (int)0x80000000;   // buffer offset past any operand
-
-// f(integral_constant<int, I>) for each I of the sequence, in order.
-template <int... I, class F>
-__device__ __forceinline__ void for_each_index(std::integer_sequence<int, I...>, F &&f)
-{
-    (f(std::integral_constant<int, I>{}), ...);
-}
-
-template <int BM, int BN, int BKS, int NS, int WM, int WN, int GM, bool F16W, bool STORE_ACC>
+template <int BM, int BN, int BKS, int NS, int WM, int WN, int GM, bool F16W, bool STORE_ACC, int EPI>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     const int8_t *__restrict__ Xq, const int8_t *__restrict__ Wq,
     const float *__restrict__ sX, const float *__restrict__ sW,
     const int32_t *__restrict__ meta, const uint16_t *__restrict__ XO,
     const int8_t *__restrict__ WO, const int32_t *__restrict__ idx_g,
     const int32_t *__restrict__ wpre_g, int T, int K, int N, int tiles_m, int tiles_n,
-    uint16_t *__restrict__ Y, int32_t *__restrict__ acc_out)
+    uint16_t *Y, int32_t *__restrict__ acc_out, EpiParams epi)
 {
     constexpr int NT = WM * WN * 64, NW = WM * WN;
     constexpr int FM = BM / (WM * 32);
@@ -142,8 +95,13 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     constexpr int WO_B = (16 * WOE * BN > BN * CAP) ? 16 * WOE * BN : BN * CAP;
     constexpr int PF_IDX = PF_WO + WO_B, PF_WPRE = PF_IDX + 4 * CAP;
     constexpr int PF_DUMMY = PF_WPRE + (CAP > 0 ? 4 * (NWMAX + 1) : 0);
-    constexpr int PF_END = PF_DUMMY + (CAP > 0 ? NT : 0);
-    constexpr int LDSB = (PF_END > STG) ? PF_END : STG;
+    // EPI_LINEAR, EPI_GATED: biases as fp32 past the rest; their staging rows
+    // have no padding and lie inside the ring
+    constexpr int PF_BIAS = (PF_DUMMY + (CAP > 0 ? NT : 0) + 15) & ~15;
+    constexpr int PF_END = EPI != EPI_PLAIN ? PF_BIAS + 4 * BN : PF_DUMMY + (CAP > 0 ? NT : 0);
+    constexpr int LDSB = (PF_END > STG || EPI != EPI_PLAIN) ? PF_END : STG;
+    static_assert(EPI == EPI_PLAIN || (!F16W && !STORE_ACC && 2 * BM * BN <= NS * SSZ), "epilogue variants");
+    static_assert(EPI != EPI_GATED || FN % 2 == 0, "gate and up blocks in pairs");
     static_assert(FM * WM * 32 == BM && FN * WN * 32 == BN, "tile shape");
     static_assert(LA * NT == BM * CPR && LB * NT == BN * CPR, "loader shape");
     static_assert(KS % 2 == 0 && NS >= 2 && BKS == 32 * KS, "pipeline shape");
@@ -173,6 +131,20 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     const int nO = min(max(meta[0], 0), K);   // (a bad workspace cannot lengthen the loop)
     asm volatile("" ::"s"(nO));
     const int nk = (K + BKS - 1) / BKS;
+    // weight row of the tile's local row c (clamped to the last one)
+    const int F = N >> 1;
+    auto wrow = [&](int c) {
+        if constexpr (EPI == EPI_GATED) {
+            const int f = min((n0 >> 1) + (c >> 6) * 32 + (c & 31), F - 1);
+            return (c & 32) ? F + f : f;
+        } else {
+            return min(n0 + c, N - 1);
+        }
+    };
+    float bias_v = 0.0f;
+    if constexpr (EPI != EPI_PLAIN)
+        if (epi.bias)
+            bias_v = h2f(epi.bias[wrow(min(tid, BN - 1))]);
     const bool fold = CAP > 0 && nO > kFoldMin && nO <= CAP && K <= kFoldMaxK;   // (uniform)
 
     // ---- global -> LDS loaders: load i of this lane fills LDS chunk
@@ -190,7 +162,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
 #pragma unroll
     for (int i = 0; i < LB; i++) {
         const int p = i * NT + wid * 64 + lane, row = p / CPR, q = (p % CPR) ^ swz<CPR>(row);
-        voB[i] = min(n0 + row, N - 1) * K + q * 16;
+        voB[i] = wrow(row) * K + q * 16;
         kmB[i] = K - q * 16;
     }
     auto issue = [&](int kt) {
@@ -391,8 +363,9 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         const int swb = N < (1 << 29) ? 4 * N : 0x7fffffff;
         prefetch(make_rsrc(sX, sxb), PF_SX, B4{}, BM,
                  [&](int c) { return (int)(4u * (unsigned)(m0 + c)); });
-        prefetch(make_rsrc(sW, swb), PF_SW, B4{}, BN,
-                 [&](int c) { return (int)(4u * (unsigned)(n0 + c)); });
+        prefetch(make_rsrc(sW, swb), PF_SW, B4{}, BN, [&](int c) {
+            return (int)(4u * (unsigned)(EPI == EPI_GATED ? wrow(c) : n0 + c));
+        });
         if (nO > 0) {   // then K >= 16: chunk 0 lies inside every row
             prefetch(rXO, PF_XO, B16{}, 2 * BM, [&](int c) {
                 return (int)((unsigned)min(m0 + (c >> 1), T - 1) * 32u + 16u * (c & 1));
@@ -406,11 +379,10 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         else if (nO > 0) {   // chunk 0 of the gathered WO
             if constexpr (F16W)
                 prefetch(rWO, PF_WO, B16{}, 2 * BN, [&](int c) {
-                    return (int)((unsigned)min(n0 + (c >> 1), N - 1) * 32u + 16u * (c & 1));
+                    return (int)((unsigned)wrow(c >> 1) * 32u + 16u * (c & 1));
                 });
             else
-                prefetch(rWO, PF_WO, B16{}, BN,
-                         [&](int c) { return (int)((unsigned)min(n0 + c, N - 1) * 16u); });
+                prefetch(rWO, PF_WO, B16{}, BN, [&](int c) { return (int)((unsigned)wrow(c) * 16u); });
         }
     }
 #pragma unroll
@@ -424,6 +396,9 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         wait_loads_barrier<0>();
         lread(0, 0, 0);
     }
+    if constexpr (EPI != EPI_PLAIN)   // (visible after the barriers below)
+        if (tid < BN)
+            *reinterpret_cast<float *>(lds + PF_BIAS + 4 * tid) = bias_v;
 
     // the main loop, in a second copy with the fold's copies when this
     // call folds (the other copy is the plain loop)
@@ -463,8 +438,28 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
                         acc_out[(int64_t)t * N + n] = acc[a][b][r];
                 }
     }
-    if (nk == 0 || fold)   // prefetched operands landed; fold: every wave's WOT copies done
+    if (nk == 0 || fold || EPI != EPI_PLAIN)   // prefetched operands landed; fold: every wave's WOT copies done
         wait_loads_barrier<0>();
+    // (EPI_LINEAR, EPI_GATED: and the ring is free for the staging rows)
+    constexpr int CPRW = FN * 32 / 8;   // 16-byte chunks per sub-tile row
+    constexpr int NCH = FM * 32 * CPRW;
+    const int rbase = m0 + wm * FM * 32, cbase = n0 + wn * FN * 32;
+    int8_t *own = lds + wid * (FM * 32) * CPRW * 16;   // this wave's staging rows
+    // The residual's sub-tile comes into the staging rows, where the sums
+    // take its place; its loads pass while the outlier product runs.
+    auto load_residual = [&]() {
+#pragma unroll
+        for (int i = 0; i < NCH / 64; i++) {
+            const int id = i * 64 + lane, row = id / CPRW;
+            const int ch = (stage_off<CPRW>(row, id % CPRW) >> 4) - row * CPRW;   // (its own inverse)
+            load_to_lds_at(epi.residual + (int64_t)min(rbase + row, T - 1) * N + min(cbase + ch * 8, N - 8),
+                           own + i * 1024);
+        }
+    };
+    const bool res_lds = EPI == EPI_LINEAR && epi.residual && (N & 7) == 0;
+    if constexpr (EPI == EPI_LINEAR)
+        if (res_lds && !epi.pre)
+            load_residual();
     // token scales from the prefetch
     const int ltok = wm * FM * 32 + (lane & 31);                 // local token row
     const int lfea = wn * FN * 32 + (lane & 31);                 // local weight row
@@ -484,8 +479,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         voX[a] = (int)((unsigned)min(tok0 + 32 * a, T - 1) * 32u + khalf * 16u);
 #pragma unroll
     for (int b = 0; b < FN; b++)
-        voW[b] = (int)((unsigned)min(n0 + wn * FN * 32 + 32 * b + (lane & 31), N - 1) * 16u * WOE +
-                       khalf * 8 * WOE);
+        voW[b] = (int)((unsigned)wrow(wn * FN * 32 + 32 * b + (lane & 31)) * 16u * WOE + khalf * 8 * WOE);
     // chunk c of the outlier operands starts at c * cXO bytes of XO and c * cWO of WO
     const unsigned cXO = 32u * (unsigned)T, cWO = 16u * WOE * (unsigned)N;
     v8h ox[2][FM];
@@ -600,60 +594,199 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    if constexpr (!F16W)
-        load_sw();
-    // Y = fp16(fl32(D * sW)), four consecutive features per 8-byte LDS write
-    // into the wave's staging rows (one row per token).  The ring buffers
-    // are reused for the staging: every wave must be done reading them.
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    uint16_t *stg = reinterpret_cast<uint16_t *>(lds) + wid * (FM * 32) * RS;
-#pragma unroll
-    for (int a = 0; a < FM; a++)
+    if constexpr (EPI != EPI_PLAIN) {
+        // z = fl32(D * sW) + bias, in place
 #pragma unroll
         for (int b = 0; b < FN; b++)
 #pragma unroll
             for (int g = 0; g < 4; g++) {
-                const float s4[4] = {sw[b][g].x, sw[b][g].y, sw[b][g].z, sw[b][g].w};
-                float p[4];
+                const int c = fea0 - n0 + 32 * b + 8 * g;   // (a multiple of 4)
+                const float4 s4 = *reinterpret_cast<const float4 *>(lds + PF_SW + 4 * c);
+                const float4 b4 = *reinterpret_cast<const float4 *>(lds + PF_BIAS + 4 * c);
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    // fl32(D * sW) first, then one rounding to fp16: the
-                    // empty asm keeps the compiler from fusing the product
-                    // and the conversion into a single-rounding
-                    // v_fma_mixlo_f16
-                    p[j] = d[a][b][4 * g + j];
-                    if constexpr (!F16W)
-                        p[j] *= s4[j];
-                    asm("" : "+v"(p[j]));
+                for (int a = 0; a < FM; a++) {
+                    d[a][b][4 * g] = d[a][b][4 * g] * s4.x + b4.x;
+                    d[a][b][4 * g + 1] = d[a][b][4 * g + 1] * s4.y + b4.y;
+                    d[a][b][4 * g + 2] = d[a][b][4 * g + 2] * s4.z + b4.z;
+                    d[a][b][4 * g + 3] = d[a][b][4 * g + 3] * s4.w + b4.w;
                 }
-                *reinterpret_cast<uint2 *>(stg + (a * 32 + (lane & 31)) * RS + b * 32 + 8 * g +
-                                           4 * khalf) = make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
             }
-    // each wave stores its own sub-tile (only its own LDS rows: no barrier).
-    // Non-temporal stores: Y is not read again by this kernel, and output
-    // left dirty in the L2 is written back when the kernel ends, which the
-    // next kernel waits for (the 13B call: 77 -> 73 us)
-    constexpr int CPRW = FN * 32 / 8;   // 16-byte chunks per sub-tile row
-    constexpr int NCH = FM * 32 * CPRW;
-    const int rbase = m0 + wm * FM * 32, cbase = n0 + wn * FN * 32;
-    if ((N & 7) == 0) {
+        // staging place of token row 32a + (l & 31), block b's features 8g + 4 khalf ..
+        auto place = [&](auto cpr, int a, int b, int g) {
+            return reinterpret_cast<uint2 *>(
+                own + stage_off<decltype(cpr)::value>(a * 32 + (lane & 31), b * 4 + g) + 8 * khalf);
+        };
+        using CF = std::integral_constant<int, CPRW>;
+        auto round4 = [](const float (&p)[4]) {
+            return make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
+        };
+        // staged rows of CP chunks to `out` (row stride `ld`, chunk ch's first
+        // column given by colof, its features ending at `width` of their part)
+        auto store_rows = [&](auto cpr, uint16_t *out, int64_t ld, bool vec, auto colof) {
+            constexpr int CP = decltype(cpr)::value;
 #pragma unroll
-        for (int i = 0; i < NCH / 64; i++) {
-            const int id = i * 64 + lane, row = id / CPRW, ch = id % CPRW;
-            const v4i v = *reinterpret_cast<const v4i *>(stg + row * RS + ch * 8);
-            const int grow = rbase + row, gcol = cbase + ch * 8;
-            if (grow < T && gcol < N)
-                __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(Y + (int64_t)grow * N + gcol));
+            for (int i = 0; i < FM * 32 * CP / 64; i++) {
+                const int id = i * 64 + lane, row = id / CP, ch = id % CP;
+                const v4i v = *reinterpret_cast<const v4i *>(own + stage_off<CP>(row, ch));
+                int left;   // features of the chunk that exist
+                const int64_t col = colof(ch, left);
+                if (rbase + row >= T)
+                    continue;
+                uint16_t *dst = out + (int64_t)(rbase + row) * ld + col;
+                if (vec) {   // (rows and parts are multiples of 8 wide)
+                    if (left > 0)
+                        __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(dst));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (e < left)
+                            dst[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+                }
+            }
+        };
+        if (epi.pre) {
+#pragma unroll
+            for (int a = 0; a < FM; a++)
+#pragma unroll
+                for (int b = 0; b < FN; b++)
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {
+                        const float p[4] = {d[a][b][4 * g], d[a][b][4 * g + 1], d[a][b][4 * g + 2],
+                                            d[a][b][4 * g + 3]};
+                        *place(CF{}, a, b, g) = round4(p);
+                    }
+            if constexpr (EPI == EPI_GATED)
+                store_rows(CF{}, epi.pre, N, (F & 7) == 0, [&](int ch, int &left) {
+                    const int b = wn * FN + (ch >> 2), f = (n0 >> 1) + (b >> 1) * 32 + (ch & 3) * 8;
+                    left = F - f;
+                    return (b & 1) ? F + f : f;
+                });
+            else
+                store_rows(CF{}, epi.pre, N, (N & 7) == 0, [&](int ch, int &left) {
+                    left = N - (cbase + ch * 8);
+                    return cbase + ch * 8;
+                });
+            if constexpr (EPI == EPI_LINEAR)
+                if (res_lds) {
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the rows are read
+                    load_residual();
+                }
         }
-    } else {   // rows not 16-byte aligned: element stores
-        for (int i = 0; i < NCH / 64; i++) {
-            const int id = i * 64 + lane, row = id / CPRW, ch = id % CPRW;
-            const int grow = rbase + row;
+        auto finish = [&](auto kind_c) {
+            constexpr int KIND = decltype(kind_c)::value;
+            if constexpr (EPI == EPI_GATED) {
+                using CH = std::integral_constant<int, CPRW / 2>;
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int gcol = cbase + ch * 8 + e;
+                for (int a = 0; a < FM; a++)
+#pragma unroll
+                    for (int b = 0; b < FN; b += 2)
+#pragma unroll
+                        for (int g = 0; g < 4; g++) {
+                            float p[4];
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                p[j] = act_value<KIND>(d[a][b][4 * g + j], epi.act) * d[a][b + 1][4 * g + j];
+                            *place(CH{}, a, b >> 1, g) = round4(p);
+                        }
+            } else {
+                if (res_lds)
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (this wave's own rows)
+#pragma unroll
+                for (int a = 0; a < FM; a++)
+#pragma unroll
+                    for (int b = 0; b < FN; b++)
+#pragma unroll
+                        for (int g = 0; g < 4; g++) {
+                            float p[4];
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                p[j] = act_value<KIND>(d[a][b][4 * g + j], epi.act);
+                            if (res_lds) {
+                                const uint2 r = *place(CF{}, a, b, g);
+                                p[0] += h2f(r.x & 0xffffu);
+                                p[1] += h2f(r.x >> 16);
+                                p[2] += h2f(r.y & 0xffffu);
+                                p[3] += h2f(r.y >> 16);
+                            } else if (epi.residual) {   // rows not 16-byte aligned: element loads
+                                const int t = min(tok0 + 32 * a, T - 1), n = fea0 + 32 * b + 8 * g;
+#pragma unroll
+                                for (int j = 0; j < 4; j++)
+                                    p[j] += h2f(epi.residual[(int64_t)t * N + min(n + j, N - 1)]);
+                            }
+                            *place(CF{}, a, b, g) = round4(p);
+                        }
+            }
+        };
+        if (epi.act.kind == 0)
+            finish(std::integral_constant<int, 0>{});
+        else if (epi.act.kind == 1)
+            finish(std::integral_constant<int, 1>{});
+        else
+            finish(std::integral_constant<int, 2>{});
+        if constexpr (EPI == EPI_GATED)
+            store_rows(std::integral_constant<int, CPRW / 2>{}, Y, F, (F & 7) == 0, [&](int ch, int &left) {
+                const int f = (n0 >> 1) + (wn * (FN / 2) + (ch >> 2)) * 32 + (ch & 3) * 8;
+                left = F - f;
+                return f;
+            });
+        else
+            store_rows(CF{}, Y, N, (N & 7) == 0, [&](int ch, int &left) {
+                left = N - (cbase + ch * 8);
+                return cbase + ch * 8;
+            });
+    } else {
+        if constexpr (!F16W)
+            load_sw();
+        // Y = fp16(fl32(D * sW)), four consecutive features per 8-byte LDS write
+        // into the wave's staging rows (one row per token).  The ring buffers
+        // are reused for the staging: every wave must be done reading them.
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        uint16_t *stg = reinterpret_cast<uint16_t *>(lds) + wid * (FM * 32) * RS;
+#pragma unroll
+        for (int a = 0; a < FM; a++)
+#pragma unroll
+            for (int b = 0; b < FN; b++)
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const float s4[4] = {sw[b][g].x, sw[b][g].y, sw[b][g].z, sw[b][g].w};
+                    float p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        // fl32(D * sW) first, then one rounding to fp16: the
+                        // empty asm keeps the compiler from fusing the product
+                        // and the conversion into a single-rounding
+                        // v_fma_mixlo_f16
+                        p[j] = d[a][b][4 * g + j];
+                        if constexpr (!F16W)
+                            p[j] *= s4[j];
+                        asm("" : "+v"(p[j]));
+                    }
+                    *reinterpret_cast<uint2 *>(stg + (a * 32 + (lane & 31)) * RS + b * 32 + 8 * g +
+                                               4 * khalf) = make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
+                }
+        // each wave stores its own sub-tile (only its own LDS rows: no barrier).
+        // Non-temporal stores: Y is not read again by this kernel, and output
+        // left dirty in the L2 is written back when the kernel ends, which the
+        // next kernel waits for (the 13B call: 77 -> 73 us)
+        if ((N & 7) == 0) {
+#pragma unroll
+            for (int i = 0; i < NCH / 64; i++) {
+                const int id = i * 64 + lane, row = id / CPRW, ch = id % CPRW;
+                const v4i v = *reinterpret_cast<const v4i *>(stg + row * RS + ch * 8);
+                const int grow = rbase + row, gcol = cbase + ch * 8;
                 if (grow < T && gcol < N)
-                    Y[(int64_t)grow * N + gcol] = stg[row * RS + ch * 8 + e];
+                    __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(Y + (int64_t)grow * N + gcol));
+            }
+        } else {   // rows not 16-byte aligned: element stores
+            for (int i = 0; i < NCH / 64; i++) {
+                const int id = i * 64 + lane, row = id / CPRW, ch = id % CPRW;
+                const int grow = rbase + row;
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const int gcol = cbase + ch * 8 + e;
+                    if (grow < T && gcol < N)
+                        Y[(int64_t)grow * N + gcol] = stg[row * RS + ch * 8 + e];
+                }
             }
         }
     }
@@ -676,13 +809,33 @@ hipError_t launch_cfg(const int8_t *Wq, const float *sW, int64_t T, int64_t K, i
     const int32_t *idx = reinterpret_cast<const int32_t *>(ws + L.idx);
     const int32_t *wpre = reinterpret_cast<const int32_t *>(ws + L.wpre);
     if (acc)
-        hipLaunchKernelGGL((k_gemm<BM, BN, BKS, NS, WM, WN, GM, F16W, true>), grid, block, 0, s, Xq, Wq,
-                           sX, sW, meta, XO, WO, idx, wpre, (int)T, (int)K, (int)N, tiles_m, tiles_n, Y,
-                           acc);
+        hipLaunchKernelGGL((k_gemm<BM, BN, BKS, NS, WM, WN, GM, F16W, true, EPI_PLAIN>), grid, block, 0, s,
+                           Xq, Wq, sX, sW, meta, XO, WO, idx, wpre, (int)T, (int)K, (int)N, tiles_m, tiles_n,
+                           Y, acc, EpiParams{});
     else
-        hipLaunchKernelGGL((k_gemm<BM, BN, BKS, NS, WM, WN, GM, F16W, false>), grid, block, 0, s, Xq, Wq,
-                           sX, sW, meta, XO, WO, idx, wpre, (int)T, (int)K, (int)N, tiles_m, tiles_n, Y,
-                           acc);
+        hipLaunchKernelGGL((k_gemm<BM, BN, BKS, NS, WM, WN, GM, F16W, false, EPI_PLAIN>), grid, block, 0, s,
+                           Xq, Wq, sX, sW, meta, XO, WO, idx, wpre, (int)T, (int)K, (int)N, tiles_m, tiles_n,
+                           Y, acc, EpiParams{});
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int BKS, int NS, int WM, int WN, int GM, int EPI>
+hipError_t launch_epi_cfg(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
+                          uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s)
+{
+    // (a pair's tile of BN rows is BN/2 of its N/2 features)
+    const int tiles_m = (int)((T + BM - 1) / BM);
+    const int tiles_n = EPI == EPI_GATED ? (int)((N / 2 + BN / 2 - 1) / (BN / 2)) : (int)((N + BN - 1) / BN);
+    hipLaunchKernelGGL((k_gemm<BM, BN, BKS, NS, WM, WN, GM, false, false, EPI>),
+                       dim3((unsigned)(tiles_m * tiles_n)), dim3(WM * WN * 64), 0, s,
+                       reinterpret_cast<const int8_t *>(ws + L.Xq), Wq,
+                       reinterpret_cast<const float *>(ws + L.sX), sW,
+                       reinterpret_cast<const int32_t *>(ws + L.meta),
+                       reinterpret_cast<const uint16_t *>(ws + L.XO),
+                       reinterpret_cast<const int8_t *>(ws + L.WO),
+                       reinterpret_cast<const int32_t *>(ws + L.idx),
+                       reinterpret_cast<const int32_t *>(ws + L.wpre), (int)T, (int)K, (int)N, tiles_m,
+                       tiles_n, Y, nullptr, epi);
     return hipGetLastError();
 }
 
@@ -701,7 +854,7 @@ hipError_t launch_cfg(const int8_t *Wq, const float *sW, int64_t T, int64_t K, i
 // 512 x 5120 x 13824 one round of 256x128 tiles beats both.)
 constexpr int kCUs = 256;
 
-GemmPlan gemm_plan(int64_t T, int64_t K, int64_t N)
+GemmPlan gemm_plan(int64_t T, int64_t K, int64_t N, bool gated)
 {
     const int64_t tm = (T + 255) / 256;
     const int64_t big = tm * ((N + 255) / 256), mid = tm * ((N + 191) / 192),
@@ -716,9 +869,9 @@ GemmPlan gemm_plan(int64_t T, int64_t K, int64_t N)
     // copies cost the 256- and 192-wide main loops 19 and 10 us at about 30
     // outlier columns, where the gather costs 4-5 us)
     const bool fold_k = K <= kFoldMaxK;
-    if (cost_small < cost_big && cost_small <= cost_mid)
+    if (cost_small < cost_big && (cost_small <= cost_mid || gated))
         return {256, 128, fold_k ? 256 : 0};
-    if (cost_mid < cost_big)
+    if (cost_mid < cost_big && !gated)
         return {256, 192, 0};
     return {256, 256, 0};
 }
@@ -736,6 +889,21 @@ hipError_t launch_gemm(const int8_t *Wq, const float *sW, int64_t T, int64_t K, 
                      : launch_cfg<256, 192, 128, 2, 4, 2, 4, false>(Wq, sW, T, K, N, Y, acc, ws, L, s, WO);
     return fp16w ? launch_cfg<256, 256, 128, 2, 2, 4, 4, true>(Wq, sW, T, K, N, Y, acc, ws, L, s, WO)
                  : launch_cfg<256, 256, 128, 2, 2, 4, 4, false>(Wq, sW, T, K, N, Y, acc, ws, L, s, WO);
+}
+
+hipError_t launch_gemm_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
+                           uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s)
+{
+    const GemmPlan p = gemm_plan(T, K, N, epi.gated);
+    if (epi.gated)
+        return p.bn == 128
+                   ? launch_epi_cfg<256, 128, 128, 2, 4, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s)
+                   : launch_epi_cfg<256, 256, 128, 2, 2, 4, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s);
+    if (p.bn == 128)
+        return launch_epi_cfg<256, 128, 128, 2, 4, 2, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
+    if (p.bn == 192)
+        return launch_epi_cfg<256, 192, 128, 2, 4, 2, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
+    return launch_epi_cfg<256, 256, 128, 2, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
 }
 
 } // namespace li8

@@ -6,6 +6,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "act_math.h"
+#include "llm_int8.h"
+
 namespace li8 {
 
 // Largest K for which sum_{j<K} |q_x q_w| <= K * 127 * 127 fits in int32.
@@ -93,6 +96,11 @@ inline CacheLayout cache_layout(int64_t K, int64_t N)
     return C;
 }
 
+// Host checks shared by the entry points (api.hip): dimensions, and the
+// binary16 magnitude pattern H with |x| > thr <=> (bits(x) & 0x7fff) > H.
+li8_status check_shape(int64_t T, int64_t K, int64_t N);
+uint16_t threshold_magnitude(float thr);
+
 // Launchers (quant.hip).  All asynchronous on `s`; return hipGetLastError().
 hipError_t launch_quantize_weight(const uint16_t *W, int64_t N, int64_t K,
                                   int8_t *Wq, float *sW, hipStream_t s);
@@ -125,7 +133,23 @@ constexpr int64_t kFoldMaxK = 8192;
 struct GemmPlan {
     int bm, bn, fold;
 };
-GemmPlan gemm_plan(int64_t T, int64_t K, int64_t N);
+// gated: the N = 2F rows of a gated pair, whose tiles take gate and up rows in
+// pairs of 32-row blocks (not the 192-wide tiles, whose waves hold three blocks).
+GemmPlan gemm_plan(int64_t T, int64_t K, int64_t N, bool gated = false);
+
+// Variants of the kernels' epilogue.  EPI_PLAIN: Y = fp16(D * sW).
+enum { EPI_PLAIN, EPI_LINEAR, EPI_GATED };
+
+// What the other two do with z = fl32(D * sW) + bias.  EPI_LINEAR (gated
+// false): Y[T,N] = fp16(act(z) + residual); EPI_GATED (true): N = 2F and H[T,F] =
+// fp16(act(z_gate) * z_up).
+// pre: null, or [T,N] fp16 that receives z.
+struct EpiParams {
+    const uint16_t *bias, *residual;
+    uint16_t *pre;
+    ActParams act;
+    bool gated;
+};
 
 // Launcher (gemm.hip).
 // fp16w: the outlier product uses the fp16 weight columns that the prepare
@@ -135,6 +159,9 @@ hipError_t launch_gemm(const int8_t *Wq, const float *sW, int64_t T, int64_t K,
                        int64_t N, uint16_t *Y, int32_t *acc, const char *ws,
                        const WsLayout &L, bool fp16w, hipStream_t s,
                        const int8_t *WO = nullptr);
+hipError_t launch_gemm_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
+                           uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi,
+                           hipStream_t s);
 
 // Few-token path (decode.hip).  decode_shape(T, K) says whether both
 // entry points use it for this shape; the fused launch does the whole
@@ -144,6 +171,9 @@ bool decode_shape(int64_t T, int64_t K);
 hipError_t launch_decode_fused(const uint16_t *X, const int8_t *Wq, const float *sW,
                                const uint16_t *W16, uint16_t thr_mag, int64_t T, int64_t K,
                                int64_t N, uint16_t *Y, hipStream_t s);
+hipError_t launch_decode_epi(const uint16_t *X, const int8_t *Wq, const float *sW, uint16_t thr_mag,
+                             int64_t T, int64_t K, int64_t N, uint16_t *Y, const EpiParams &epi,
+                             hipStream_t s);
 hipError_t launch_decode_gemm(const int8_t *Wq, const float *sW, const uint16_t *W16, int64_t T,
                               int64_t K, int64_t N, uint16_t *Y, int32_t *acc, const char *ws,
                               const WsLayout &L, hipStream_t s);
@@ -167,12 +197,37 @@ struct SplitLayout {
 SplitLayout split_layout(int64_t T, int64_t K, int64_t N);
 hipError_t launch_split_fused(const uint16_t *X, const int8_t *Wq, const float *sW,
                               const uint16_t *W16, uint16_t thr_mag, int64_t T, int64_t K,
-                              int64_t N, uint16_t *Y, char *ws, hipStream_t s);
+                              int64_t N, uint16_t *Y, char *ws, hipStream_t s,
+                              const EpiParams *epi = nullptr);
 // The workspace route: codes, scales and outlier stages from launch_prepare,
 // the partial sums in the WO region (the few-token kernels never read it).
 hipError_t launch_split_gemm(const int8_t *Wq, const float *sW, const uint16_t *W16, int64_t T,
                              int64_t K, int64_t N, uint16_t *Y, int32_t *acc, const char *ws,
                              const WsLayout &L, hipStream_t s);
+
+// Gradients through the weight (backward.hip).  Np: N rounded up to a stage of
+// the product.  Most features: the operand's rows are reached with 32-bit
+// offsets from a tile's first row.
+constexpr int64_t kMaxGradN = (int64_t)1 << 21;
+constexpr int kMaxGradSplits = 32;
+constexpr int kMaxColStrips = 64;
+struct BackwardPlan {
+    int bm, splits;
+};
+BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N);
+// Workspace: the product's operand A fp16 [T,Np], its rows' factors fp32 [T],
+// dbias' partial sums fp32 [kMaxColStrips][N], the split product's partial
+// sums fp32 [splits][T,K].
+struct BackwardLayout {
+    size_t A, fac, cols, part, total;
+    int Np;
+};
+BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N);
+// gated: N = 2F, dY is dH [T,F].  pre, grad_pre, dbias may be null (pre: no
+// activation).  No workspace is used where N or T is 0.
+hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActParams &act, bool gated,
+                           const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
+                           uint16_t *dX, uint16_t *grad_pre, float *dbias, char *ws, hipStream_t s);
 
 // SmoothQuant-style W8A8 (smoothquant.hip).  Column absmax of fp16 A
 // [rows,K] as fp32; factors s and fl32(1/s); smoothed weight quantization;
