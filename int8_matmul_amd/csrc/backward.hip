@@ -315,8 +315,35 @@ __device__ __forceinline__ v8h codes_to_f16(v2i w)
 
 __device__ __forceinline__ v2i read_codes_tr(const int8_t *p)
 {
-    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((LI8_LDS v2i *)(uintptr_t)(LI8_LDS int8_t *)p);
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((LI8_LDS v2i *)const_cast<int8_t *>(p));
 }
+
+// A buffer's description as the four scalar words that the instruction takes.
+__device__ __forceinline__ v4i rsrc_words(const void *p, int bytes)
+{
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+               __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xffff),
+               __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+}
+
+// 16 bytes per lane from r at voffset + soffset into LDS at dst + 16*lane.  As
+// load_to_lds, but written out: behind the builtin the compiler lets every
+// transposing LDS read wait for all loads in flight (vmcnt(0)).  It has no
+// register to write, and what it writes to LDS is ordered by
+// wait_loads_barrier, which counts it.  M0 holds the LDS address (one wait state
+// before its use); nothing else in k_grad_gemm uses M0.
+__device__ __forceinline__ void load_to_lds_raw(v4i r, uint32_t dst, int voffset, int soffset)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(dst), "v"(voffset), "s"(r), "s"(soffset));
+}
+
+// Permutation of the 16-byte chunks of A's 128-byte rows: 16 rows' reads of one
+// chunk meet all banks, and rows 32 apart have the same one, so that a
+// lane's fragments are at constant distances.
+__device__ __forceinline__ int swz_a(int row) { return (row ^ ((row >> 3) & 3)) & 7; }
 
 template <int BM, int NS, int WM, int WN, int GM, bool SPLIT>
 __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
@@ -365,12 +392,12 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
     // of A than threads the waves fill them twice over, with the same bytes, so
     // that every wave counts the same loads ----
     const int rows = min(BM, T - m0);
-    const __amdgpu_buffer_rsrc_t rA = make_rsrc(A + (int64_t)m0 * Np, 2 * rows * Np);
-    const __amdgpu_buffer_rsrc_t rB = make_rsrc(Wq, N * K);
+    const v4i rA = rsrc_words(A + (int64_t)m0 * Np, 2 * rows * Np), rB = rsrc_words(Wq, N * K);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LI8_LDS int8_t *)lds;
     int voA[LA], voB[LB], rowB[LB];
 #pragma unroll
     for (int i = 0; i < LA; i++) {
-        const int p = (i * NT + tid) % CA, row = p >> 3, q = (p & 7) ^ swz<8>(row);
+        const int p = (i * NT + tid) % CA, row = p >> 3, q = (p & 7) ^ swz_a(row);
         voA[i] = min(row, rows - 1) * Np * 2 + q * 16;
     }
 #pragma unroll
@@ -379,31 +406,29 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
         voB[i] = row * K + k;
         rowB[i] = k < K ? N - row : 0;   // the row exists while n0 < rowB
     }
-    auto issue = [&](int it) {
+    auto issue = [&](int it, int buf) {
         const int n0 = (st0 + it) * kGN;
-        int8_t *st = lds + (it % NS) * SSZ;
+        const uint32_t dst = lds0 + (uint32_t)buf;
 #pragma unroll
         for (int i = 0; i < LA; i++)
-            load_to_lds(rA, st + ((i * NT + wid * 64) % CA) * 16, voA[i], 2 * n0);
+            load_to_lds_raw(rA, dst + ((i * NT + wid * 64) % CA) * 16, voA[i], 2 * n0);
 #pragma unroll
         for (int i = 0; i < LB; i++)
-            load_to_lds(rB, st + ASZ + (i * NT + wid * 64) * 16, n0 < rowB[i] ? voB[i] : kOutOfRange, n0 * K);
+            load_to_lds_raw(rB, dst + ASZ + (i * NT + wid * 64) * 16, n0 < rowB[i] ? voB[i] : kOutOfRange, n0 * K);
     };
 
     // ---- fragments ----
+    // lane l supplies token row l & 31 of each block and the 16 bytes of chunk
+    // 2 kk + (l >> 5) of k-step kk; of the weight it reads half (l & 1) of the
+    // chunk of 16 columns (l >> 4) & 1 in row 8 (l >> 5) + (l & 15) / 2 of the
+    // k-step, and gets column l & 31.  Everything else is a constant offset.
     const int khalf = lane >> 5;
-    int offA[FM][KS], offB[FK];
-#pragma unroll
-    for (int a = 0; a < FM; a++) {
-        const int row = wm * FM * 32 + a * 32 + (lane & 31);
+    int offA[KS], offB[FK];
+    {
+        const int row = wm * FM * 32 + (lane & 31), r = (lane & 15) >> 1;
 #pragma unroll
         for (int kk = 0; kk < KS; kk++)
-            offA[a][kk] = row * 128 + (((kk * 2 + khalf) ^ swz<8>(row)) * 16);
-    }
-    // lane l reads half (l & 1) of the chunk of 16 columns (l >> 4) & 1 in row
-    // 8 (l >> 5) + (l & 15) / 2 of the k-step, and gets column l & 31
-    {
-        const int r = (lane & 15) >> 1;
+            offA[kk] = row * 128 + (((kk * 2 + khalf) ^ swz_a(row)) * 16);
 #pragma unroll
         for (int b = 0; b < FK; b++) {
             const int c = (wn * FK + b) * 2 + ((lane >> 4) & 1);
@@ -417,28 +442,50 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
         for (int b = 0; b < FK; b++)
             acc[a][b] = v16f{};
 
-    v8h fa[2][FM];
-    v2i fb[2][FK];
-    auto lread = [&](int set, int it, int kk) {
-        const int8_t *base = lds + (it % NS) * SSZ;
+    // Fragments of two k-steps: while one is multiplied the next is read, and
+    // its codes are converted behind the first products.
+    v8h fa[2][FM], fb[2][FK];
+    v2i raw[FK];
+    auto lread = [&](int set, int st, int kk) {
+#pragma unroll
+        for (int b = 0; b < FK; b++)
+            raw[b] = read_codes_tr(lds + st + offB[b] + kk * 16 * kGK);
 #pragma unroll
         for (int a = 0; a < FM; a++)
-            fa[set][a] = *reinterpret_cast<const v8h *>(base + offA[a][kk]);
+            fa[set][a] = *reinterpret_cast<const v8h *>(lds + st + offA[kk] + a * 32 * 128);
+    };
+    auto convert = [&](int set) {
 #pragma unroll
         for (int b = 0; b < FK; b++)
-            fb[set][b] = read_codes_tr(base + offB[b] + kk * 16 * kGK);
+            fb[set][b] = codes_to_f16(raw[b]);
     };
     auto mfmas = [&](int set) {
-        v8h wf[FK];
-#pragma unroll
-        for (int b = 0; b < FK; b++)
-            wf[b] = codes_to_f16(fb[set][b]);
 #pragma unroll
         for (int a = 0; a < FM; a++)
 #pragma unroll
             for (int b = 0; b < FK; b++)
-                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wf[b], fa[set][a], acc[a][b], 0, 0, 0);
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[set][b], fa[set][a], acc[a][b], 0, 0, 0);
     };
+    // One MFMA with up to two LDS reads after it until they are all issued, then
+    // with the conversions' share
+    constexpr int NMF = FM * FK, NRD = FM + FK, RPM = (NRD + NMF / 2) / (NMF / 2 ? NMF / 2 : 1);
+    auto interleave = [&](int nld) {
+        int rd = 0;
+#pragma unroll
+        for (int i = 0; i < NMF; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (rd < NRD) {
+                __builtin_amdgcn_sched_group_barrier(0x100, RPM, 0);
+                rd += RPM;
+            } else {
+                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+            }
+            if (i < nld)
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int st = 0;   // this stage's ring buffer
     auto stage = [&](int it, auto wait_c, auto issue_c, auto last_c) {
         constexpr int WAIT = decltype(wait_c)::value;
         constexpr bool ISSUE = decltype(issue_c)::value;
@@ -447,14 +494,19 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
         for (int kk = 0; kk < KS; kk++) {
             const int cur = kk & 1;
             if (kk + 1 < KS) {
-                lread(cur ^ 1, it, kk + 1);
+                lread(cur ^ 1, st, kk + 1);
                 mfmas(cur);
+                convert(cur ^ 1);
+                interleave(0);
             } else if constexpr (!LAST) {
                 wait_loads_barrier<WAIT>();   // stage it+1 landed; stage it read by all
                 if constexpr (ISSUE)
-                    issue(it + NS);
-                lread(cur ^ 1, it + 1, 0);
+                    issue(it + NS, st);
+                st = st + SSZ == NS * SSZ ? 0 : st + SSZ;
+                lread(cur ^ 1, st, 0);
                 mfmas(cur);
+                convert(cur ^ 1);
+                interleave(ISSUE ? LA + LB : 0);
             } else {
                 mfmas(cur);
             }
@@ -474,12 +526,13 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
 #pragma unroll
     for (int s = 0; s < NS; s++)
         if (s < ns)
-            issue(s);
+            issue(s, s * SSZ);
     if (ns >= NS)
         wait_loads_barrier<(NS - 1) * (LA + LB)>();   // stage 0 landed
     else
         wait_loads_barrier<0>();
     lread(0, 0, 0);
+    convert(0);
     int it = 0;
     for (; it + NS < ns; it++)      // steady state
         stage(it, WS{}, TT{}, TF{});
