@@ -916,42 +916,71 @@ def kv_attention(Q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float |
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
-def _activation(name: str) -> int:
-    if name not in ACTIVATIONS:
-        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
-    return ACTIVATIONS[name]
+def _matrix(t: torch.Tensor, name: str) -> torch.device:
+    """Checks an fp16 [rows, columns] tensor on a GPU and returns its device."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.float16 and t.dim() == 2
+            and t.is_contiguous()):
+        _require(t, torch.float16, name, 2)
+    return t.device
 
 
-def _fitted(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tuple, device) -> torch.Tensor | None:
-    """Checks an optional tensor of a known shape on a known device."""
-    if t is not None:
+def _fitted(t: torch.Tensor, dtype: torch.dtype, name: str, shape: tuple, device) -> int:
+    """Checks a tensor of a known shape on a known device and returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device):
         _require(t, dtype, name, len(shape))
-        if tuple(t.shape) != shape or t.device != device:
-            raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
-    return t
+        raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _weight(Wq: torch.Tensor, sW: torch.Tensor, device, gated: bool) -> tuple:
-    _require(Wq, torch.int8, "Wq", 2)
-    N, K = Wq.shape
-    _require(sW, torch.float32, "sW", 1)
-    if sW.shape[0] != N:
-        raise ValueError(f"shape mismatch: Wq {tuple(Wq.shape)}, sW {tuple(sW.shape)}")
-    if gated and N % 2:
-        raise ValueError(f"a gated pair's weight has an even number of rows, got {N}")
-    for name, t in (("Wq", Wq), ("sW", sW)):
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return N, K
+def _weight(Wq: torch.Tensor, sW: torch.Tensor, device, gated: bool) -> torch.Size:
+    if not (isinstance(Wq, torch.Tensor) and Wq.dtype is torch.int8 and Wq.dim() == 2 and Wq.is_contiguous()
+            and Wq.device == device):
+        _require(Wq, torch.int8, "Wq", 2)
+        raise ValueError(f"Wq is on {Wq.device}, expected {device}")
+    shape = Wq.shape
+    _fitted(sW, torch.float32, "sW", shape[:1], device)
+    if gated and shape[0] % 2:
+        raise ValueError(f"a gated pair's weight has an even number of rows, got {shape[0]}")
+    return shape
 
 
-def _scratch(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor:
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _require(workspace, torch.uint8, "workspace", 1)
-    if workspace.device != device:
+def _scratch(workspace: torch.Tensor, device) -> tuple:
+    if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.dim() == 1
+            and workspace.is_contiguous() and workspace.device == device):
+        _require(workspace, torch.uint8, "workspace", 1)
         raise ValueError(f"workspace is on {workspace.device}, expected {device}")
-    return workspace
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _forward(name: str, X, Wq, sW, threshold, bias, activation, residual, out, pre, workspace, gated):
+    dev = _matrix(X, "X")
+    T, K = X.shape
+    N, KW = _weight(Wq, sW, dev, gated)
+    if KW != K:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Wq {tuple(Wq.shape)}")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    half = torch.float16
+    F = N // 2 if gated else N
+    if out is None:
+        out = torch.empty((T, F), dtype=half, device=dev)
+        y = out.data_ptr()
+    else:
+        y = _fitted(out, half, "out", (T, F), dev)
+    b = None if bias is None else _fitted(bias, half, "bias", (N,), dev)
+    p = None if pre is None else _fitted(pre, half, "pre", (T, N), dev)
+    if workspace is None:
+        need = linear_workspace_bytes(T, K, N)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws, size = (None, 0) if workspace is None else _scratch(workspace, dev)
+    if gated:
+        _kv_call(name, dev, X.data_ptr(), Wq.data_ptr(), sW.data_ptr(), threshold, T, K, F, b, act, y, p, ws, size)
+    else:
+        r = None if residual is None else _fitted(residual, half, "residual", (T, N), dev)
+        _kv_call(name, dev, X.data_ptr(), Wq.data_ptr(), sW.data_ptr(), threshold, T, K, N, b, act, r, y, p, ws, size)
+    return out
 
 
 def linear_epilogue(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold: float = 6.0,
@@ -963,24 +992,8 @@ def linear_epilogue(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, thresho
     ``bias`` fp16 [N]; ``activation`` one of ACTIVATIONS; ``residual`` fp16 [T,N],
     which may be ``out`` itself; ``pre`` fp16 [T,N] receives Z + bias for
     ``linear_backward``.  The workspace is that of ``linear``."""
-    _require(X, torch.float16, "X", 2)
-    T, K = X.shape
-    dev = X.device
-    N, KW = _weight(Wq, sW, dev, False)
-    if KW != K:
-        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Wq {tuple(Wq.shape)}")
-    act = _activation(activation)
-    _fitted(bias, torch.float16, "bias", (N,), dev)
-    _fitted(residual, torch.float16, "residual", (T, N), dev)
-    _fitted(pre, torch.float16, "pre", (T, N), dev)
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.float16, device=dev)
-    else:
-        _fitted(out, torch.float16, "out", (T, N), dev)
-    ws = _scratch(workspace, 0 if workspace is not None else linear_workspace_bytes(T, K, N), dev)
-    _kv_call("llm_int8_linear_epilogue", dev, X.data_ptr(), Wq.data_ptr(), sW.data_ptr(), float(threshold), T, K, N,
-             _ptr(bias), act, _ptr(residual), out.data_ptr(), _ptr(pre), ws.data_ptr(), ws.numel())
-    return out
+    return _forward("llm_int8_linear_epilogue", X, Wq, sW, float(threshold), bias, activation, residual, out, pre,
+                    workspace, False)
 
 
 def gated_linear(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold: float = 6.0,
@@ -991,24 +1004,8 @@ def gated_linear(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold:
 
     ``bias`` fp16 [2F]; ``pre`` fp16 [T,2F] receives [G | U] for ``gated_backward``.
     The workspace is that of ``linear`` for N = 2F."""
-    _require(X, torch.float16, "X", 2)
-    T, K = X.shape
-    dev = X.device
-    N, KW = _weight(Wq, sW, dev, True)
-    if KW != K:
-        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Wq {tuple(Wq.shape)}")
-    F = N // 2
-    act = _activation(activation)
-    _fitted(bias, torch.float16, "bias", (N,), dev)
-    _fitted(pre, torch.float16, "pre", (T, N), dev)
-    if out is None:
-        out = torch.empty((T, F), dtype=torch.float16, device=dev)
-    else:
-        _fitted(out, torch.float16, "out", (T, F), dev)
-    ws = _scratch(workspace, 0 if workspace is not None else linear_workspace_bytes(T, K, N), dev)
-    _kv_call("llm_int8_gated_linear", dev, X.data_ptr(), Wq.data_ptr(), sW.data_ptr(), float(threshold), T, K, F,
-             _ptr(bias), act, out.data_ptr(), _ptr(pre), ws.data_ptr(), ws.numel())
-    return out
+    return _forward("llm_int8_gated_linear", X, Wq, sW, float(threshold), bias, activation, None, out, pre, workspace,
+                    True)
 
 
 def backward_workspace_bytes(T: int, K: int, N: int) -> int:
@@ -1021,25 +1018,33 @@ def new_backward_workspace(T: int, K: int, N: int, device) -> torch.Tensor:
 
 
 def _backward(name: str, dY, pre, Wq, sW, activation, out, grad_pre, dbias, workspace, gated):
-    _require(dY, torch.float16, "dH" if gated else "dY", 2)
-    dev = dY.device
+    dev = _matrix(dY, "dH" if gated else "dY")
     N, K = _weight(Wq, sW, dev, gated)
     T, F = dY.shape
     if F * (2 if gated else 1) != N:
         raise ValueError(f"shape mismatch: {'dH' if gated else 'dY'} {tuple(dY.shape)}, Wq {tuple(Wq.shape)}")
-    act = _activation(activation)
-    if pre is None and (gated or act):
-        raise TypeError("pre must be a torch.Tensor")
-    _fitted(pre, torch.float16, "pre", (T, N), dev)
-    _fitted(grad_pre, torch.float16, "grad_pre", (T, N), dev)
-    _fitted(dbias, torch.float32, "dbias", (N,), dev)
-    if out is None:
-        out = torch.empty((T, K), dtype=torch.float16, device=dev)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    half = torch.float16
+    if pre is None:
+        if gated or act:
+            raise TypeError("pre must be a torch.Tensor")
+        z = None
     else:
-        _fitted(out, torch.float16, "out", (T, K), dev)
-    ws = _scratch(workspace, 0 if workspace is not None else backward_workspace_bytes(T, K, N), dev)
-    _kv_call(name, dev, dY.data_ptr(), _ptr(pre), act, Wq.data_ptr(), sW.data_ptr(), T, K, F, out.data_ptr(),
-             _ptr(grad_pre), _ptr(dbias), ws.data_ptr(), ws.numel())
+        z = _fitted(pre, half, "pre", (T, N), dev)
+    g = None if grad_pre is None else _fitted(grad_pre, half, "grad_pre", (T, N), dev)
+    b = None if dbias is None else _fitted(dbias, torch.float32, "dbias", (N,), dev)
+    if out is None:
+        out = torch.empty((T, K), dtype=half, device=dev)
+        x = out.data_ptr()
+    else:
+        x = _fitted(out, half, "out", (T, K), dev)
+    if workspace is None:
+        need = backward_workspace_bytes(T, K, N)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws, size = (None, 0) if workspace is None else _scratch(workspace, dev)
+    _kv_call(name, dev, dY.data_ptr(), z, act, Wq.data_ptr(), sW.data_ptr(), T, K, F, x, g, b, ws, size)
     return out
 
 

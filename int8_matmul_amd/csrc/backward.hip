@@ -383,9 +383,9 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
     const int first_m = (bid / width) * GM;
     const int gm = min(tiles_m - first_m, GM);
     const int m0 = (first_m + (bid % width) % gm) * BM, k0 = (bid % width) / gm * kGK;
-    const int nst = Np / kGN;
-    const int st0 = (int)((int64_t)nst * sp / splits), st1 = (int)((int64_t)nst * (sp + 1) / splits);
-    const int ns = st1 - st0;   // (at least 1: splits <= nst)
+    const int nst = Np / kGN, stages = nst / splits, more = nst - stages * splits;
+    const int st0 = sp * stages + min(sp, more);
+    const int ns = stages + (sp < more ? 1 : 0);   // (at least 1: splits <= nst)
 
     // ---- loaders: load i of this lane fills chunk p = i*NT + tid of A's, or of
     // the weight's, rows (A: row p / 8, weight: row p / 16); with fewer chunks
@@ -586,29 +586,375 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
     }
 }
 
-// dX = fp16(fac * sum of the parts, in order); no part (N = 0): zeros.
+// ---------------------------------------------------------------------------
+// Few rows (T <= 64): one kernel from dY to partial sums of dX.  A workgroup has
+// 256 columns of dX and a range of weight rows n; it forms its range's dZ for all
+// rows itself (cheap, and the same inputs serve all column tiles from the
+// L2), so nothing has to wait for a kernel that knows whole rows: the power of
+// two of a row is that of its largest value so far, and the sums so far are
+// brought to the new one when it grows, exactly.  The weight's codes are
+// requested before anything else.  Every range's workgroup of the first
+// column tile sees all rows of its dZ: it writes dbias and grad_pre.
+// 8 waves of 32 columns, BM rows.  Half a wave forms a row's chunk of at most 256
+// n, so its maximum is a reduction over 32 lanes.  CS is the stages of 64 n of a
+// chunk: 4 for a range that is no longer than that; else 3 (24 of the 32 lanes),
+// with LDS for the codes of two chunks: while a chunk is multiplied, the next one's
+// inputs come into registers and its codes into the other half of the ring.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 64;      // most rows
+
+// KIND of a linear gradient without an activation: dZ = dY, Z is not read.
+constexpr int kNoAct = 3;
+
+// Inputs of the eight weight rows n .. n+7 (of a pair: of gate or up rows) in
+// row t as they are in memory; 0 past the ends.  Buffer loads at an offset
+// past the end where there is nothing to read: no branches.
+template <bool GATED, int KIND, bool VEC>
+struct RawRows {
+    static constexpr bool kPre = KIND != kNoAct;
+    uint32_t d[4], g[kPre ? 4 : 1], u[GATED ? 4 : 1];
+
+    struct Source {
+        __amdgpu_buffer_rsrc_t dY, pre;
+    };
+    static __device__ __forceinline__ Source source(const GradArgs &a)
+    {
+        const int F = GATED ? a.N >> 1 : a.N;   // (64 rows of 2^21 features at most: offsets fit)
+        return {make_rsrc(a.dY, 2 * a.T * F), make_rsrc(a.pre, kPre ? 2 * a.T * a.N : 0)};
+    }
+
+    __device__ __forceinline__ void load(const Source &s, const GradArgs &a, int t, int n)
+    {
+        const int F = GATED ? a.N >> 1 : a.N;
+        const bool row = t < a.T;
+        if constexpr (VEC) {   // (F is a multiple of 8: all of one part)
+            const int f = GATED && n >= F ? n - F : n;
+            const bool ok = row && n < a.N;
+            vec(s.dY, ok ? 2 * (t * F + f) : kOutOfRange, d);
+            if constexpr (kPre)
+                vec(s.pre, ok ? 2 * (t * a.N + f) : kOutOfRange, g);
+            if constexpr (GATED)
+                vec(s.pre, ok ? 2 * (t * a.N + F + f) : kOutOfRange, u);
+        } else {
+            uint32_t h[3][8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int f = GATED && n + e >= F ? n + e - F : n + e;
+                const bool ok = row && n + e < a.N;
+                h[0][e] = __builtin_amdgcn_raw_buffer_load_b16(s.dY, ok ? 2 * (t * F + f) : kOutOfRange, 0, 0);
+                if constexpr (kPre)
+                    h[1][e] = __builtin_amdgcn_raw_buffer_load_b16(s.pre, ok ? 2 * (t * a.N + f) : kOutOfRange, 0, 0);
+                if constexpr (GATED)
+                    h[2][e] =
+                        __builtin_amdgcn_raw_buffer_load_b16(s.pre, ok ? 2 * (t * a.N + F + f) : kOutOfRange, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                d[i] = h[0][2 * i] | h[0][2 * i + 1] << 16;
+                if constexpr (kPre)
+                    g[i] = h[1][2 * i] | h[1][2 * i + 1] << 16;
+                if constexpr (GATED)
+                    u[i] = h[2][2 * i] | h[2][2 * i + 1] << 16;
+            }
+        }
+    }
+
+    // dZ of them
+    __device__ __forceinline__ void grad(const GradArgs &a, int n, float (&z)[8]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int sh = 16 * (e & 1);
+            const float dv = h2f((d[e >> 1] >> sh) & 0xffffu);
+            if constexpr (!kPre) {
+                z[e] = dv;
+            } else {
+                float v, s;
+                act_value_slope<KIND>(h2f((g[e >> 1] >> sh) & 0xffffu), a.act, v, s);
+                if constexpr (GATED)
+                    z[e] = n + e >= a.N >> 1 ? dv * v : dv * h2f((u[e >> 1] >> sh) & 0xffffu) * s;
+                else
+                    z[e] = dv * s;
+            }
+        }
+    }
+
+private:
+    static __device__ __forceinline__ void vec(__amdgpu_buffer_rsrc_t r, int off, uint32_t (&w)[4])
+    {
+        const v4i x = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            w[i] = (uint32_t)x[i];
+    }
+};
+
+// Maximum over the 32 lanes of each half of a wave, in every lane of it.
+__device__ __forceinline__ uint32_t half_wave_max(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));    // [1,0,3,2]
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));    // [2,3,0,1]
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));   // half mirror
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));   // row mirror
+    const auto r16 = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max((uint32_t)r16[0], (uint32_t)r16[1]);
+}
+
+template <bool GATED, int KIND, bool VEC, int BM, int CS>
+__global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__restrict__ Wq, int K,
+                                                  int stages, int more, uint16_t *__restrict__ dX,
+                                                  float *__restrict__ part, float *__restrict__ dbias)
+{
+    constexpr int kFewCS = CS, kFewChunk = CS * kGN, kFewStages = CS == 4 ? 4 : 2 * CS;
+    constexpr int NT = 512, FM = BM / 32, PASSES = BM / 16, KS = kGN / 16;
+    constexpr int BSZ = kGN * kGK, ASZ = BM * 128;    // a stage of codes, of A
+    constexpr int LB = BSZ / 16 / NT;
+    constexpr int oA = kFewStages * BSZ, oSum = oA + kFewCS * ASZ, oRow = oSum + 16 * kFewChunk * 4;
+    __shared__ __attribute__((aligned(1024))) int8_t lds[oRow + 2 * BM * 4];
+    float *sums = reinterpret_cast<float *>(lds + oSum);   // [16 half waves][chunk] column sums
+    float *grow = reinterpret_cast<float *>(lds + oRow);   // [BM] what the sums so far are multiplied by
+    float *unit = grow + BM;                               // [BM] a row's unit at the end
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // range sp of the weight's rows: `stages` stages, one more in the first `more` ranges
+    const int tile = blockIdx.x, sp = blockIdx.y, k0 = tile * kGK;
+    const int st0 = sp * stages + min(sp, more), ns = stages + (sp < more ? 1 : 0);
+
+    // ---- the weight's codes (as in k_grad_gemm) ----
+    const v4i rB = rsrc_words(Wq, a.N * K);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LI8_LDS int8_t *)lds;
+    int voB[LB], rowB[LB];
+#pragma unroll
+    for (int i = 0; i < LB; i++) {
+        const int p = i * NT + tid, row = p >> 4, k = k0 + 16 * ((p & 15) ^ (2 * (row & 7)));
+        voB[i] = row * K + k;
+        rowB[i] = k < K ? a.N - row : 0;
+    }
+    auto issue = [&](int it) {
+        const int n0 = (st0 + it) * kGN;
+#pragma unroll
+        for (int i = 0; i < LB; i++)
+            load_to_lds_raw(rB, lds0 + (uint32_t)(it % kFewStages) * BSZ + (i * NT + wid * 64) * 16,
+                            n0 < rowB[i] ? voB[i] : kOutOfRange, n0 * K);
+    };
+#pragma unroll
+    for (int it = 0; it < kFewStages; it++)
+        if (it < ns)
+            issue(it);
+
+    const int half = tid >> 5, l32 = tid & 31;   // half wave 0..15: rows half, half + 16, ...
+    uint32_t expo[PASSES];                       // biased exponent of the rows' units so far
+#pragma unroll
+    for (int p = 0; p < PASSES; p++)
+        expo[p] = 20;
+    v16f acc[FM];
+#pragma unroll
+    for (int m = 0; m < FM; m++)
+        acc[m] = v16f{};
+    const int khalf = lane >> 5, arow = lane & 31;
+    int offA[KS], offB;
+#pragma unroll
+    for (int kk = 0; kk < KS; kk++)
+        offA[kk] = oA + arow * 128 + (((kk * 2 + khalf) ^ swz_a(arow)) * 16);
+    {
+        const int r = (lane & 15) >> 1, c = wid * 2 + ((lane >> 4) & 1);
+        offB = (8 * khalf + r) * kGK + ((c ^ (2 * r)) * 16) + 8 * (lane & 1);
+    }
+
+    using Raw = RawRows<GATED, KIND, VEC>;
+    Raw raw[PASSES];
+    const typename Raw::Source src = Raw::source(a);
+    const __amdgpu_buffer_rsrc_t rS = make_rsrc(a.sW, 4 * a.N);
+    float w[8];
+    // inputs of the chunk that starts with stage c0 (lanes past the range, or
+    // past the chunk, take none: those rows are the next workgroup's)
+    auto load = [&](int c0) {
+        const int n = (st0 + c0) * kGN + 8 * l32;
+        const bool in = 8 * l32 < min(kFewCS, ns - c0) * kGN;
+#pragma unroll
+        for (int p = 0; p < PASSES; p++)
+            raw[p].load(src, a, in ? half + 16 * p : a.T, n);
+        // (past the last row of the weight: zeros)
+        const v4i lo = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rS, in ? 4 * n : kOutOfRange, 0, 0));
+        const v4i hi =
+            __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rS, in ? 4 * n + 16 : kOutOfRange, 0, 0));
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            w[e] = __builtin_bit_cast(float, (int)lo[e]);
+            w[4 + e] = __builtin_bit_cast(float, (int)hi[e]);
+        }
+    };
+    load(0);
+    for (int c0 = 0; c0 < ns; c0 += kFewCS) {
+        const int cs = min(kFewCS, ns - c0);
+        const int n = (st0 + c0) * kGN + 8 * l32;
+        const bool in = 8 * l32 < cs * kGN;
+        float sum[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            sum[e] = 0.0f;
+#pragma unroll
+        for (int p = 0; p < PASSES; p++) {
+            const int t = half + 16 * p;
+            if (p > 0 && 16 * p >= a.T) {   // (rows that do not exist: zeros, once)
+                if (c0 == 0) {
+                    if (l32 == 0)
+                        grow[t] = unit[t] = 0.0f;
+                    for (int q = l32; q < kFewCS * 8; q += 32)
+                        *reinterpret_cast<uint4 *>(lds + oA + (q >> 3) * ASZ + t * 128 + (q & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
+                continue;
+            }
+            float z[8];
+            raw[p].grad(a, n, z);   // (zeros for rows and lanes without inputs)
+            if (tile == 0 && a.grad_pre && in && t < a.T)
+                store8<VEC>(a.grad_pre + (int64_t)t * a.N + n, a.N - n, z);
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                sum[e] += z[e];
+                z[e] *= w[e];
+                m = max(m, __builtin_bit_cast(uint32_t, z[e]) & 0x7fffffffu);
+            }
+            m = half_wave_max(m);
+            const uint32_t e8 = m >> 23, old = expo[p];
+            // (a row with infinities or NaN keeps its unit and its infinities)
+            const uint32_t now = e8 == 255 ? old : max(old, e8);
+            expo[p] = now;
+            const float scale = __builtin_bit_cast(float, (268u - now) << 23);
+            if (l32 == 0) {
+                const int d = 127 + (int)old - (int)now;   // 2^(old - now), 0 where that is no fp32 number
+                grow[t] = d > 0 ? __builtin_bit_cast(float, (uint32_t)d << 23) : 0.0f;
+                unit[t] = __builtin_bit_cast(float, (now - 14u) << 23);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                z[e] *= scale;
+                asm("" : "+v"(z[e]));
+            }
+            const int ss = l32 >> 3, q = l32 & 7;
+            if (ss < kFewCS)
+                *reinterpret_cast<uint4 *>(lds + oA + ss * ASZ + t * 128 + ((q ^ swz_a(t)) * 16)) =
+                    make_uint4(pack_f16x2(z[0], z[1]), pack_f16x2(z[2], z[3]), pack_f16x2(z[4], z[5]),
+                               pack_f16x2(z[6], z[7]));
+        }
+        if (tile == 0 && dbias && in)
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                sums[half * kFewChunk + 8 * l32 + e] = sum[e];
+        wait_loads_barrier<0>();   // the chunk's codes landed; A, grow and the sums are there
+        if (c0 + cs < ns) {
+            // the other half of the ring is free since the last barrier but one
+            if (c0 > 0)
+                for (int it = c0 + cs; it < min(ns, c0 + cs + kFewCS); it++)
+                    issue(it);
+            load(c0 + cs);
+        }
+        if (tile == 0 && dbias && tid < cs * kGN) {
+            const int nn = (st0 + c0) * kGN + tid;
+            if (nn < a.N) {
+                float v = 0.0f;
+#pragma unroll
+                for (int h = 0; h < 16; h++)
+                    v += sums[h * kFewChunk + tid];
+                dbias[nn] = v;
+            }
+        }
+        if (c0 > 0) {
+#pragma unroll
+            for (int m = 0; m < FM; m++) {
+                const float g = grow[arow + 32 * m];
+#pragma unroll
+                for (int r = 0; r < 16; r++)
+                    acc[m][r] *= g;
+            }
+        }
+        for (int ss = 0; ss < cs; ss++) {
+            const int8_t *b = lds + (c0 + ss) % kFewStages * BSZ + offB;
+            v2i codes[KS];
+            v8h fa[KS][FM];
+#pragma unroll
+            for (int kk = 0; kk < KS; kk++) {
+                codes[kk] = read_codes_tr(b + kk * 16 * kGK);
+#pragma unroll
+                for (int m = 0; m < FM; m++)
+                    fa[kk][m] = *reinterpret_cast<const v8h *>(lds + ss * ASZ + offA[kk] + m * 32 * 128);
+            }
+#pragma unroll
+            for (int kk = 0; kk < KS; kk++) {
+                const v8h fb = codes_to_f16(codes[kk]);
+#pragma unroll
+                for (int m = 0; m < FM; m++)
+                    acc[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, fa[kk][m], acc[m], 0, 0, 0);
+            }
+        }
+        if (c0 + cs < ns)
+            lds_barrier();   // the chunk is read by all
+    }
+
+    // acc[m], register r: token arow + 32m, column 32 wid + 8 (r/4) + 4 khalf + r%4 of
+    // the tile.  Through LDS, so that the stores are whole lines of a row's 32
+    // columns; those of partial sums are non-temporal (what is dirty in the L2
+    // when the kernel ends is written back before the next one starts).
+    float u[FM];
+#pragma unroll
+    for (int m = 0; m < FM; m++)
+        u[m] = unit[arow + 32 * m];
+    lds_barrier();   // codes, A and units are read by all
+    int8_t *own = lds + wid * BM * 128;
+    static_assert(8 * BM * 128 <= oSum, "staging rows below the sums");
+#pragma unroll
+    for (int m = 0; m < FM; m++)
+#pragma unroll
+        for (int g = 0; g < 4; g++) {
+            const int row = arow + 32 * m;
+            *reinterpret_cast<v4f *>(own + row * 128 + (((2 * g + khalf) ^ (row & 7)) * 16)) =
+                v4f{acc[m][4 * g], acc[m][4 * g + 1], acc[m][4 * g + 2], acc[m][4 * g + 3]} * u[m];
+        }
+#pragma unroll
+    for (int i = 0; i < BM * 8 / 64; i++) {
+        const int id = i * 64 + lane, t = id >> 3, k = k0 + 32 * wid + 4 * (id & 7);
+        const v4f v = *reinterpret_cast<const v4f *>(own + t * 128 + (((id & 7) ^ (t & 7)) * 16));
+        if (t < a.T && k < K) {
+            if (part)
+                __builtin_nontemporal_store(v, reinterpret_cast<v4f *>(part + ((int64_t)sp * a.T + t) * K + k));
+            else
+                *reinterpret_cast<uint2 *>(dX + (int64_t)t * K + k) =
+                    make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
+        }
+    }
+}
+
+// dX = fp16(fac * sum of the parts, in order); fac null: the parts are in dX's
+// units; no part (N = 0): zeros.
 __global__ __launch_bounds__(256) void k_grad_join(const float *__restrict__ part, const float *__restrict__ fac,
                                                    int splits, int T, int K, uint16_t *__restrict__ dX)
 {
-    const int64_t n = (int64_t)T * K, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int64_t n = (int64_t)T * K, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n)
         return;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < splits; s++) {
-        const float4 lo = *reinterpret_cast<const float4 *>(part + s * n + i);
-        const float4 hi = *reinterpret_cast<const float4 *>(part + s * n + i + 4);
-        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
-        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
-    }
-    if (splits) {
-        const float f = fac[i / K];   // (K is a multiple of 16: one row)
+    v4f v = {0, 0, 0, 0};
+    int s = 0;
+    for (; s + 8 <= splits; s += 8) {   // eight loads in flight
+        v4f x[8];
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            v[e] *= f;
-            asm("" : "+v"(v[e]));
-        }
+        for (int j = 0; j < 8; j++)
+            x[j] = *reinterpret_cast<const v4f *>(part + (s + j) * n + i);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v += x[j];
     }
-    store8<true>(dX + i, 8, v);
+    for (; s < splits; s++)
+        v += *reinterpret_cast<const v4f *>(part + s * n + i);
+    const float f = fac && splits ? fac[i / K] : 1.0f;   // (K is a multiple of 16: one row)
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        v[e] *= f;
+        asm("" : "+v"(v[e]));
+    }
+    *reinterpret_cast<uint2 *>(dX + i) = make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
 }
 
 } // namespace
@@ -617,11 +963,17 @@ __global__ __launch_bounds__(256) void k_grad_join(const float *__restrict__ par
 BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N)
 {
     const int64_t nst = (N + kGN - 1) / kGN;
-    const int bm = T > 128 ? 256 : T > 64 ? 128 : T > 32 ? 64 : 32;
+    if (T <= kFewRows) {
+        const int64_t tiles = (K + kGK - 1) / kGK;
+        const int64_t s = std::min<int64_t>({std::max<int64_t>(1, 256 / std::max<int64_t>(tiles, 1)), nst,
+                                             (int64_t)kMaxGradSplits});
+        return {T <= 32 ? 32 : 64, (int)s, true};
+    }
+    const int bm = T > 128 ? 256 : 128;
     const int64_t tiles = ((T + bm - 1) / bm) * ((K + kGK - 1) / kGK);
     const int64_t s = std::min<int64_t>({std::max<int64_t>(1, 256 / std::max<int64_t>(tiles, 1)),
                                          std::max<int64_t>(1, nst / 4), (int64_t)kMaxGradSplits});
-    return {bm, (int)s};
+    return {bm, (int)s, false};
 }
 
 BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
@@ -631,9 +983,10 @@ BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
     BackwardLayout L;
     L.Np = (int)((N + kGN - 1) / kGN * kGN);
     size_t off = 0;
-    L.A = off;     off = align_up(off + 2 * (size_t)T * (size_t)L.Np, A);
-    L.fac = off;   off = align_up(off + 4 * (size_t)T, A);
-    L.cols = off;  off = align_up(off + 4 * (size_t)kMaxColStrips * (size_t)N, A);
+    const bool rows = !p.few || K == 0;   // (K = 0: no product, and few rows go the general way)
+    L.A = off;     off = align_up(off + (rows ? 2 * (size_t)T * (size_t)L.Np : 0), A);
+    L.fac = off;   off = align_up(off + (rows ? 4 * (size_t)T : 0), A);
+    L.cols = off;  off = align_up(off + (rows ? 4 * (size_t)kMaxColStrips * (size_t)N : 0), A);
     L.part = off;  off = align_up(off + (p.splits > 1 ? 4 * (size_t)p.splits * (size_t)T * (size_t)K : 0), A);
     L.total = off;
     return L;
@@ -684,6 +1037,43 @@ void launch_by_kind(const GradArgs &a, uint16_t *A, float *fac, float *cols, flo
         launch_elementwise<GATED, 2, VEC>(a, A, fac, cols, dbias, s);
 }
 
+template <bool GATED, int KIND, bool VEC, int BM>
+void launch_few_cs(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
+                   float *dbias, hipStream_t s)
+{
+    const int nst = (a.N + kGN - 1) / kGN, stages = nst / p.splits, more = nst % p.splits;
+    const dim3 grid((unsigned)((K + kGK - 1) / kGK), (unsigned)p.splits), block(512);
+    part = p.splits > 1 ? part : nullptr;
+    if (stages + (more > 0) <= 4)
+        hipLaunchKernelGGL((k_grad_few<GATED, KIND, VEC, BM, 4>), grid, block, 0, s, a, Wq, K, stages, more, dX, part, dbias);
+    else
+        hipLaunchKernelGGL((k_grad_few<GATED, KIND, VEC, BM, 3>), grid, block, 0, s, a, Wq, K, stages, more, dX, part, dbias);
+}
+
+template <bool GATED, int KIND, bool VEC>
+void launch_few_bm(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
+                   float *dbias, hipStream_t s)
+{
+    if (p.bm == 32)
+        launch_few_cs<GATED, KIND, VEC, 32>(a, Wq, K, p, dX, part, dbias, s);
+    else
+        launch_few_cs<GATED, KIND, VEC, 64>(a, Wq, K, p, dX, part, dbias, s);
+}
+
+template <bool GATED, bool VEC>
+void launch_few(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
+                float *dbias, hipStream_t s)
+{
+    if (!GATED && !a.pre)
+        launch_few_bm<GATED, GATED ? 0 : kNoAct, VEC>(a, Wq, K, p, dX, part, dbias, s);
+    else if (a.act.kind == 0)
+        launch_few_bm<GATED, 0, VEC>(a, Wq, K, p, dX, part, dbias, s);
+    else if (a.act.kind == 1)
+        launch_few_bm<GATED, 1, VEC>(a, Wq, K, p, dX, part, dbias, s);
+    else
+        launch_few_bm<GATED, 2, VEC>(a, Wq, K, p, dX, part, dbias, s);
+}
+
 template <int BM, int NS, int WM, int WN, int GM>
 void launch_tiles(const uint16_t *A, const int8_t *Wq, const float *fac, int T, int K, int N, int Np, int splits,
                   uint16_t *dX, float *part, hipStream_t s)
@@ -700,7 +1090,7 @@ void launch_tiles(const uint16_t *A, const int8_t *Wq, const float *fac, int T, 
 
 void launch_join(const float *part, const float *fac, int splits, int64_t T, int64_t K, uint16_t *dX, hipStream_t s)
 {
-    const int64_t blocks = (T * K / 8 + 255) / 256;
+    const int64_t blocks = (T * K / 4 + 255) / 256;
     hipLaunchKernelGGL(k_grad_join, dim3((unsigned)blocks), dim3(256), 0, s, part, fac, splits, (int)T, (int)K, dX);
 }
 
@@ -722,6 +1112,18 @@ hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActPar
     float *part = reinterpret_cast<float *>(ws + L.part);
     const GradArgs a{dY, pre, sW, grad_pre, act, (int)T, (int)N, L.Np};
     const bool vec = (gated ? N / 2 : N) % 8 == 0;
+    if (p.few && T > 0 && K > 0) {
+        const int k = (int)K;
+        if (gated)
+            vec ? launch_few<true, true>(a, Wq, k, p, dX, part, dbias, s)
+                : launch_few<true, false>(a, Wq, k, p, dX, part, dbias, s);
+        else
+            vec ? launch_few<false, true>(a, Wq, k, p, dX, part, dbias, s)
+                : launch_few<false, false>(a, Wq, k, p, dX, part, dbias, s);
+        if (p.splits > 1)
+            launch_join(part, nullptr, p.splits, T, K, dX, s);
+        return hipGetLastError();
+    }
     if (gated)
         vec ? launch_by_kind<true, true>(a, A, fac, cols, dbias, s) : launch_by_kind<true, false>(a, A, fac, cols, dbias, s);
     else
@@ -731,12 +1133,8 @@ hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActPar
     const int t = (int)T, k = (int)K, n = (int)N;
     if (p.bm == 256)
         launch_tiles<256, 3, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
-    else if (p.bm == 128)
-        launch_tiles<128, 4, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
-    else if (p.bm == 64)
-        launch_tiles<64, 4, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
     else
-        launch_tiles<32, 4, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+        launch_tiles<128, 4, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
     if (p.splits > 1)
         launch_join(part, fac, p.splits, T, K, dX, s);
     return hipGetLastError();

@@ -448,6 +448,15 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     // The residual's sub-tile comes into the staging rows, where the sums
     // take its place; its loads pass while the outlier product runs.
     auto load_residual = [&]() {
+        if ((N & 7) != 0) {   // rows not 16-byte aligned: element by element
+#pragma unroll 8
+            for (int i = 0; i < NCH * 8 / 64; i++) {
+                const int id = i * 64 + lane, row = id / (CPRW * 8), e = id % (CPRW * 8);
+                *reinterpret_cast<uint16_t *>(own + stage_off<CPRW>(row, e >> 3) + 2 * (e & 7)) =
+                    epi.residual[(int64_t)min(rbase + row, T - 1) * N + min(cbase + e, N - 1)];
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NCH / 64; i++) {
             const int id = i * 64 + lane, row = id / CPRW;
@@ -456,9 +465,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
                            own + i * 1024);
         }
     };
-    const bool res_lds = EPI == EPI_LINEAR && epi.residual && (N & 7) == 0;
     if constexpr (EPI == EPI_LINEAR)
-        if (res_lds && !epi.pre)
+        if (epi.residual && !epi.pre)
             load_residual();
     // token scales from the prefetch
     const int ltok = wm * FM * 32 + (lane & 31);                 // local token row
@@ -620,29 +628,37 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         auto round4 = [](const float (&p)[4]) {
             return make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
         };
-        // staged rows of CP chunks to `out` (row stride `ld`, chunk ch's first
-        // column given by colof, its features ending at `width` of their part)
-        auto store_rows = [&](auto cpr, uint16_t *out, int64_t ld, bool vec, auto colof) {
-            constexpr int CP = decltype(cpr)::value;
-#pragma unroll
-            for (int i = 0; i < FM * 32 * CP / 64; i++) {
-                const int id = i * 64 + lane, row = id / CP, ch = id % CP;
-                const v4i v = *reinterpret_cast<const v4i *>(own + stage_off<CP>(row, ch));
-                int left;   // features of the chunk that exist
-                const int64_t col = colof(ch, left);
-                if (rbase + row >= T)
+        // staged rows of CP chunks to `out` (row stride `ld`; colof gives chunk
+        // ch's first column and how many of its features exist).  Rows of a
+        // multiple of 8 features take 16-byte stores; others as wide ones as
+        // their alignment allows, neighbouring lanes on neighbouring addresses
+        // (777 x 1040 x 2 * 2731 with the kept z: 39.6 -> RAGGED us for the kernel
+        // against eight 2-byte stores of a chunk from one lane).
+        auto store_as = [&](auto cpr, auto gran, uint16_t *out, int64_t ld, auto colof) {
+            constexpr int CP = decltype(cpr)::value, G = decltype(gran)::value, U = CP * 8 / G;
+#pragma unroll 8
+            for (int i = 0; i < FM * 32 * U / 64; i++) {
+                const int id = i * 64 + lane, row = id / U, e = id % U * G;
+                const int8_t *src = own + stage_off<CP>(row, e >> 3) + 2 * (e & 7);
+                int left;
+                uint16_t *dst = out + (int64_t)(rbase + row) * ld + colof(e >> 3, left) + (e & 7);
+                if (rbase + row >= T || (e & 7) >= left)
                     continue;
-                uint16_t *dst = out + (int64_t)(rbase + row) * ld + col;
-                if (vec) {   // (rows and parts are multiples of 8 wide)
-                    if (left > 0)
-                        __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(dst));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        if (e < left)
-                            dst[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
-                }
+                if constexpr (G == 8)
+                    __builtin_nontemporal_store(*reinterpret_cast<const v4i *>(src), reinterpret_cast<v4i *>(dst));
+                else if constexpr (G == 2)
+                    *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(src);
+                else
+                    *dst = *reinterpret_cast<const uint16_t *>(src);
             }
+        };
+        auto store_rows = [&](auto cpr, uint16_t *out, int64_t ld, int width, auto colof) {
+            if ((width & 7) == 0)
+                store_as(cpr, std::integral_constant<int, 8>{}, out, ld, colof);
+            else if ((width & 1) == 0)
+                store_as(cpr, std::integral_constant<int, 2>{}, out, ld, colof);
+            else
+                store_as(cpr, std::integral_constant<int, 1>{}, out, ld, colof);
         };
         if (epi.pre) {
 #pragma unroll
@@ -656,18 +672,18 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
                         *place(CF{}, a, b, g) = round4(p);
                     }
             if constexpr (EPI == EPI_GATED)
-                store_rows(CF{}, epi.pre, N, (F & 7) == 0, [&](int ch, int &left) {
+                store_rows(CF{}, epi.pre, N, F, [&](int ch, int &left) {
                     const int b = wn * FN + (ch >> 2), f = (n0 >> 1) + (b >> 1) * 32 + (ch & 3) * 8;
                     left = F - f;
                     return (b & 1) ? F + f : f;
                 });
             else
-                store_rows(CF{}, epi.pre, N, (N & 7) == 0, [&](int ch, int &left) {
+                store_rows(CF{}, epi.pre, N, N, [&](int ch, int &left) {
                     left = N - (cbase + ch * 8);
                     return cbase + ch * 8;
                 });
             if constexpr (EPI == EPI_LINEAR)
-                if (res_lds) {
+                if (epi.residual) {
                     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the rows are read
                     load_residual();
                 }
@@ -689,7 +705,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
                             *place(CH{}, a, b >> 1, g) = round4(p);
                         }
             } else {
-                if (res_lds)
+                if (epi.residual)
                     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (this wave's own rows)
 #pragma unroll
                 for (int a = 0; a < FM; a++)
@@ -701,17 +717,12 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
 #pragma unroll
                             for (int j = 0; j < 4; j++)
                                 p[j] = act_value<KIND>(d[a][b][4 * g + j], epi.act);
-                            if (res_lds) {
+                            if (epi.residual) {
                                 const uint2 r = *place(CF{}, a, b, g);
                                 p[0] += h2f(r.x & 0xffffu);
                                 p[1] += h2f(r.x >> 16);
                                 p[2] += h2f(r.y & 0xffffu);
                                 p[3] += h2f(r.y >> 16);
-                            } else if (epi.residual) {   // rows not 16-byte aligned: element loads
-                                const int t = min(tok0 + 32 * a, T - 1), n = fea0 + 32 * b + 8 * g;
-#pragma unroll
-                                for (int j = 0; j < 4; j++)
-                                    p[j] += h2f(epi.residual[(int64_t)t * N + min(n + j, N - 1)]);
                             }
                             *place(CF{}, a, b, g) = round4(p);
                         }
@@ -724,13 +735,13 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         else
             finish(std::integral_constant<int, 2>{});
         if constexpr (EPI == EPI_GATED)
-            store_rows(std::integral_constant<int, CPRW / 2>{}, Y, F, (F & 7) == 0, [&](int ch, int &left) {
+            store_rows(std::integral_constant<int, CPRW / 2>{}, Y, F, F, [&](int ch, int &left) {
                 const int f = (n0 >> 1) + (wn * (FN / 2) + (ch >> 2)) * 32 + (ch & 3) * 8;
                 left = F - f;
                 return f;
             });
         else
-            store_rows(CF{}, Y, N, (N & 7) == 0, [&](int ch, int &left) {
+            store_rows(CF{}, Y, N, N, [&](int ch, int &left) {
                 left = N - (cbase + ch * 8);
                 return cbase + ch * 8;
             });

@@ -213,6 +213,7 @@ constexpr int kMaxGradSplits = 32;
 constexpr int kMaxColStrips = 64;
 struct BackwardPlan {
     int bm, splits;
+    bool few;   // the one kernel for few rows
 };
 BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N);
 // Workspace: the product's operand A fp16 [T,Np], its rows' factors fp32 [T],
