@@ -119,6 +119,18 @@ __device__ __forceinline__ void grad8(const GradArgs &a, int64_t t, int f, float
     }
 }
 
+// From a row's largest magnitude (its bits; NaN above all), of biased exponent e:
+// the scale 2^(14 - e) for the product's operand and its inverse for the result.
+// (Below 2^-107 the scale stays at 2^121; an all-zero row and one with
+// infinities or NaN take 1.)
+__device__ __forceinline__ void row_unit(uint32_t m, float &scale, float &inverse)
+{
+    const uint32_t e = m >> 23, ec = max(e, 20u);
+    const bool one = m == 0 || e == 255;
+    scale = one ? 1.0f : __builtin_bit_cast(float, (268u - ec) << 23);
+    inverse = one ? 1.0f : __builtin_bit_cast(float, (ec - 14u) << 23);
+}
+
 constexpr int kRowThreads = 512;   // k_grad_rows: 4096 features a round
 
 // NR > 0: the row's NR rounds stay in registers between the maximum and the
@@ -184,15 +196,10 @@ __global__ __launch_bounds__(kRowThreads) void k_grad_rows(GradArgs a, uint16_t 
 #pragma unroll
         for (int w = 0; w < kRowThreads / 64; w++)
             m = max(m, wmax[w]);
-        // biased exponent e of the maximum: the scale 2^(14 - e), its inverse for the
-        // product.  (Below 2^-107 the scale stays at 2^121; an all-zero row and
-        // one with infinities or NaN take 1.)
-        const uint32_t e8 = m >> 23;
-        const bool one = m == 0 || e8 == 255;
-        const uint32_t ec = max(e8, 20u);
-        const float scale = one ? 1.0f : __builtin_bit_cast(float, (268u - ec) << 23);
+        float scale, inverse;
+        row_unit(m, scale, inverse);
         if (tid == 0)
-            fac[t] = one ? 1.0f : __builtin_bit_cast(float, (ec - 14u) << 23);
+            fac[t] = inverse;
         auto put = [&](int f, float (&z)[P][8]) {
 #pragma unroll
             for (int p = 0; p < P; p++) {
@@ -589,19 +596,19 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
 // ---------------------------------------------------------------------------
 // Few rows (T <= 64): one kernel from dY to partial sums of dX.  A workgroup has
 // 256 columns of dX and a range of weight rows n; it forms its range's dZ for all
-// rows itself (cheap, and the same inputs serve all column tiles from the
-// L2), so nothing has to wait for a kernel that knows whole rows: the power of
-// two of a row is that of its largest value so far, and the sums so far are
-// brought to the new one when it grows, exactly.  The weight's codes are
-// requested before anything else.  Every range's workgroup of the first
-// column tile sees all rows of its dZ: it writes dbias and grad_pre.
-// 8 waves of 32 columns, BM rows.  Half a wave forms a row's chunk of at most 256
-// n, so its maximum is a reduction over 32 lanes.  CS is the stages of 64 n of a
-// chunk: 4 for a range that is no longer than that; else 3 (24 of the 32 lanes),
-// with LDS for the codes of two chunks: while a chunk is multiplied, the next one's
-// inputs come into registers and its codes into the other half of the ring.
+// rows itself (the same inputs serve all column tiles from the L2), so nothing
+// has to wait for a kernel that knows whole rows: a row's power of two is that of
+// its largest value in the range, and the partial sums are stored without it.
+// The weight's codes are requested before anything else.  Every range's
+// workgroup of the first column tile sees all rows of its dZ: it writes dbias and
+// grad_pre.
+// 8 waves of 32 columns, BM rows, at most 256 n: half a wave forms a row, so its
+// maximum is a reduction over 32 lanes.  (Longer ranges in a loop, with the next
+// inputs and codes on their way, were built: FEWLOOP)
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 64;      // most rows
+constexpr int kFewStages = 4;     // most stages of 64 n in a range
+constexpr int kFewN = kFewStages * kGN;
 
 // KIND of a linear gradient without an activation: dZ = dY, Z is not read.
 constexpr int kNoAct = 3;
@@ -700,20 +707,18 @@ __device__ __forceinline__ uint32_t half_wave_max(uint32_t v)
     return max((uint32_t)r16[0], (uint32_t)r16[1]);
 }
 
-template <bool GATED, int KIND, bool VEC, int BM, int CS>
+template <bool GATED, int KIND, bool VEC, int BM>
 __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__restrict__ Wq, int K,
                                                   int stages, int more, uint16_t *__restrict__ dX,
                                                   float *__restrict__ part, float *__restrict__ dbias)
 {
-    constexpr int kFewCS = CS, kFewChunk = CS * kGN, kFewStages = CS == 4 ? 4 : 2 * CS;
     constexpr int NT = 512, FM = BM / 32, PASSES = BM / 16, KS = kGN / 16;
     constexpr int BSZ = kGN * kGK, ASZ = BM * 128;    // a stage of codes, of A
     constexpr int LB = BSZ / 16 / NT;
-    constexpr int oA = kFewStages * BSZ, oSum = oA + kFewCS * ASZ, oRow = oSum + 16 * kFewChunk * 4;
-    __shared__ __attribute__((aligned(1024))) int8_t lds[oRow + 2 * BM * 4];
-    float *sums = reinterpret_cast<float *>(lds + oSum);   // [16 half waves][chunk] column sums
-    float *grow = reinterpret_cast<float *>(lds + oRow);   // [BM] what the sums so far are multiplied by
-    float *unit = grow + BM;                               // [BM] a row's unit at the end
+    constexpr int oA = kFewStages * BSZ, oSum = oA + kFewStages * ASZ, oRow = oSum + 16 * kFewN * 4;
+    __shared__ __attribute__((aligned(1024))) int8_t lds[oRow + BM * 4];
+    float *sums = reinterpret_cast<float *>(lds + oSum);   // [16 half waves][256] column sums
+    float *unit = reinterpret_cast<float *>(lds + oRow);   // [BM] the rows' units
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -731,23 +736,17 @@ __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__re
         voB[i] = row * K + k;
         rowB[i] = k < K ? a.N - row : 0;
     }
-    auto issue = [&](int it) {
-        const int n0 = (st0 + it) * kGN;
-#pragma unroll
-        for (int i = 0; i < LB; i++)
-            load_to_lds_raw(rB, lds0 + (uint32_t)(it % kFewStages) * BSZ + (i * NT + wid * 64) * 16,
-                            n0 < rowB[i] ? voB[i] : kOutOfRange, n0 * K);
-    };
 #pragma unroll
     for (int it = 0; it < kFewStages; it++)
-        if (it < ns)
-            issue(it);
+        if (it < ns) {
+            const int n0 = (st0 + it) * kGN;
+#pragma unroll
+            for (int i = 0; i < LB; i++)
+                load_to_lds_raw(rB, lds0 + (uint32_t)it * BSZ + (i * NT + wid * 64) * 16,
+                                n0 < rowB[i] ? voB[i] : kOutOfRange, n0 * K);
+        }
 
     const int half = tid >> 5, l32 = tid & 31;   // half wave 0..15: rows half, half + 16, ...
-    uint32_t expo[PASSES];                       // biased exponent of the rows' units so far
-#pragma unroll
-    for (int p = 0; p < PASSES; p++)
-        expo[p] = 20;
     v16f acc[FM];
 #pragma unroll
     for (int m = 0; m < FM; m++)
@@ -767,15 +766,13 @@ __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__re
     const typename Raw::Source src = Raw::source(a);
     const __amdgpu_buffer_rsrc_t rS = make_rsrc(a.sW, 4 * a.N);
     float w[8];
-    // inputs of the chunk that starts with stage c0 (lanes past the range, or
-    // past the chunk, take none: those rows are the next workgroup's)
-    auto load = [&](int c0) {
-        const int n = (st0 + c0) * kGN + 8 * l32;
-        const bool in = 8 * l32 < min(kFewCS, ns - c0) * kGN;
+    // this lane's eight weight rows (past the range: the next workgroup's, none)
+    const int n = st0 * kGN + 8 * l32;
+    const bool in = 8 * l32 < ns * kGN;
 #pragma unroll
-        for (int p = 0; p < PASSES; p++)
-            raw[p].load(src, a, in ? half + 16 * p : a.T, n);
-        // (past the last row of the weight: zeros)
+    for (int p = 0; p < PASSES; p++)
+        raw[p].load(src, a, in ? half + 16 * p : a.T, n);
+    {   // (past the last row of the weight: zeros)
         const v4i lo = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rS, in ? 4 * n : kOutOfRange, 0, 0));
         const v4i hi =
             __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rS, in ? 4 * n + 16 : kOutOfRange, 0, 0));
@@ -784,114 +781,76 @@ __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__re
             w[e] = __builtin_bit_cast(float, (int)lo[e]);
             w[4 + e] = __builtin_bit_cast(float, (int)hi[e]);
         }
-    };
-    load(0);
-    for (int c0 = 0; c0 < ns; c0 += kFewCS) {
-        const int cs = min(kFewCS, ns - c0);
-        const int n = (st0 + c0) * kGN + 8 * l32;
-        const bool in = 8 * l32 < cs * kGN;
-        float sum[8];
+    }
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        sum[e] = 0.0f;
+#pragma unroll
+    for (int p = 0; p < PASSES; p++) {
+        const int t = half + 16 * p;
+        uint4 *dst = reinterpret_cast<uint4 *>(lds + oA + (l32 >> 3) * ASZ + t * 128 + (((l32 & 7) ^ swz_a(t)) * 16));
+        if (p > 0 && 16 * p >= a.T) {   // (no such rows)
+            *dst = make_uint4(0, 0, 0, 0);
+            if (l32 == 0)
+                unit[t] = 0.0f;
+            continue;
+        }
+        float z[8];
+        raw[p].grad(a, n, z);   // (zeros for rows and lanes without inputs)
+        if (tile == 0 && a.grad_pre && in && t < a.T)
+            store8<VEC>(a.grad_pre + (int64_t)t * a.N + n, a.N - n, z);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            sum[e] += z[e];
+            z[e] *= w[e];
+            m = max(m, __builtin_bit_cast(uint32_t, z[e]) & 0x7fffffffu);
+        }
+        // scale and unit as in k_grad_rows
+        float scale, inverse;
+        row_unit(half_wave_max(m), scale, inverse);
+        if (l32 == 0)
+            unit[t] = inverse;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            z[e] *= scale;
+            asm("" : "+v"(z[e]));
+        }
+        *dst = make_uint4(pack_f16x2(z[0], z[1]), pack_f16x2(z[2], z[3]), pack_f16x2(z[4], z[5]),
+                          pack_f16x2(z[6], z[7]));
+    }
+    const bool cols = tile == 0 && dbias;
+    if (cols)
 #pragma unroll
         for (int e = 0; e < 8; e++)
-            sum[e] = 0.0f;
+            sums[half * kFewN + 8 * l32 + e] = sum[e];
+    wait_loads_barrier<0>();   // the codes landed; A, units and sums are there
+    if (cols && tid < ns * kGN && st0 * kGN + tid < a.N) {
+        float v = 0.0f;
 #pragma unroll
-        for (int p = 0; p < PASSES; p++) {
-            const int t = half + 16 * p;
-            if (p > 0 && 16 * p >= a.T) {   // (rows that do not exist: zeros, once)
-                if (c0 == 0) {
-                    if (l32 == 0)
-                        grow[t] = unit[t] = 0.0f;
-                    for (int q = l32; q < kFewCS * 8; q += 32)
-                        *reinterpret_cast<uint4 *>(lds + oA + (q >> 3) * ASZ + t * 128 + (q & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                }
-                continue;
-            }
-            float z[8];
-            raw[p].grad(a, n, z);   // (zeros for rows and lanes without inputs)
-            if (tile == 0 && a.grad_pre && in && t < a.T)
-                store8<VEC>(a.grad_pre + (int64_t)t * a.N + n, a.N - n, z);
-            uint32_t m = 0;
+        for (int h = 0; h < 16; h++)
+            v += sums[h * kFewN + tid];
+        dbias[st0 * kGN + tid] = v;
+    }
+    for (int ss = 0; ss < ns; ss++) {
+        const int8_t *b = lds + ss * BSZ + offB;
+        v2i codes[KS];
+        v8h fa[KS][FM];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                sum[e] += z[e];
-                z[e] *= w[e];
-                m = max(m, __builtin_bit_cast(uint32_t, z[e]) & 0x7fffffffu);
-            }
-            m = half_wave_max(m);
-            const uint32_t e8 = m >> 23, old = expo[p];
-            // (a row with infinities or NaN keeps its unit and its infinities)
-            const uint32_t now = e8 == 255 ? old : max(old, e8);
-            expo[p] = now;
-            const float scale = __builtin_bit_cast(float, (268u - now) << 23);
-            if (l32 == 0) {
-                const int d = 127 + (int)old - (int)now;   // 2^(old - now), 0 where that is no fp32 number
-                grow[t] = d > 0 ? __builtin_bit_cast(float, (uint32_t)d << 23) : 0.0f;
-                unit[t] = __builtin_bit_cast(float, (now - 14u) << 23);
-            }
+        for (int kk = 0; kk < KS; kk++) {
+            codes[kk] = read_codes_tr(b + kk * 16 * kGK);
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                z[e] *= scale;
-                asm("" : "+v"(z[e]));
-            }
-            const int ss = l32 >> 3, q = l32 & 7;
-            if (ss < kFewCS)
-                *reinterpret_cast<uint4 *>(lds + oA + ss * ASZ + t * 128 + ((q ^ swz_a(t)) * 16)) =
-                    make_uint4(pack_f16x2(z[0], z[1]), pack_f16x2(z[2], z[3]), pack_f16x2(z[4], z[5]),
-                               pack_f16x2(z[6], z[7]));
+            for (int m = 0; m < FM; m++)
+                fa[kk][m] = *reinterpret_cast<const v8h *>(lds + ss * ASZ + offA[kk] + m * 32 * 128);
         }
-        if (tile == 0 && dbias && in)
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                sums[half * kFewChunk + 8 * l32 + e] = sum[e];
-        wait_loads_barrier<0>();   // the chunk's codes landed; A, grow and the sums are there
-        if (c0 + cs < ns) {
-            // the other half of the ring is free since the last barrier but one
-            if (c0 > 0)
-                for (int it = c0 + cs; it < min(ns, c0 + cs + kFewCS); it++)
-                    issue(it);
-            load(c0 + cs);
+        for (int kk = 0; kk < KS; kk++) {
+            const v8h fb = codes_to_f16(codes[kk]);
+#pragma unroll
+            for (int m = 0; m < FM; m++)
+                acc[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, fa[kk][m], acc[m], 0, 0, 0);
         }
-        if (tile == 0 && dbias && tid < cs * kGN) {
-            const int nn = (st0 + c0) * kGN + tid;
-            if (nn < a.N) {
-                float v = 0.0f;
-#pragma unroll
-                for (int h = 0; h < 16; h++)
-                    v += sums[h * kFewChunk + tid];
-                dbias[nn] = v;
-            }
-        }
-        if (c0 > 0) {
-#pragma unroll
-            for (int m = 0; m < FM; m++) {
-                const float g = grow[arow + 32 * m];
-#pragma unroll
-                for (int r = 0; r < 16; r++)
-                    acc[m][r] *= g;
-            }
-        }
-        for (int ss = 0; ss < cs; ss++) {
-            const int8_t *b = lds + (c0 + ss) % kFewStages * BSZ + offB;
-            v2i codes[KS];
-            v8h fa[KS][FM];
-#pragma unroll
-            for (int kk = 0; kk < KS; kk++) {
-                codes[kk] = read_codes_tr(b + kk * 16 * kGK);
-#pragma unroll
-                for (int m = 0; m < FM; m++)
-                    fa[kk][m] = *reinterpret_cast<const v8h *>(lds + ss * ASZ + offA[kk] + m * 32 * 128);
-            }
-#pragma unroll
-            for (int kk = 0; kk < KS; kk++) {
-                const v8h fb = codes_to_f16(codes[kk]);
-#pragma unroll
-                for (int m = 0; m < FM; m++)
-                    acc[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb, fa[kk][m], acc[m], 0, 0, 0);
-            }
-        }
-        if (c0 + cs < ns)
-            lds_barrier();   // the chunk is read by all
     }
 
     // acc[m], register r: token arow + 32m, column 32 wid + 8 (r/4) + 4 khalf + r%4 of
@@ -959,21 +918,31 @@ __global__ __launch_bounds__(256) void k_grad_join(const float *__restrict__ par
 
 } // namespace
 
-// Tile height and parts of the contraction.  (To be chosen by measurement.)
+// Which kernels, the tile's rows, and into how many ranges the weight's rows are
+// split.
+//  - k_grad_few for T <= 64 where its column tiles times the least number of
+//    ranges of 256 rows are at most one workgroup per CU: past that every CU
+//    forms dZ several times over.  At T, K, N (silu), against k_grad_rows and
+//    k_grad_gemm at their best split: 1, 4096, 4096: 7.6 and 9.8 us; 37, 4096,
+//    4096: 14.4 and 14.8; 64, 4096, 4096: 17.5 and 18.1; 8, 1024, 1024: 6.2 and
+//    8.3; but 8, 11008, 4096: 20.3 and 17.7; 64, 11008, 4096: 40 and 23.
+//    At least 8 ranges: 8, 1024, 1024 takes 7.7 us with 4, 6.2 with 8, 6.6 with
+//    16; 37, 1024, 2048: 9.8, 10.0 and 11.7 with 8, 16 and 32.
+//  - else tiles of 256 rows (128, 64, 32 where T is no larger), and the
+//    weight's rows in as many ranges of 4 stages or more as fill the CUs once
+//    (16, 4096, 22016: 35 us with 16 ranges, 39 with 8 and 32).
 BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N)
 {
-    const int64_t nst = (N + kGN - 1) / kGN;
+    const int64_t nst = std::max<int64_t>(1, (N + kGN - 1) / kGN), tk = std::max<int64_t>(1, (K + kGK - 1) / kGK);
     if (T <= kFewRows) {
-        const int64_t tiles = (K + kGK - 1) / kGK;
-        const int64_t s = std::min<int64_t>({std::max<int64_t>(1, 256 / std::max<int64_t>(tiles, 1)), nst,
-                                             (int64_t)kMaxGradSplits});
-        return {T <= 32 ? 32 : 64, (int)s, true};
+        const int64_t least = (nst + kFewStages - 1) / kFewStages;
+        if (tk * least <= 256 && least <= kMaxGradSplits)
+            return {T <= 32 ? 32 : 64, (int)std::min(std::max<int64_t>(least, 8), nst), true};
     }
-    const int bm = T > 128 ? 256 : 128;
-    const int64_t tiles = ((T + bm - 1) / bm) * ((K + kGK - 1) / kGK);
-    const int64_t s = std::min<int64_t>({std::max<int64_t>(1, 256 / std::max<int64_t>(tiles, 1)),
-                                         std::max<int64_t>(1, nst / 4), (int64_t)kMaxGradSplits});
-    return {bm, (int)s, false};
+    const int bm = T > 128 ? 256 : T > 64 ? 128 : T > 32 ? 64 : 32;
+    const int64_t tiles = (T + bm - 1) / bm * tk;
+    const int64_t s = std::min<int64_t>({256 / tiles, nst / 4, (int64_t)kMaxGradSplits});
+    return {bm, (int)std::max<int64_t>(1, s), false};
 }
 
 BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
@@ -1038,16 +1007,13 @@ void launch_by_kind(const GradArgs &a, uint16_t *A, float *fac, float *cols, flo
 }
 
 template <bool GATED, int KIND, bool VEC, int BM>
-void launch_few_cs(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
+void launch_few_kernel(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
                    float *dbias, hipStream_t s)
 {
     const int nst = (a.N + kGN - 1) / kGN, stages = nst / p.splits, more = nst % p.splits;
     const dim3 grid((unsigned)((K + kGK - 1) / kGK), (unsigned)p.splits), block(512);
     part = p.splits > 1 ? part : nullptr;
-    if (stages + (more > 0) <= 4)
-        hipLaunchKernelGGL((k_grad_few<GATED, KIND, VEC, BM, 4>), grid, block, 0, s, a, Wq, K, stages, more, dX, part, dbias);
-    else
-        hipLaunchKernelGGL((k_grad_few<GATED, KIND, VEC, BM, 3>), grid, block, 0, s, a, Wq, K, stages, more, dX, part, dbias);
+    hipLaunchKernelGGL((k_grad_few<GATED, KIND, VEC, BM>), grid, block, 0, s, a, Wq, K, stages, more, dX, part, dbias);
 }
 
 template <bool GATED, int KIND, bool VEC>
@@ -1055,9 +1021,9 @@ void launch_few_bm(const GradArgs &a, const int8_t *Wq, int K, const BackwardPla
                    float *dbias, hipStream_t s)
 {
     if (p.bm == 32)
-        launch_few_cs<GATED, KIND, VEC, 32>(a, Wq, K, p, dX, part, dbias, s);
+        launch_few_kernel<GATED, KIND, VEC, 32>(a, Wq, K, p, dX, part, dbias, s);
     else
-        launch_few_cs<GATED, KIND, VEC, 64>(a, Wq, K, p, dX, part, dbias, s);
+        launch_few_kernel<GATED, KIND, VEC, 64>(a, Wq, K, p, dX, part, dbias, s);
 }
 
 template <bool GATED, bool VEC>
@@ -1133,8 +1099,12 @@ hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActPar
     const int t = (int)T, k = (int)K, n = (int)N;
     if (p.bm == 256)
         launch_tiles<256, 3, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
-    else
+    else if (p.bm == 128)
         launch_tiles<128, 4, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+    else if (p.bm == 64)
+        launch_tiles<64, 6, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+    else
+        launch_tiles<32, 7, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
     if (p.splits > 1)
         launch_join(part, fac, p.splits, T, K, dX, s);
     return hipGetLastError();
