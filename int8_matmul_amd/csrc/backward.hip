@@ -27,7 +27,9 @@ namespace {
 
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef v4i v4i_any __attribute__((aligned(2)));   // at any fp16 element
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef v4f v4f_any __attribute__((aligned(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
@@ -36,43 +38,75 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 // Elementwise part: eight features f .. f+7 of a row.
 // ---------------------------------------------------------------------------
 
-// Eight fp16 values at p, as fp32; `n` of them exist (VEC: all or none, and p is
-// 16-byte aligned), the others are 0.
-template <bool VEC>
-__device__ __forceinline__ void load8(const uint16_t *p, int n, float (&v)[8])
-{
-    uint32_t w[4] = {0, 0, 0, 0};
-    if constexpr (VEC) {
-        if (n > 0) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p);
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            if (e < n)
-                w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++)
-        v[e] = h2f((w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-}
+// Eight fp16 values in memory order; `n` of them exist, the others are 0.  WHOLE:
+// all or none do, and p is 16-byte aligned (rows of a multiple of 8 features).
+// Otherwise whole groups take 16-byte accesses at the alignment they have (the
+// hardware takes any) and a row's last ones go element by element.
+template <bool WHOLE>
+struct Half8 {
+    v4i w;
 
-template <bool VEC>
+    __device__ __forceinline__ void load(const uint16_t *p, int n)
+    {
+        w = v4i{0, 0, 0, 0};
+        if constexpr (WHOLE) {
+            if (n > 0)
+                w = *reinterpret_cast<const v4i *>(p);
+        } else if (n >= 8) {
+            w = *reinterpret_cast<const v4i_any *>(p);
+        } else if (n > 0) {
+#pragma unroll
+            for (int e = 0; e < 7; e++)
+                if (e < n)
+                    w[e >> 1] |= (int)((uint32_t)p[e] << (16 * (e & 1)));
+        }
+    }
+    __device__ __forceinline__ float value(int e) const
+    {
+        return h2f(((uint32_t)w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+    }
+};
+
+template <bool WHOLE>
 __device__ __forceinline__ void store8(uint16_t *p, int n, const float (&v)[8])
 {
-    const uint32_t w[4] = {pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
-                           pack_f16x2(v[6], v[7])};
-    if constexpr (VEC) {
+    const v4i w = {(int)pack_f16x2(v[0], v[1]), (int)pack_f16x2(v[2], v[3]), (int)pack_f16x2(v[4], v[5]),
+                   (int)pack_f16x2(v[6], v[7])};
+    if constexpr (WHOLE) {
         if (n > 0)
-            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
+            *reinterpret_cast<v4i *>(p) = w;
+    } else if (n >= 8) {
+        *reinterpret_cast<v4i_any *>(p) = w;
+    } else if (n > 0) {
 #pragma unroll
-        for (int e = 0; e < 8; e++)
+        for (int e = 0; e < 7; e++)
             if (e < n)
-                p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                p[e] = (uint16_t)((uint32_t)w[e >> 1] >> (16 * (e & 1)));
     }
 }
+
+template <bool WHOLE>
+__device__ __forceinline__ void load8f(const float *p, int n, float (&v)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        v[e] = 0.0f;
+    if (WHOLE ? n > 0 : n >= 8) {
+        const v4f_any *q = reinterpret_cast<const v4f_any *>(p);
+        const v4f lo = q[0], hi = q[1];
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            v[e] = lo[e], v[4 + e] = hi[e];
+    } else if (!WHOLE && n > 0) {
+#pragma unroll
+        for (int e = 0; e < 7; e++)
+            if (e < n)
+                v[e] = p[e];
+    }
+}
+
+// KIND of a linear gradient without an activation: dZ = dY, Z is not read.
+constexpr int kNoAct = 3;
 
 struct GradArgs {
     const uint16_t *dY;    // [T, F] (F = N, or N / 2 for a pair)
@@ -83,41 +117,42 @@ struct GradArgs {
     int T, N, Np;
 };
 
-// dZ of eight features: z[0] (linear), or z[0] the gate's and z[1] the up
-// projection's (pair).
-template <bool GATED, int KIND, bool VEC>
-__device__ __forceinline__ void grad8(const GradArgs &a, int64_t t, int f, float (&z)[1 + GATED][8])
-{
-    const int F = GATED ? a.N >> 1 : a.N, n = F - f;
-    float d[8], g[8];
-    load8<VEC>(a.dY + t * F + f, n, d);
-    if constexpr (GATED) {
-        float u[8];
-        load8<VEC>(a.pre + t * a.N + f, n, g);
-        load8<VEC>(a.pre + t * a.N + F + f, n, u);
+// Inputs of eight features f .. f+7 of row t.
+template <bool GATED, bool WHOLE>
+struct RawGrad {
+    Half8<WHOLE> d, g, u;
+
+    __device__ __forceinline__ void load(const GradArgs &a, int64_t t, int f)
+    {
+        const int F = GATED ? a.N >> 1 : a.N, n = F - f;
+        d.load(a.dY + t * F + f, n);
+        if (GATED || a.pre)
+            g.load(a.pre + t * a.N + f, n);
+        if constexpr (GATED)
+            u.load(a.pre + t * a.N + F + f, n);
+    }
+
+    // dZ: z[0] (linear), or z[0] the gate's and z[1] the up projection's (pair)
+    template <int KIND>
+    __device__ __forceinline__ void grad(const GradArgs &a, float (&z)[1 + GATED][8]) const
+    {
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            float v, s;
-            act_value_slope<KIND>(g[e], a.act, v, s);
-            z[0][e] = d[e] * u[e] * s;
-            z[1][e] = d[e] * v;
-        }
-    } else {
-        if (a.pre) {
-            load8<VEC>(a.pre + t * a.N + f, n, g);
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
+            if constexpr (KIND == kNoAct) {
+                z[0][e] = d.value(e);
+            } else {
                 float v, s;
-                act_value_slope<KIND>(g[e], a.act, v, s);
-                z[0][e] = d[e] * s;
+                act_value_slope<KIND>(g.value(e), a.act, v, s);
+                if constexpr (GATED) {
+                    z[0][e] = d.value(e) * u.value(e) * s;
+                    z[1][e] = d.value(e) * v;
+                } else {
+                    z[0][e] = d.value(e) * s;
+                }
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                z[0][e] = d[e];
         }
     }
-}
+};
 
 // From a row's largest magnitude (its bits; NaN above all), of biased exponent e:
 // the scale 2^(14 - e) for the product's operand and its inverse for the result.
@@ -133,61 +168,55 @@ __device__ __forceinline__ void row_unit(uint32_t m, float &scale, float &invers
 
 constexpr int kRowThreads = 512;   // k_grad_rows: 4096 features a round
 
-// NR > 0: the row's NR rounds stay in registers between the maximum and the
-// conversion; 0: rows of any length, computed a second time.
-template <bool GATED, int KIND, bool VEC, int NR>
-__global__ __launch_bounds__(kRowThreads) void k_grad_rows(GradArgs a, uint16_t *__restrict__ A,
+// NR > 0: the row's NR rounds, their inputs requested ahead (all of them; of four
+// rounds of a pair one at a time: two workgroups a CU have 128 registers), their
+// results in registers between the maximum and the conversion; 0: rows of any length, computed a second time.  (512 threads
+// against 1024 with half the rounds: F = 11008, 4096 rows, dZ kept: 133 and 164 us.)
+template <bool GATED, int KIND, bool WHOLE, int NR>
+__global__ __launch_bounds__(kRowThreads, 4) void k_grad_rows(GradArgs a, uint16_t *__restrict__ A,
                                                            float *__restrict__ fac)
 {
-    constexpr int P = 1 + GATED;
+    constexpr int P = 1 + GATED, R = NR > 0 ? NR : 1, AHEAD = GATED && NR == 4 ? 1 : R;
     __shared__ uint32_t wmax[kRowThreads / 64];
     const int tid = threadIdx.x;
     const int F = GATED ? a.N >> 1 : a.N;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        float keep[NR > 0 ? NR : 1][P][8];
+        RawGrad<GATED, WHOLE> raw[AHEAD];
+        float keep[R][P][8];
         uint32_t m = 0;   // largest magnitude as bits (NaN above all)
-        auto scaled = [&](int f, float (&z)[P][8]) {
-#pragma unroll
-            for (int p = 0; p < P; p++) {
-                float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if constexpr (VEC) {
-                    if (f < F) {
-                        const float4 lo = *reinterpret_cast<const float4 *>(a.sW + p * F + f);
-                        const float4 hi = *reinterpret_cast<const float4 *>(a.sW + p * F + f + 4);
-                        s[0] = lo.x, s[1] = lo.y, s[2] = lo.z, s[3] = lo.w;
-                        s[4] = hi.x, s[5] = hi.y, s[6] = hi.z, s[7] = hi.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        if (f + e < F)
-                            s[e] = a.sW[p * F + f + e];
-                }
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    z[p][e] *= s[e];
-            }
-        };
-        auto first = [&](int f, float (&z)[P][8]) {
-            grad8<GATED, KIND, VEC>(a, t, f, z);
-            if (a.grad_pre)
+        // dZ of a round, written where it is asked for, times sW
+        auto compute = [&](int r, int f, bool first) {
+            raw[r % AHEAD].template grad<KIND>(a, keep[r]);
+            if (first && a.grad_pre)
 #pragma unroll
                 for (int p = 0; p < P; p++)
-                    store8<VEC>(a.grad_pre + t * a.N + p * F + f, F - f, z[p]);
-            scaled(f, z);
+                    store8<WHOLE>(a.grad_pre + t * a.N + p * F + f, F - f, keep[r][p]);
 #pragma unroll
-            for (int p = 0; p < P; p++)
+            for (int p = 0; p < P; p++) {
+                float s[8];
+                load8f<WHOLE>(a.sW + p * F + f, F - f, s);
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    m = max(m, __builtin_bit_cast(uint32_t, z[p][e]) & 0x7fffffffu);
+                for (int e = 0; e < 8; e++) {
+                    keep[r][p][e] *= s[e];
+                    m = max(m, __builtin_bit_cast(uint32_t, keep[r][p][e]) & 0x7fffffffu);
+                }
+            }
         };
         if constexpr (NR > 0) {
 #pragma unroll
-            for (int r = 0; r < NR; r++)
-                first(8 * (tid + r * kRowThreads), keep[r]);
+            for (int r0 = 0; r0 < NR; r0 += AHEAD) {
+#pragma unroll
+                for (int r = 0; r < AHEAD; r++)
+                    raw[r].load(a, t, 8 * (tid + (r0 + r) * kRowThreads));
+#pragma unroll
+                for (int r = r0; r < r0 + AHEAD; r++)
+                    compute(r, 8 * (tid + r * kRowThreads), true);
+            }
         } else {
-            for (int f = 8 * tid; f < F; f += 8 * kRowThreads)
-                first(f, keep[0]);
+            for (int f = 8 * tid; f < F; f += 8 * kRowThreads) {
+                raw[0].load(a, t, f);
+                compute(0, f, true);
+            }
         }
         m = wave_max(m);
         if ((tid & 63) == 0)
@@ -200,26 +229,24 @@ __global__ __launch_bounds__(kRowThreads) void k_grad_rows(GradArgs a, uint16_t 
         row_unit(m, scale, inverse);
         if (tid == 0)
             fac[t] = inverse;
-        auto put = [&](int f, float (&z)[P][8]) {
+        auto put = [&](int r, int f) {
 #pragma unroll
             for (int p = 0; p < P; p++) {
 #pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    z[p][e] *= scale;
-                    asm("" : "+v"(z[p][e]));   // (no product and conversion in one: equal on both ways here)
-                }
-                store8<VEC>(A + t * a.Np + p * F + f, F - f, z[p]);
+                for (int e = 0; e < 8; e++)
+                    keep[r][p][e] *= scale;   // (a power of two: exact)
+                store8<WHOLE>(A + t * a.Np + p * F + f, F - f, keep[r][p]);
             }
         };
         if constexpr (NR > 0) {
 #pragma unroll
             for (int r = 0; r < NR; r++)
-                put(8 * (tid + r * kRowThreads), keep[r]);
+                put(r, 8 * (tid + r * kRowThreads));
         } else {
             for (int f = 8 * tid; f < F; f += 8 * kRowThreads) {
-                grad8<GATED, KIND, VEC>(a, t, f, keep[0]);
-                scaled(f, keep[0]);
-                put(f, keep[0]);
+                raw[0].load(a, t, f);
+                compute(0, f, false);
+                put(0, f);
             }
         }
         if (tid < a.Np - a.N)   // (less than 64)
@@ -234,7 +261,7 @@ __global__ __launch_bounds__(kRowThreads) void k_grad_rows(GradArgs a, uint16_t 
 // ---------------------------------------------------------------------------
 constexpr int kColThreads = 256;
 
-template <bool GATED, int KIND, bool VEC>
+template <bool GATED, int KIND, bool WHOLE>
 __global__ __launch_bounds__(kColThreads) void k_grad_cols(GradArgs a, float *__restrict__ part)
 {
     constexpr int P = 1 + GATED;
@@ -251,8 +278,10 @@ __global__ __launch_bounds__(kColThreads) void k_grad_cols(GradArgs a, float *__
             s[p][e] = 0.0f;
     if (f < F)
         for (int t = t0 + wid; t < t1; t += kColThreads / 64) {
+            RawGrad<GATED, WHOLE> raw;
             float z[P][8];
-            grad8<GATED, KIND, VEC>(a, t, f, z);
+            raw.load(a, t, f);
+            raw.template grad<KIND>(a, z);
 #pragma unroll
             for (int p = 0; p < P; p++)
 #pragma unroll
@@ -610,13 +639,10 @@ constexpr int kFewRows = 64;      // most rows
 constexpr int kFewStages = 4;     // most stages of 64 n in a range
 constexpr int kFewN = kFewStages * kGN;
 
-// KIND of a linear gradient without an activation: dZ = dY, Z is not read.
-constexpr int kNoAct = 3;
-
 // Inputs of the eight weight rows n .. n+7 (of a pair: of gate or up rows) in
 // row t as they are in memory; 0 past the ends.  Buffer loads at an offset
 // past the end where there is nothing to read: no branches.
-template <bool GATED, int KIND, bool VEC>
+template <bool GATED, int KIND, bool WHOLE>
 struct RawRows {
     static constexpr bool kPre = KIND != kNoAct;
     uint32_t d[4], g[kPre ? 4 : 1], u[GATED ? 4 : 1];
@@ -634,7 +660,7 @@ struct RawRows {
     {
         const int F = GATED ? a.N >> 1 : a.N;
         const bool row = t < a.T;
-        if constexpr (VEC) {   // (F is a multiple of 8: all of one part)
+        if constexpr (WHOLE) {   // (F is a multiple of 8: all of one part)
             const int f = GATED && n >= F ? n - F : n;
             const bool ok = row && n < a.N;
             vec(s.dY, ok ? 2 * (t * F + f) : kOutOfRange, d);
@@ -707,7 +733,7 @@ __device__ __forceinline__ uint32_t half_wave_max(uint32_t v)
     return max((uint32_t)r16[0], (uint32_t)r16[1]);
 }
 
-template <bool GATED, int KIND, bool VEC, int BM>
+template <bool GATED, int KIND, bool WHOLE, int BM>
 __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__restrict__ Wq, int K,
                                                   int stages, int more, uint16_t *__restrict__ dX,
                                                   float *__restrict__ part, float *__restrict__ dbias)
@@ -761,7 +787,7 @@ __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__re
         offB = (8 * khalf + r) * kGK + ((c ^ (2 * r)) * 16) + 8 * (lane & 1);
     }
 
-    using Raw = RawRows<GATED, KIND, VEC>;
+    using Raw = RawRows<GATED, KIND, WHOLE>;
     Raw raw[PASSES];
     const typename Raw::Source src = Raw::source(a);
     const __amdgpu_buffer_rsrc_t rS = make_rsrc(a.sW, 4 * a.N);
@@ -799,7 +825,7 @@ __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__re
         float z[8];
         raw[p].grad(a, n, z);   // (zeros for rows and lanes without inputs)
         if (tile == 0 && a.grad_pre && in && t < a.T)
-            store8<VEC>(a.grad_pre + (int64_t)t * a.N + n, a.N - n, z);
+            store8<WHOLE>(a.grad_pre + (int64_t)t * a.N + n, a.N - n, z);
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
@@ -963,81 +989,78 @@ BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
 
 namespace {
 
-template <bool GATED, int KIND, bool VEC>
+template <bool GATED, int KIND, bool WHOLE>
 void launch_rows(const GradArgs &a, uint16_t *A, float *fac, hipStream_t s)
 {
     const int F = GATED ? a.N / 2 : a.N, rounds = (F + 8 * kRowThreads - 1) / (8 * kRowThreads);
     const dim3 grid((unsigned)std::min(a.T, 1 << 20)), block(kRowThreads);
-    if (rounds <= 1)
-        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 1>), grid, block, 0, s, a, A, fac);
-    else if (rounds <= 2)
-        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 2>), grid, block, 0, s, a, A, fac);
-    else if (rounds <= 4)
-        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 4>), grid, block, 0, s, a, A, fac);
-    else
-        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, VEC, 0>), grid, block, 0, s, a, A, fac);
+    if (rounds <= 1) {
+        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 1>), grid, block, 0, s, a, A, fac);
+        return;
+    }
+    if constexpr (WHOLE) {   // (ragged rows: the tails of several rounds would cost more than the second pass)
+        if (rounds <= 4) {
+            if (rounds == 2)
+                hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 2>), grid, block, 0, s, a, A, fac);
+            else if (rounds == 3)
+                hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 3>), grid, block, 0, s, a, A, fac);
+            else
+                hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 4>), grid, block, 0, s, a, A, fac);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 0>), grid, block, 0, s, a, A, fac);
 }
 
-template <bool GATED, int KIND, bool VEC>
+template <bool GATED, int KIND, bool WHOLE>
 void launch_elementwise(const GradArgs &a, uint16_t *A, float *fac, float *cols, float *dbias, hipStream_t s)
 {
     if (a.T > 0)
-        launch_rows<GATED, KIND, VEC>(a, A, fac, s);
+        launch_rows<GATED, KIND, WHOLE>(a, A, fac, s);
     if (!dbias)
         return;
     int strips = 0;
     if (a.T > 0) {
         const int F = GATED ? a.N / 2 : a.N, blocks = (F + 511) / 512;
         strips = std::max(1, std::min({kMaxColStrips, (a.T + 31) / 32, 2048 / blocks}));
-        hipLaunchKernelGGL((k_grad_cols<GATED, KIND, VEC>), dim3((unsigned)blocks, (unsigned)strips),
-                           dim3(kColThreads), 0, s, a, cols);
+        hipLaunchKernelGGL((k_grad_cols<GATED, KIND, WHOLE>), dim3((unsigned)blocks, (unsigned)strips), dim3(kColThreads), 0, s,
+                           a, cols);
     }
     hipLaunchKernelGGL(k_cols_join, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, cols, strips, a.N, dbias);
 }
 
-template <bool GATED, bool VEC>
-void launch_by_kind(const GradArgs &a, uint16_t *A, float *fac, float *cols, float *dbias, hipStream_t s)
+// f(integral_constant<int, KIND>) for the call's activation.
+template <bool GATED, class F>
+void by_kind(const GradArgs &a, F &&f)
 {
-    if (a.act.kind == 0)
-        launch_elementwise<GATED, 0, VEC>(a, A, fac, cols, dbias, s);
+    if (!GATED && !a.pre)
+        f(std::integral_constant<int, GATED ? 0 : kNoAct>{});
+    else if (a.act.kind == 0)
+        f(std::integral_constant<int, 0>{});
     else if (a.act.kind == 1)
-        launch_elementwise<GATED, 1, VEC>(a, A, fac, cols, dbias, s);
+        f(std::integral_constant<int, 1>{});
     else
-        launch_elementwise<GATED, 2, VEC>(a, A, fac, cols, dbias, s);
+        f(std::integral_constant<int, 2>{});
 }
 
-template <bool GATED, int KIND, bool VEC, int BM>
+template <bool GATED, int KIND, bool WHOLE, int BM>
 void launch_few_kernel(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
                    float *dbias, hipStream_t s)
 {
     const int nst = (a.N + kGN - 1) / kGN, stages = nst / p.splits, more = nst % p.splits;
     const dim3 grid((unsigned)((K + kGK - 1) / kGK), (unsigned)p.splits), block(512);
     part = p.splits > 1 ? part : nullptr;
-    hipLaunchKernelGGL((k_grad_few<GATED, KIND, VEC, BM>), grid, block, 0, s, a, Wq, K, stages, more, dX, part, dbias);
+    hipLaunchKernelGGL((k_grad_few<GATED, KIND, WHOLE, BM>), grid, block, 0, s, a, Wq, K, stages, more, dX, part, dbias);
 }
 
-template <bool GATED, int KIND, bool VEC>
+template <bool GATED, int KIND, bool WHOLE>
 void launch_few_bm(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
                    float *dbias, hipStream_t s)
 {
     if (p.bm == 32)
-        launch_few_kernel<GATED, KIND, VEC, 32>(a, Wq, K, p, dX, part, dbias, s);
+        launch_few_kernel<GATED, KIND, WHOLE, 32>(a, Wq, K, p, dX, part, dbias, s);
     else
-        launch_few_kernel<GATED, KIND, VEC, 64>(a, Wq, K, p, dX, part, dbias, s);
-}
-
-template <bool GATED, bool VEC>
-void launch_few(const GradArgs &a, const int8_t *Wq, int K, const BackwardPlan &p, uint16_t *dX, float *part,
-                float *dbias, hipStream_t s)
-{
-    if (!GATED && !a.pre)
-        launch_few_bm<GATED, GATED ? 0 : kNoAct, VEC>(a, Wq, K, p, dX, part, dbias, s);
-    else if (a.act.kind == 0)
-        launch_few_bm<GATED, 0, VEC>(a, Wq, K, p, dX, part, dbias, s);
-    else if (a.act.kind == 1)
-        launch_few_bm<GATED, 1, VEC>(a, Wq, K, p, dX, part, dbias, s);
-    else
-        launch_few_bm<GATED, 2, VEC>(a, Wq, K, p, dX, part, dbias, s);
+        launch_few_kernel<GATED, KIND, WHOLE, 64>(a, Wq, K, p, dX, part, dbias, s);
 }
 
 template <int BM, int NS, int WM, int WN, int GM>
@@ -1077,23 +1100,32 @@ hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActPar
     float *fac = reinterpret_cast<float *>(ws + L.fac), *cols = reinterpret_cast<float *>(ws + L.cols);
     float *part = reinterpret_cast<float *>(ws + L.part);
     const GradArgs a{dY, pre, sW, grad_pre, act, (int)T, (int)N, L.Np};
-    const bool vec = (gated ? N / 2 : N) % 8 == 0;
+    const auto pair = [&](auto gated_c) {
+        constexpr bool G = decltype(gated_c)::value;
+        by_kind<G>(a, [&](auto kind_c) {
+            constexpr int KIND = decltype(kind_c)::value;
+            const auto go = [&](auto whole_c) {
+                constexpr bool WHOLE = decltype(whole_c)::value;
+                if (p.few && T > 0 && K > 0)
+                    launch_few_bm<G, KIND, WHOLE>(a, Wq, (int)K, p, dX, part, dbias, s);
+                else
+                    launch_elementwise<G, KIND, WHOLE>(a, A, fac, cols, dbias, s);
+            };
+            if ((G ? N / 2 : N) % 8 == 0)
+                go(std::true_type{});
+            else
+                go(std::false_type{});
+        });
+    };
+    if (gated)
+        pair(std::true_type{});
+    else
+        pair(std::false_type{});
     if (p.few && T > 0 && K > 0) {
-        const int k = (int)K;
-        if (gated)
-            vec ? launch_few<true, true>(a, Wq, k, p, dX, part, dbias, s)
-                : launch_few<true, false>(a, Wq, k, p, dX, part, dbias, s);
-        else
-            vec ? launch_few<false, true>(a, Wq, k, p, dX, part, dbias, s)
-                : launch_few<false, false>(a, Wq, k, p, dX, part, dbias, s);
         if (p.splits > 1)
             launch_join(part, nullptr, p.splits, T, K, dX, s);
         return hipGetLastError();
     }
-    if (gated)
-        vec ? launch_by_kind<true, true>(a, A, fac, cols, dbias, s) : launch_by_kind<true, false>(a, A, fac, cols, dbias, s);
-    else
-        vec ? launch_by_kind<false, true>(a, A, fac, cols, dbias, s) : launch_by_kind<false, false>(a, A, fac, cols, dbias, s);
     if (T == 0 || K == 0)
         return hipGetLastError();
     const int t = (int)T, k = (int)K, n = (int)N;

@@ -48,6 +48,7 @@ namespace li8 {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef v4i v4i_any __attribute__((aligned(2)));   // at any fp16 element
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
@@ -448,12 +449,21 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     // The residual's sub-tile comes into the staging rows, where the sums
     // take its place; its loads pass while the outlier product runs.
     auto load_residual = [&]() {
-        if ((N & 7) != 0) {   // rows not 16-byte aligned: element by element
-#pragma unroll 8
-            for (int i = 0; i < NCH * 8 / 64; i++) {
-                const int id = i * 64 + lane, row = id / (CPRW * 8), e = id % (CPRW * 8);
-                *reinterpret_cast<uint16_t *>(own + stage_off<CPRW>(row, e >> 3) + 2 * (e & 7)) =
-                    epi.residual[(int64_t)min(rbase + row, T - 1) * N + min(cbase + e, N - 1)];
+        if ((N & 7) != 0) {   // rows not 16-byte aligned: through registers
+#pragma unroll 4
+            for (int i = 0; i < NCH / 64; i++) {
+                const int id = i * 64 + lane, row = id / CPRW, c = cbase + (id % CPRW) * 8;
+                const uint16_t *src = epi.residual + (int64_t)min(rbase + row, T - 1) * N;
+                v4i v = {0, 0, 0, 0};
+                if (c + 8 <= N) {
+                    v = *reinterpret_cast<const v4i_any *>(src + c);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; e++)
+                        if (c + e < N)
+                            v[e >> 1] |= (int)((uint32_t)src[c + e] << (16 * (e & 1)));
+                }
+                *reinterpret_cast<v4i *>(own + stage_off<CPRW>(row, id % CPRW)) = v;
             }
             return;
         }
@@ -628,37 +638,31 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         auto round4 = [](const float (&p)[4]) {
             return make_uint2(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]));
         };
-        // staged rows of CP chunks to `out` (row stride `ld`; colof gives chunk
-        // ch's first column and how many of its features exist).  Rows of a
-        // multiple of 8 features take 16-byte stores; others as wide ones as
-        // their alignment allows, neighbouring lanes on neighbouring addresses
-        // (777 x 1040 x 2 * 2731 with the kept z: 39.6 -> RAGGED us for the kernel
-        // against eight 2-byte stores of a chunk from one lane).
-        auto store_as = [&](auto cpr, auto gran, uint16_t *out, int64_t ld, auto colof) {
-            constexpr int CP = decltype(cpr)::value, G = decltype(gran)::value, U = CP * 8 / G;
-#pragma unroll 8
-            for (int i = 0; i < FM * 32 * U / 64; i++) {
-                const int id = i * 64 + lane, row = id / U, e = id % U * G;
-                const int8_t *src = own + stage_off<CP>(row, e >> 3) + 2 * (e & 7);
+        // Staged rows of CP chunks to `out` (row stride `ld`; colof gives chunk
+        // ch's first column and how many of its features exist).  16-byte
+        // stores at whatever alignment the row has (the hardware takes any);
+        // element by element only a row's last chunk.  (777 x 1040 x 2 * 2731
+        // with the kept z, 2-byte stores by neighbouring lanes: 28.5 us the
+        // kernel, RAGGED with these.)
+        auto store_rows = [&](auto cpr, uint16_t *out, int64_t ld, auto colof) {
+            constexpr int CP = decltype(cpr)::value;
+#pragma unroll
+            for (int i = 0; i < FM * 32 * CP / 64; i++) {
+                const int id = i * 64 + lane, row = id / CP, ch = id % CP;
+                const v4i v = *reinterpret_cast<const v4i *>(own + stage_off<CP>(row, ch));
                 int left;
-                uint16_t *dst = out + (int64_t)(rbase + row) * ld + colof(e >> 3, left) + (e & 7);
-                if (rbase + row >= T || (e & 7) >= left)
+                uint16_t *dst = out + (int64_t)(rbase + row) * ld + colof(ch, left);
+                if (rbase + row >= T)
                     continue;
-                if constexpr (G == 8)
-                    __builtin_nontemporal_store(*reinterpret_cast<const v4i *>(src), reinterpret_cast<v4i *>(dst));
-                else if constexpr (G == 2)
-                    *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(src);
-                else
-                    *dst = *reinterpret_cast<const uint16_t *>(src);
+                if (left >= 8) {
+                    __builtin_nontemporal_store(v, reinterpret_cast<v4i_any *>(dst));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; e++)
+                        if (e < left)
+                            dst[e] = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+                }
             }
-        };
-        auto store_rows = [&](auto cpr, uint16_t *out, int64_t ld, int width, auto colof) {
-            if ((width & 7) == 0)
-                store_as(cpr, std::integral_constant<int, 8>{}, out, ld, colof);
-            else if ((width & 1) == 0)
-                store_as(cpr, std::integral_constant<int, 2>{}, out, ld, colof);
-            else
-                store_as(cpr, std::integral_constant<int, 1>{}, out, ld, colof);
         };
         if (epi.pre) {
 #pragma unroll
@@ -672,13 +676,13 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
                         *place(CF{}, a, b, g) = round4(p);
                     }
             if constexpr (EPI == EPI_GATED)
-                store_rows(CF{}, epi.pre, N, F, [&](int ch, int &left) {
+                store_rows(CF{}, epi.pre, N, [&](int ch, int &left) {
                     const int b = wn * FN + (ch >> 2), f = (n0 >> 1) + (b >> 1) * 32 + (ch & 3) * 8;
                     left = F - f;
                     return (b & 1) ? F + f : f;
                 });
             else
-                store_rows(CF{}, epi.pre, N, N, [&](int ch, int &left) {
+                store_rows(CF{}, epi.pre, N, [&](int ch, int &left) {
                     left = N - (cbase + ch * 8);
                     return cbase + ch * 8;
                 });
@@ -735,13 +739,13 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         else
             finish(std::integral_constant<int, 2>{});
         if constexpr (EPI == EPI_GATED)
-            store_rows(std::integral_constant<int, CPRW / 2>{}, Y, F, F, [&](int ch, int &left) {
+            store_rows(std::integral_constant<int, CPRW / 2>{}, Y, F, [&](int ch, int &left) {
                 const int f = (n0 >> 1) + (wn * (FN / 2) + (ch >> 2)) * 32 + (ch & 3) * 8;
                 left = F - f;
                 return f;
             });
         else
-            store_rows(CF{}, Y, N, N, [&](int ch, int &left) {
+            store_rows(CF{}, Y, N, [&](int ch, int &left) {
                 left = N - (cbase + ch * 8);
                 return cbase + ch * 8;
             });
