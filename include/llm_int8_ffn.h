@@ -80,7 +80,8 @@ li8_status llm_int8_gated_linear(const void *X, const int8_t *Wq, const float *s
 
 /*
  * Bytes of workspace for the gradients through a weight [N,K] (N = 2F for a
- * gated pair); 0 for an invalid or empty shape.
+ * gated pair); 0 for an invalid or empty shape and where none is needed (NULL
+ * is accepted then).
  */
 size_t llm_int8_backward_workspace_bytes(int64_t T, int64_t K, int64_t N);
 

@@ -929,7 +929,7 @@ def _fitted(t: torch.Tensor, dtype: torch.dtype, name: str, shape: tuple, device
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
             and t.device == device):
         _require(t, dtype, name, len(shape))
-        raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
+        raise ValueError(f"{name} must be {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
