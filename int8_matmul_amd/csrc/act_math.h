@@ -21,28 +21,9 @@
 
 #include <hip/hip_runtime.h>
 
-#include "llm_int8_ffn.h"
+#include "li8_internal.h"
 
 namespace li8 {
-
-struct ActParams {
-    int kind;       // 0: max(z, lo); 1: z s(.); 2: z P(z)
-    float c1, c3;   // kind 1: exp(-x) = 2^(z (c1 + c3 z^2))
-    float lo;       // kind 0
-};
-
-inline ActParams act_params(int act)
-{
-    const double log2e = 1.4426950408889634, k = 1.5957691216057308;   // 2 sqrt(2/pi)
-    const float none = -__builtin_inff();
-    switch (act) {
-    case LI8_ACT_RELU: return {0, 0.0f, 0.0f, 0.0f};
-    case LI8_ACT_SILU: return {1, (float)-log2e, 0.0f, none};
-    case LI8_ACT_GELU: return {2, 0.0f, 0.0f, none};
-    case LI8_ACT_GELU_TANH: return {1, (float)(-log2e * k), (float)(-log2e * k * 0.044715), none};
-    default: return {0, 0.0f, 0.0f, none};
-    }
-}
 
 // s(x) with exp(-x) = 2^(z (c1 + c3 z^2)): 0 and 1 at the ends, never NaN for finite z
 __device__ __forceinline__ float act_sigmoid(float z, const ActParams &p)

@@ -18,6 +18,7 @@
 // dbias: k_grad_cols and k_cols_join, only where asked for.
 #include <algorithm>
 
+#include "act_math.h"
 #include "li8_internal.h"
 #include "quant_math.h"
 #include "tile_common.h"

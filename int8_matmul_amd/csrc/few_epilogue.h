@@ -9,6 +9,7 @@
 // exchange joins them, and the groups are as many as for 2F plain rows.
 #pragma once
 
+#include "act_math.h"
 #include "li8_internal.h"
 #include "quant_math.h"
 

@@ -6,8 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "act_math.h"
-#include "llm_int8.h"
+#include "llm_int8_ffn.h"
 
 namespace li8 {
 
@@ -136,6 +135,27 @@ struct GemmPlan {
 // gated: the N = 2F rows of a gated pair, whose tiles take gate and up rows in
 // pairs of 32-row blocks (not the 192-wide tiles, whose waves hold three blocks).
 GemmPlan gemm_plan(int64_t T, int64_t K, int64_t N, bool gated = false);
+
+// An activation (li8_act) as the kernels take it: one of three forms and its
+// numbers (act_math.h).
+struct ActParams {
+    int kind;       // 0: max(z, lo); 1: z s(.); 2: z P(z)
+    float c1, c3;   // kind 1: exp(-x) = 2^(z (c1 + c3 z^2))
+    float lo;       // kind 0
+};
+
+inline ActParams act_params(int act)
+{
+    const double log2e = 1.4426950408889634, k = 1.5957691216057308;   // 2 sqrt(2/pi)
+    const float none = -__builtin_inff();
+    switch (act) {
+    case LI8_ACT_RELU: return {0, 0.0f, 0.0f, 0.0f};
+    case LI8_ACT_SILU: return {1, (float)-log2e, 0.0f, none};
+    case LI8_ACT_GELU: return {2, 0.0f, 0.0f, none};
+    case LI8_ACT_GELU_TANH: return {1, (float)(-log2e * k), (float)(-log2e * k * 0.044715), none};
+    default: return {0, 0.0f, 0.0f, none};
+    }
+}
 
 // Variants of the kernels' epilogue.  EPI_PLAIN: Y = fp16(D * sW).
 enum { EPI_PLAIN, EPI_LINEAR, EPI_GATED };
