@@ -15,7 +15,8 @@
 // 2. k_grad_gemm: dX = A . Wq on v_mfma_f32_32x32x16_f16 (fp32 sums), codes
 //    converted on the way from LDS to the registers; times 2^(e - 14).
 // 3. k_grad_join where the contraction was split between workgroups.
-// dbias: k_grad_cols and k_cols_join, only where asked for.
+// dbias comes from workgroups of its own in the first launch, and where its rows
+// were split its sums are added in the last one.
 #include <algorithm>
 
 #include "act_math.h"
@@ -39,10 +40,9 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 // Elementwise part: eight features f .. f+7 of a row.
 // ---------------------------------------------------------------------------
 
-// Eight fp16 values in memory order; `n` of them exist, the others are 0.  WHOLE:
-// all or none do, and p is 16-byte aligned (rows of a multiple of 8 features).
-// Otherwise whole groups take 16-byte accesses at the alignment they have (the
-// hardware takes any) and a row's last ones go element by element.
+// Eight fp16 values in memory order; `n` of them exist, the others are 0.  16-byte
+// accesses at whatever alignment p has (the hardware takes any).  WHOLE: all
+// or none exist; otherwise a part goes element by element.
 template <bool WHOLE>
 struct Half8 {
     v4i w;
@@ -52,7 +52,7 @@ struct Half8 {
         w = v4i{0, 0, 0, 0};
         if constexpr (WHOLE) {
             if (n > 0)
-                w = *reinterpret_cast<const v4i *>(p);
+                w = *reinterpret_cast<const v4i_any *>(p);
         } else if (n >= 8) {
             w = *reinterpret_cast<const v4i_any *>(p);
         } else if (n > 0) {
@@ -75,7 +75,7 @@ __device__ __forceinline__ void store8(uint16_t *p, int n, const float (&v)[8])
                    (int)pack_f16x2(v[6], v[7])};
     if constexpr (WHOLE) {
         if (n > 0)
-            *reinterpret_cast<v4i *>(p) = w;
+            *reinterpret_cast<v4i_any *>(p) = w;
     } else if (n >= 8) {
         *reinterpret_cast<v4i_any *>(p) = w;
     } else if (n > 0) {
@@ -123,9 +123,10 @@ template <bool GATED, bool WHOLE>
 struct RawGrad {
     Half8<WHOLE> d, g, u;
 
-    __device__ __forceinline__ void load(const GradArgs &a, int64_t t, int f)
+    // `n` of them: 8 or 0 with WHOLE
+    __device__ __forceinline__ void load(const GradArgs &a, int64_t t, int f, int n)
     {
-        const int F = GATED ? a.N >> 1 : a.N, n = F - f;
+        const int F = GATED ? a.N >> 1 : a.N;
         d.load(a.dY + t * F + f, n);
         if (GATED || a.pre)
             g.load(a.pre + t * a.N + f, n);
@@ -167,35 +168,136 @@ __device__ __forceinline__ void row_unit(uint32_t m, float &scale, float &invers
     inverse = one ? 1.0f : __builtin_bit_cast(float, (ec - 14u) << 23);
 }
 
-constexpr int kRowThreads = 512;   // k_grad_rows: 4096 features a round
+// How a row of F features falls into groups of eight: EVEN, F a multiple of 8;
+// MOVED, F > 8: the last group is moved back to end with the row, so that it
+// is whole and some features are formed twice, alike; SHORT, F < 8: one group.
+enum { EVEN, MOVED, SHORT };
 
-// NR > 0: the row's NR rounds, their inputs requested ahead (all of them; of four
-// rounds of a pair one at a time: two workgroups a CU have 128 registers), their
-// results in registers between the maximum and the conversion; 0: rows of any length, computed a second time.  (512 threads
-// against 1024 with half the rounds: F = 11008, 4096 rows, dZ kept: 133 and 164 us.)
-template <bool GATED, int KIND, bool WHOLE, int NR>
-__global__ __launch_bounds__(kRowThreads, 4) void k_grad_rows(GradArgs a, uint16_t *__restrict__ A,
-                                                           float *__restrict__ fac)
+inline int row_mode(int F) { return F < 8 ? SHORT : F % 8 ? MOVED : EVEN; }
+
+// First feature of group g, and how many of its eight count.
+template <int MODE>
+__device__ __forceinline__ int group_start(int g, int F, int &n)
 {
-    constexpr int P = 1 + GATED, R = NR > 0 ? NR : 1, AHEAD = GATED && NR == 4 ? 1 : R;
+    const bool ok = g < (F + 7) / 8;
+    n = ok ? (MODE == SHORT ? F : 8) : 0;
+    return MODE == MOVED ? min(8 * g, F - 8) : 8 * g;
+}
+
+constexpr int kRowThreads = 512;
+
+// ---------------------------------------------------------------------------
+// dbias: a workgroup has 16 groups of 8 features and a strip of the rows, shared
+// by 32 lanes of threads with four rows in flight each; sums of more than one
+// strip go to partial sums [strips][N], added in order by k_grad_join.
+// ---------------------------------------------------------------------------
+struct ColSums {
+    float *out;     // dbias, or the partial sums; null: none asked for
+    int blocks;     // of 128 features
+    int strips;
+};
+
+template <bool GATED, int KIND, int MODE>
+__device__ void grad_cols(const GradArgs &a, const ColSums &c, int block)
+{
+    constexpr int P = 1 + GATED, LANES = kRowThreads / 16, AHEAD = 4;
+    constexpr bool WHOLE = MODE != SHORT;
+    __shared__ float sum[LANES][P][128];
+    const int gl = threadIdx.x & 15, rl = threadIdx.x >> 4, strip = block / c.blocks;
+    const int F = GATED ? a.N >> 1 : a.N, g0 = (block - strip * c.blocks) * 16;
+    int n;
+    const int f = group_start<MODE>(g0 + gl, F, n);
+    const int t0 = (int)((int64_t)a.T * strip / c.strips), t1 = (int)((int64_t)a.T * (strip + 1) / c.strips);
+    float s[P][8];
+#pragma unroll
+    for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            s[p][e] = 0.0f;
+    for (int t = t0 + rl; t < t1; t += AHEAD * LANES) {
+        RawGrad<GATED, WHOLE> raw[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++)
+            raw[i].load(a, t + i * LANES, f, t + i * LANES < t1 ? n : 0);
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++) {   // (rows past the end: zeros)
+            float z[P][8];
+            raw[i].template grad<KIND>(a, z);
+#pragma unroll
+            for (int p = 0; p < P; p++)
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    s[p][e] += z[p][e];
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            sum[rl][p][8 * gl + e] = s[p][e];
+    __syncthreads();
+    if (threadIdx.x < P * 128) {
+        const int p = threadIdx.x >> 7, i = threadIdx.x & 127;
+        int m;
+        const int col = group_start<MODE>(g0 + (i >> 3), F, m) + (i & 7);
+        if ((i & 7) < m) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < LANES; w++)
+                v += sum[w][p][i];
+            c.out[(int64_t)strip * a.N + p * F + col] = v;
+        }
+    }
+}
+
+// TPR threads a row: 64 (a wave, eight rows a workgroup) or all 512.
+// NR > 0: the row's NR rounds of 8 TPR features, their inputs requested ahead (all
+// of them; of four rounds of a pair one at a time: two workgroups a CU have
+// 128 registers), their results in registers between the maximum and the
+// conversion; 0: rows of any length, computed a second time.  (512 threads against
+// 1024 with half the rounds: F = 11008, 4096 rows, dZ kept: 133 and 164 us.)
+// The launch's first workgroups form the column sums, where asked for: with 75
+// rows a launch of their own costs more than they do.
+template <bool GATED, int KIND, int MODE, int TPR, int NR>
+__global__ __launch_bounds__(kRowThreads, 4) void k_grad_rows(GradArgs a, ColSums c,
+                                                              uint16_t *__restrict__ A, float *__restrict__ fac)
+{
+    constexpr int P = 1 + GATED, R = NR > 0 ? NR : 1, AHEAD = GATED && NR == 4 ? 1 : R, ROWS = kRowThreads / TPR;
+    constexpr bool WHOLE = MODE != SHORT;
+    static_assert(TPR == 64 || TPR == kRowThreads, "a wave or the workgroup");
     __shared__ uint32_t wmax[kRowThreads / 64];
-    const int tid = threadIdx.x;
-    const int F = GATED ? a.N >> 1 : a.N;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int cols = c.out ? c.blocks * c.strips : 0;
+    if ((int)blockIdx.x < cols) {
+        grad_cols<GATED, KIND, MODE>(a, c, blockIdx.x);
+        return;
+    }
+    const int first = blockIdx.x - cols, stride = (gridDim.x - cols) * ROWS;
+    const int tid = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int row = TPR == 64 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0;   // (uniform: scalar addresses)
+    const int F = GATED ? a.N >> 1 : a.N, groups = (F + 7) / 8;
+    // (a wave's row is the same for all its lanes, a workgroup's for all its waves)
+    for (int64_t t = (int64_t)first * ROWS + row; t < a.T; t += stride) {
         RawGrad<GATED, WHOLE> raw[AHEAD];
         float keep[R][P][8];
         uint32_t m = 0;   // largest magnitude as bits (NaN above all)
+        auto request = [&](int r, int g) {
+            int n;
+            const int f = group_start<MODE>(g, F, n);
+            raw[r].load(a, t, f, n);
+        };
         // dZ of a round, written where it is asked for, times sW
-        auto compute = [&](int r, int f, bool first) {
+        auto compute = [&](int r, int g, bool first) {
+            int n;
+            const int f = group_start<MODE>(g, F, n);
             raw[r % AHEAD].template grad<KIND>(a, keep[r]);
             if (first && a.grad_pre)
 #pragma unroll
                 for (int p = 0; p < P; p++)
-                    store8<WHOLE>(a.grad_pre + t * a.N + p * F + f, F - f, keep[r][p]);
+                    store8<WHOLE>(a.grad_pre + t * a.N + p * F + f, n, keep[r][p]);
 #pragma unroll
             for (int p = 0; p < P; p++) {
                 float s[8];
-                load8f<WHOLE>(a.sW + p * F + f, F - f, s);
+                load8f<WHOLE>(a.sW + p * F + f, n, s);
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
                     keep[r][p][e] *= s[e];
@@ -208,115 +310,57 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_grad_rows(GradArgs a, uint16
             for (int r0 = 0; r0 < NR; r0 += AHEAD) {
 #pragma unroll
                 for (int r = 0; r < AHEAD; r++)
-                    raw[r].load(a, t, 8 * (tid + (r0 + r) * kRowThreads));
+                    request(r, tid + (r0 + r) * TPR);
 #pragma unroll
                 for (int r = r0; r < r0 + AHEAD; r++)
-                    compute(r, 8 * (tid + r * kRowThreads), true);
+                    compute(r, tid + r * TPR, true);
             }
         } else {
-            for (int f = 8 * tid; f < F; f += 8 * kRowThreads) {
-                raw[0].load(a, t, f);
-                compute(0, f, true);
+            for (int g = tid; g < groups; g += TPR) {
+                request(0, g);
+                compute(0, g, true);
             }
         }
         m = wave_max(m);
-        if ((tid & 63) == 0)
-            wmax[tid >> 6] = m;
-        __syncthreads();
+        if constexpr (TPR > 64) {
+            if ((tid & 63) == 0)
+                wmax[tid >> 6] = m;
+            __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kRowThreads / 64; w++)
-            m = max(m, wmax[w]);
+            for (int w = 0; w < kRowThreads / 64; w++)
+                m = max(m, wmax[w]);
+        }
         float scale, inverse;
         row_unit(m, scale, inverse);
         if (tid == 0)
             fac[t] = inverse;
-        auto put = [&](int r, int f) {
+        auto put = [&](int r, int g) {
+            int n;
+            const int f = group_start<MODE>(g, F, n);
 #pragma unroll
             for (int p = 0; p < P; p++) {
 #pragma unroll
                 for (int e = 0; e < 8; e++)
                     keep[r][p][e] *= scale;   // (a power of two: exact)
-                store8<WHOLE>(A + t * a.Np + p * F + f, F - f, keep[r][p]);
+                store8<WHOLE>(A + t * a.Np + p * F + f, n, keep[r][p]);
             }
         };
         if constexpr (NR > 0) {
 #pragma unroll
             for (int r = 0; r < NR; r++)
-                put(r, 8 * (tid + r * kRowThreads));
+                put(r, tid + r * TPR);
         } else {
-            for (int f = 8 * tid; f < F; f += 8 * kRowThreads) {
-                raw[0].load(a, t, f);
-                compute(0, f, false);
-                put(0, f);
+            for (int g = tid; g < groups; g += TPR) {
+                request(0, g);
+                compute(0, g, false);
+                put(0, g);
             }
         }
         if (tid < a.Np - a.N)   // (less than 64)
             A[t * a.Np + a.N + tid] = 0;
-        __syncthreads();   // (wmax is read)
+        if constexpr (TPR > 64)
+            __syncthreads();   // (wmax is read)
     }
-}
-
-// ---------------------------------------------------------------------------
-// dbias: 64 lanes x 8 features a workgroup, its 4 waves and the strips of the
-// grid share the rows; partial sums [strips][N] added in order by k_cols_join.
-// ---------------------------------------------------------------------------
-constexpr int kColThreads = 256;
-
-template <bool GATED, int KIND, bool WHOLE>
-__global__ __launch_bounds__(kColThreads) void k_grad_cols(GradArgs a, float *__restrict__ part)
-{
-    constexpr int P = 1 + GATED;
-    __shared__ float sum[kColThreads / 64][P][512];
-    const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-    const int F = GATED ? a.N >> 1 : a.N, f = (int)blockIdx.x * 512 + 8 * lane;
-    const int strips = gridDim.y;
-    const int t0 = (int)((int64_t)a.T * blockIdx.y / strips), t1 = (int)((int64_t)a.T * (blockIdx.y + 1) / strips);
-    float s[P][8];
-#pragma unroll
-    for (int p = 0; p < P; p++)
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            s[p][e] = 0.0f;
-    if (f < F)
-        for (int t = t0 + wid; t < t1; t += kColThreads / 64) {
-            RawGrad<GATED, WHOLE> raw;
-            float z[P][8];
-            raw.load(a, t, f);
-            raw.template grad<KIND>(a, z);
-#pragma unroll
-            for (int p = 0; p < P; p++)
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    s[p][e] += z[p][e];
-        }
-#pragma unroll
-    for (int p = 0; p < P; p++)
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            sum[wid][p][8 * lane + e] = s[p][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < P * 512; i += kColThreads) {
-        const int p = i >> 9, c = i & 511, n = (int)blockIdx.x * 512 + c;
-        if (n < F) {
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kColThreads / 64; w++)
-                v += sum[w][p][c];
-            part[(int64_t)blockIdx.y * a.N + p * F + n] = v;
-        }
-    }
-}
-
-__global__ __launch_bounds__(256) void k_cols_join(const float *__restrict__ part, int strips, int N,
-                                                   float *__restrict__ dbias)
-{
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= N)
-        return;
-    float v = 0.0f;
-    for (int s = 0; s < strips; s++)
-        v += part[(int64_t)s * N + n];
-    dbias[n] = v;
 }
 
 // ---------------------------------------------------------------------------
@@ -914,33 +958,57 @@ __global__ __launch_bounds__(512) void k_grad_few(GradArgs a, const int8_t *__re
 }
 
 // dX = fp16(fac * sum of the parts, in order); fac null: the parts are in dX's
-// units; no part (N = 0): zeros.
-__global__ __launch_bounds__(256) void k_grad_join(const float *__restrict__ part, const float *__restrict__ fac,
-                                                   int splits, int T, int K, uint16_t *__restrict__ dX)
+// units; no part (N = 0): zeros.  The workgroups from `blocks` on add dbias'
+// strips (none: zeros).
+struct Joins {
+    const float *part, *fac;
+    uint16_t *dX;
+    int64_t n;      // elements of dX
+    int splits, K;
+    int blocks;
+    const float *cols;
+    float *dbias;
+    int strips, N;
+};
+
+template <class V>
+__device__ __forceinline__ V sum_parts(const float *p, int64_t stride, int parts)
 {
-    const int64_t n = (int64_t)T * K, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n)
-        return;
-    v4f v = {0, 0, 0, 0};
+    V v = {};
     int s = 0;
-    for (; s + 8 <= splits; s += 8) {   // eight loads in flight
-        v4f x[8];
+    for (; s + 8 <= parts; s += 8) {   // eight loads in flight
+        V x[8];
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            x[j] = *reinterpret_cast<const v4f *>(part + (s + j) * n + i);
+            x[j] = *reinterpret_cast<const V *>(p + (s + j) * stride);
 #pragma unroll
         for (int j = 0; j < 8; j++)
             v += x[j];
     }
-    for (; s < splits; s++)
-        v += *reinterpret_cast<const v4f *>(part + s * n + i);
-    const float f = fac && splits ? fac[i / K] : 1.0f;   // (K is a multiple of 16: one row)
+    for (; s < parts; s++)
+        v += *reinterpret_cast<const V *>(p + s * stride);
+    return v;
+}
+
+__global__ __launch_bounds__(256) void k_grad_join(Joins j)
+{
+    if ((int)blockIdx.x >= j.blocks) {
+        const int n = (int)(blockIdx.x - j.blocks) * 256 + threadIdx.x;
+        if (n < j.N)
+            j.dbias[n] = sum_parts<float>(j.cols + n, j.N, j.strips);
+        return;
+    }
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= j.n)
+        return;
+    v4f v = sum_parts<v4f>(j.part + i, j.n, j.splits);
+    const float f = j.fac && j.splits ? j.fac[i / j.K] : 1.0f;   // (K is a multiple of 16: one row)
 #pragma unroll
     for (int e = 0; e < 4; e++) {
         v[e] *= f;
         asm("" : "+v"(v[e]));
     }
-    *reinterpret_cast<uint2 *>(dX + i) = make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
+    *reinterpret_cast<uint2 *>(j.dX + i) = make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
 }
 
 } // namespace
@@ -958,17 +1026,19 @@ __global__ __launch_bounds__(256) void k_grad_join(const float *__restrict__ par
 //  - else tiles of 256 rows (128, 64, 32 where T is no larger), and the
 //    weight's rows in as many ranges of 4 stages or more as fill the CUs once
 //    (16, 4096, 22016: 35 us with 16 ranges, 39 with 8 and 32).
+//  - ranges beyond 32 only while their partial sums are at most 16 MB.
 BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N)
 {
     const int64_t nst = std::max<int64_t>(1, (N + kGN - 1) / kGN), tk = std::max<int64_t>(1, (K + kGK - 1) / kGK);
+    const int64_t most = std::max<int64_t>(kGradSplits, ((int64_t)4 << 20) / std::max<int64_t>(T * K, 1));
     if (T <= kFewRows) {
         const int64_t least = (nst + kFewStages - 1) / kFewStages;
-        if (tk * least <= 256 && least <= kMaxGradSplits)
+        if (tk * least <= 256 && least <= most)
             return {T <= 32 ? 32 : 64, (int)std::min(std::max<int64_t>(least, 8), nst), true};
     }
     const int bm = T > 128 ? 256 : T > 64 ? 128 : T > 32 ? 64 : 32;
     const int64_t tiles = (T + bm - 1) / bm * tk;
-    const int64_t s = std::min<int64_t>({256 / tiles, nst / 4, (int64_t)kMaxGradSplits});
+    const int64_t s = std::min<int64_t>({256 / tiles, nst / 4, most});
     return {bm, (int)std::max<int64_t>(1, s), false};
 }
 
@@ -990,44 +1060,49 @@ BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
 
 namespace {
 
-template <bool GATED, int KIND, bool WHOLE>
-void launch_rows(const GradArgs &a, uint16_t *A, float *fac, hipStream_t s)
+template <bool GATED, int KIND, int MODE, int TPR, int NR>
+void launch_rows_as(const GradArgs &a, const ColSums &c, uint16_t *A, float *fac, hipStream_t s)
 {
-    const int F = GATED ? a.N / 2 : a.N, rounds = (F + 8 * kRowThreads - 1) / (8 * kRowThreads);
-    const dim3 grid((unsigned)std::min(a.T, 1 << 20)), block(kRowThreads);
-    if (rounds <= 1) {
-        hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 1>), grid, block, 0, s, a, A, fac);
-        return;
-    }
-    if constexpr (WHOLE) {   // (ragged rows: the tails of several rounds would cost more than the second pass)
-        if (rounds <= 4) {
-            if (rounds == 2)
-                hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 2>), grid, block, 0, s, a, A, fac);
-            else if (rounds == 3)
-                hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 3>), grid, block, 0, s, a, A, fac);
-            else
-                hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 4>), grid, block, 0, s, a, A, fac);
-            return;
-        }
-    }
-    hipLaunchKernelGGL((k_grad_rows<GATED, KIND, WHOLE, 0>), grid, block, 0, s, a, A, fac);
+    const int per = kRowThreads / TPR, rows = std::min((a.T + per - 1) / per, 1 << 20);
+    hipLaunchKernelGGL((k_grad_rows<GATED, KIND, MODE, TPR, NR>), dim3((unsigned)(rows + (c.out ? c.blocks * c.strips : 0))),
+                       dim3(kRowThreads), 0, s, a, c, A, fac);
 }
 
-template <bool GATED, int KIND, bool WHOLE>
-void launch_elementwise(const GradArgs &a, uint16_t *A, float *fac, float *cols, float *dbias, hipStream_t s)
+// A wave for short rows (a workgroup left most of its threads without work),
+// else a workgroup.  Uneven rows take more registers for their addresses, so
+// only up to two rounds of them stay in registers.
+template <bool GATED, int KIND>
+void launch_rows(const GradArgs &a, const ColSums &c, uint16_t *A, float *fac, hipStream_t s)
 {
-    if (a.T > 0)
-        launch_rows<GATED, KIND, WHOLE>(a, A, fac, s);
-    if (!dbias)
-        return;
-    int strips = 0;
-    if (a.T > 0) {
-        const int F = GATED ? a.N / 2 : a.N, blocks = (F + 511) / 512;
-        strips = std::max(1, std::min({kMaxColStrips, (a.T + 31) / 32, 2048 / blocks}));
-        hipLaunchKernelGGL((k_grad_cols<GATED, KIND, WHOLE>), dim3((unsigned)blocks, (unsigned)strips), dim3(kColThreads), 0, s,
-                           a, cols);
+    const int F = GATED ? a.N / 2 : a.N, g = (F + 7) / 8, mode = row_mode(F);
+    if (mode == SHORT) {
+        launch_rows_as<GATED, KIND, SHORT, 64, 1>(a, c, A, fac, s);
+    } else if (mode == MOVED) {
+        if (g <= 64)
+            launch_rows_as<GATED, KIND, MOVED, 64, 1>(a, c, A, fac, s);
+        else if (g <= 2 * 64)
+            launch_rows_as<GATED, KIND, MOVED, 64, 2>(a, c, A, fac, s);
+        else if (g <= kRowThreads)
+            launch_rows_as<GATED, KIND, MOVED, kRowThreads, 1>(a, c, A, fac, s);
+        else if (g <= 2 * kRowThreads)
+            launch_rows_as<GATED, KIND, MOVED, kRowThreads, 2>(a, c, A, fac, s);
+        else
+            launch_rows_as<GATED, KIND, MOVED, kRowThreads, 0>(a, c, A, fac, s);
+    } else if (g <= 64) {
+        launch_rows_as<GATED, KIND, EVEN, 64, 1>(a, c, A, fac, s);
+    } else if (g <= 2 * 64) {
+        launch_rows_as<GATED, KIND, EVEN, 64, 2>(a, c, A, fac, s);
+    } else if (g <= kRowThreads) {
+        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 1>(a, c, A, fac, s);
+    } else if (g <= 2 * kRowThreads) {
+        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 2>(a, c, A, fac, s);
+    } else if (g <= 3 * kRowThreads) {
+        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 3>(a, c, A, fac, s);
+    } else if (g <= 4 * kRowThreads) {
+        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 4>(a, c, A, fac, s);
+    } else {
+        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 0>(a, c, A, fac, s);
     }
-    hipLaunchKernelGGL(k_cols_join, dim3((unsigned)((a.N + 255) / 256)), dim3(256), 0, s, cols, strips, a.N, dbias);
 }
 
 // f(integral_constant<int, KIND>) for the call's activation.
@@ -1078,10 +1153,12 @@ void launch_tiles(const uint16_t *A, const int8_t *Wq, const float *fac, int T, 
                            splits, dX, part);
 }
 
-void launch_join(const float *part, const float *fac, int splits, int64_t T, int64_t K, uint16_t *dX, hipStream_t s)
+void launch_join(Joins j, hipStream_t s)
 {
-    const int64_t blocks = (T * K / 4 + 255) / 256;
-    hipLaunchKernelGGL(k_grad_join, dim3((unsigned)blocks), dim3(256), 0, s, part, fac, splits, (int)T, (int)K, dX);
+    j.blocks = j.dX ? (int)((j.n / 4 + 255) / 256) : 0;
+    const int more = j.dbias ? (j.N + 255) / 256 : 0;
+    if (j.blocks + more > 0)
+        hipLaunchKernelGGL(k_grad_join, dim3((unsigned)(j.blocks + more)), dim3(256), 0, s, j);
 }
 
 } // namespace
@@ -1090,56 +1167,69 @@ hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActPar
                            const float *sW, int64_t T, int64_t K, int64_t N, uint16_t *dX, uint16_t *grad_pre,
                            float *dbias, char *ws, hipStream_t s)
 {
-    if (T > 0 && N == 0) {
-        if (K > 0)
-            launch_join(nullptr, nullptr, 0, T, K, dX, s);
+    Joins join{};
+    join.n = T * K;
+    join.K = (int)K;
+    join.N = (int)N;
+    if (T == 0 || N == 0) {   // sums of nothing
+        join.dX = dX;
+        join.dbias = dbias;
+        launch_join(join, s);
         return hipGetLastError();
     }
     const BackwardLayout L = backward_layout(T, K, N);
     const BackwardPlan p = backward_plan(T, K, N);
     uint16_t *A = reinterpret_cast<uint16_t *>(ws + L.A);
-    float *fac = reinterpret_cast<float *>(ws + L.fac), *cols = reinterpret_cast<float *>(ws + L.cols);
-    float *part = reinterpret_cast<float *>(ws + L.part);
+    float *fac = reinterpret_cast<float *>(ws + L.fac), *part = reinterpret_cast<float *>(ws + L.part);
     const GradArgs a{dY, pre, sW, grad_pre, act, (int)T, (int)N, L.Np};
+    const bool few = p.few && K > 0;
+    const int features = (int)(gated ? N / 2 : N);
+    ColSums c{};
+    if (dbias && !few) {
+        // 512 rows a strip, while that leaves enough workgroups for the chip
+        c.blocks = (features + 127) / 128;
+        c.strips = std::max(1, std::min({kMaxColStrips, (int)((T + 255) / 512), 2048 / c.blocks}));
+        c.out = c.strips > 1 ? reinterpret_cast<float *>(ws + L.cols) : dbias;
+        if (c.strips > 1) {
+            join.cols = c.out;
+            join.strips = c.strips;
+            join.dbias = dbias;
+        }
+    }
     const auto pair = [&](auto gated_c) {
         constexpr bool G = decltype(gated_c)::value;
         by_kind<G>(a, [&](auto kind_c) {
             constexpr int KIND = decltype(kind_c)::value;
-            const auto go = [&](auto whole_c) {
-                constexpr bool WHOLE = decltype(whole_c)::value;
-                if (p.few && T > 0 && K > 0)
-                    launch_few_bm<G, KIND, WHOLE>(a, Wq, (int)K, p, dX, part, dbias, s);
-                else
-                    launch_elementwise<G, KIND, WHOLE>(a, A, fac, cols, dbias, s);
-            };
-            if ((G ? N / 2 : N) % 8 == 0)
-                go(std::true_type{});
+            if (!few)
+                launch_rows<G, KIND>(a, c, A, fac, s);
+            else if (features % 8 == 0)
+                launch_few_bm<G, KIND, true>(a, Wq, (int)K, p, dX, part, dbias, s);
             else
-                go(std::false_type{});
+                launch_few_bm<G, KIND, false>(a, Wq, (int)K, p, dX, part, dbias, s);
         });
     };
     if (gated)
         pair(std::true_type{});
     else
         pair(std::false_type{});
-    if (p.few && T > 0 && K > 0) {
-        if (p.splits > 1)
-            launch_join(part, nullptr, p.splits, T, K, dX, s);
-        return hipGetLastError();
+    if (!few && K > 0) {
+        const int t = (int)T, k = (int)K, n = (int)N;
+        if (p.bm == 256)
+            launch_tiles<256, 3, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+        else if (p.bm == 128)
+            launch_tiles<128, 4, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+        else if (p.bm == 64)
+            launch_tiles<64, 6, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
+        else
+            launch_tiles<32, 7, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
     }
-    if (T == 0 || K == 0)
-        return hipGetLastError();
-    const int t = (int)T, k = (int)K, n = (int)N;
-    if (p.bm == 256)
-        launch_tiles<256, 3, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
-    else if (p.bm == 128)
-        launch_tiles<128, 4, 2, 4, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
-    else if (p.bm == 64)
-        launch_tiles<64, 6, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
-    else
-        launch_tiles<32, 7, 1, 8, 4>(A, Wq, fac, t, k, n, L.Np, p.splits, dX, part, s);
-    if (p.splits > 1)
-        launch_join(part, fac, p.splits, T, K, dX, s);
+    if (p.splits > 1 && K > 0) {
+        join.part = part;
+        join.fac = few ? nullptr : fac;
+        join.splits = p.splits;
+        join.dX = dX;
+    }
+    launch_join(join, s);
     return hipGetLastError();
 }
 

@@ -229,7 +229,7 @@ hipError_t launch_split_gemm(const int8_t *Wq, const float *sW, const uint16_t *
 // the product.  Most features: the operand's rows are reached with 32-bit
 // offsets from a tile's first row.
 constexpr int64_t kMaxGradN = (int64_t)1 << 21;
-constexpr int kMaxGradSplits = 32;
+constexpr int kGradSplits = 32;
 constexpr int kMaxColStrips = 64;
 struct BackwardPlan {
     int bm, splits;
