@@ -625,22 +625,35 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
     // acc[a][b], register r: token ltok + 32a, column 32b + 8 (r/4) + 4 khalf + r%4
     // of the wave's columns
     const int col0 = k0 + wn * FK * 32;
-    if constexpr (SPLIT) {   // fp32, in the rows' units
+    wait_loads_barrier<0>();   // the ring is free
+    if constexpr (SPLIT) {
+        // fp32, in the rows' units: 32 columns at a time through LDS, so that the
+        // stores are whole lines; non-temporal, so that the L2 holds nothing to
+        // write back when the kernel ends
         float *out = part + (int64_t)sp * T * K;
+        int8_t *own = lds + wid * (FM * 32) * 128;
+        static_assert(NW * FM * 32 * 128 <= LDSB, "staging rows");
 #pragma unroll
-        for (int a = 0; a < FM; a++)
+        for (int b = 0; b < FK; b++) {
 #pragma unroll
-            for (int b = 0; b < FK; b++)
+            for (int a = 0; a < FM; a++)
 #pragma unroll
                 for (int g = 0; g < 4; g++) {
-                    const int t = m0 + ltok + 32 * a, k = col0 + 32 * b + 8 * g + 4 * khalf;
-                    if (t < T && k < K)
-                        *reinterpret_cast<v4f *>(out + (int64_t)t * K + k) =
-                            v4f{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
+                    const int row = a * 32 + (lane & 31);
+                    *reinterpret_cast<v4f *>(own + row * 128 + (((2 * g + khalf) ^ (row & 7)) * 16)) =
+                        v4f{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2], acc[a][b][4 * g + 3]};
                 }
+#pragma unroll
+            for (int i = 0; i < FM * 32 * 8 / 64; i++) {
+                const int id = i * 64 + lane, row = id >> 3, t = m0 + wm * FM * 32 + row;
+                const int k = col0 + 32 * b + 4 * (id & 7);
+                const v4f v = *reinterpret_cast<const v4f *>(own + row * 128 + (((id & 7) ^ (row & 7)) * 16));
+                if (t < T && k < K)
+                    __builtin_nontemporal_store(v, reinterpret_cast<v4f *>(out + (int64_t)t * K + k));
+            }
+        }
         return;
     }
-    wait_loads_barrier<0>();   // the ring is free
     int8_t *own = lds + wid * (FM * 32) * CPR * 16;
 #pragma unroll
     for (int a = 0; a < FM; a++)
