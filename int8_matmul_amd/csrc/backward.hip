@@ -1036,9 +1036,14 @@ __global__ __launch_bounds__(256) void k_grad_join(Joins j)
 //    8.3; but 8, 11008, 4096: 20.3 and 17.7; 64, 11008, 4096: 40 and 23.
 //    At least 8 ranges: 8, 1024, 1024 takes 7.7 us with 4, 6.2 with 8, 6.6 with
 //    16; 37, 1024, 2048: 9.8, 10.0 and 11.7 with 8, 16 and 32.
-//  - else tiles of 256 rows (128, 64, 32 where T is no larger), and the
-//    weight's rows in as many ranges of 4 stages or more as fill the CUs once
-//    (16, 4096, 22016: 35 us with 16 ranges, 39 with 8 and 32).
+//  - else the tile's rows and the ranges of least modelled time: rounds of
+//    workgroups over the 256 CUs, each 4 us and its stages at 1.55, 1.05, 0.65
+//    or 0.5 us (tiles of 256, 128, 64, 32 rows: fewer rows use a stage's codes
+//    less), and the join of the ranges' sums at 5 TB/s.  At T, K, N, tile / ranges
+//    of the model's choice against others: 256, 4096, 4096: 64/4 25.7 us, 128/6
+//    26.9, 256/16 39; 1024, 4096, 4096: 64/1 46.9, 128/2 53.4, 256/4 61; 2048,
+//    4096, 4096: 128/1 78, 64/1 87, 256/1 90; 3000, 4096, 4096: 256/1 107, 128/1 and
+//    64/1 131; 512, 5120, 27648: 256/6 154, 128/3 179.
 //  - ranges beyond 32 only while their partial sums are at most 16 MB.
 BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N)
 {
@@ -1049,10 +1054,30 @@ BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N)
         if (tk * least <= 256 && least <= most)
             return {T <= 32 ? 32 : 64, (int)std::min(std::max<int64_t>(least, 8), nst), true};
     }
-    const int bm = T > 128 ? 256 : T > 64 ? 128 : T > 32 ? 64 : 32;
-    const int64_t tiles = (T + bm - 1) / bm * tk;
-    const int64_t s = std::min<int64_t>({256 / tiles, nst / 4, most});
-    return {bm, (int)std::max<int64_t>(1, s), false};
+    static const struct {
+        int bm;
+        double stage;
+    } kTiles[] = {{256, 1.55}, {128, 1.05}, {64, 0.65}, {32, 0.5}};
+    BackwardPlan best{256, 1, false};
+    double least = 1e300;
+    for (const auto &c : kTiles) {
+        // (rows that a tile of half the size holds would leave it half empty; 32 only for few rows)
+        if ((c.bm > 64 && T <= c.bm / 2) || (c.bm == 64 && T <= 32) || (c.bm == 32 && T > 32))
+            continue;
+        const int64_t tiles = (T + c.bm - 1) / c.bm * tk;
+        for (int64_t s = 1; s <= std::min<int64_t>({std::max<int64_t>(1, nst / 2), most, 64}); s++) {
+            if (s > 1 && tiles * s > 256 + tiles)   // (past one round, more ranges only add sums)
+                break;
+            const double join = s > 1 ? 3.0 + (double)(s * T * K) * 8.0 / 5.0e6 : 0.0;
+            const double cost =
+                (double)((tiles * s + 255) / 256) * (4.0 + c.stage * (double)((nst + s - 1) / s)) + join;
+            if (cost < least) {
+                least = cost;
+                best = BackwardPlan{c.bm, (int)s, false};
+            }
+        }
+    }
+    return best;
 }
 
 BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
