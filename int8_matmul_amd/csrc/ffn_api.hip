@@ -51,7 +51,7 @@ li8_status forward(const void *X, const int8_t *Wq, const float *sW, float thres
         return from_hip(launch_split_fused(x, Wq, sW, nullptr, thr, T, K, N, y, ws, stream, &epi));
     const WsLayout L = ws_layout(T, K, N);
     const hipError_t e = launch_prepare(x, Wq, nullptr, thr, T, K, N, ws, L, stream, nullptr,
-                                        GatherSkip{kFoldMin, gemm_plan(T, K, N, gated).fold});
+                                        GatherSkip{kFoldMin, epi_plan(T, K, N, gated).fold});
     if (e != hipSuccess)
         return LI8_ERR_HIP;
     return from_hip(launch_gemm_epi(Wq, sW, T, K, N, y, ws, L, epi, stream));

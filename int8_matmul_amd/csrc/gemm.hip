@@ -906,10 +906,33 @@ hipError_t launch_gemm(const int8_t *Wq, const float *sW, int64_t T, int64_t K, 
                  : launch_cfg<256, 256, 128, 2, 2, 4, 4, false>(Wq, sW, T, K, N, Y, acc, ws, L, s, WO);
 }
 
+// The epilogue variants have one tile more, 64x128 (8 waves of 32x32, or 4 of
+// 32x64 for a pair, four stages ahead), for calls whose larger tiles are
+// fewer than the CUs: its stages take a third of a 256x256 tile's.  Whole calls,
+// against the tile that gemm_plan gives: 64 x 4096 x 4096 34.8 -> 20.9 us, 256 x 4096 x
+// 4096 39.0 -> 23.1, 512 x 4096 x 4096 41.3 -> 25.4, 3553 x 5264 x 259 75 -> 45, gated
+// 64 x 4096 x 2 * 11008 38.1 -> 26.7; with two rounds of them 1024 x 4096 x 4096 43.2 ->
+// 40.4 and gated 512 x 1024 x 2 * 4096 19.4 -> 20.3; with three gated 256 x 4096 x 2 * 11008
+// 41.8 -> 52.1.
+GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated)
+{
+    const GemmPlan p = gemm_plan(T, K, N, gated);
+    const auto rounds = [&](int64_t bm, int64_t bn) {
+        return (double)(((T + bm - 1) / bm * ((N + bn - 1) / bn) + kCUs - 1) / kCUs);
+    };
+    const double cost = rounds(p.bm, p.bn) * (p.bn == 256 ? 1.0 : p.bn == 192 ? 0.75 * 1.15 : 0.5 * 1.35);
+    if (0.33 * rounds(64, 128) < cost)
+        return {64, 128, K <= kFoldMaxK ? 256 : 0};
+    return p;
+}
+
 hipError_t launch_gemm_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
                            uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s)
 {
-    const GemmPlan p = gemm_plan(T, K, N, epi.gated);
+    const GemmPlan p = epi_plan(T, K, N, epi.gated);
+    if (p.bm == 64)
+        return epi.gated ? launch_epi_cfg<64, 128, 128, 4, 2, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s)
+                         : launch_epi_cfg<64, 128, 128, 4, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
     if (epi.gated)
         return p.bn == 128
                    ? launch_epi_cfg<256, 128, 128, 2, 4, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s)

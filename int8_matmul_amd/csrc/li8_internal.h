@@ -135,6 +135,8 @@ struct GemmPlan {
 // gated: the N = 2F rows of a gated pair, whose tiles take gate and up rows in
 // pairs of 32-row blocks (not the 192-wide tiles, whose waves hold three blocks).
 GemmPlan gemm_plan(int64_t T, int64_t K, int64_t N, bool gated = false);
+// The same for the epilogue variants, which have a tile for few rows too.
+GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated);
 
 // An activation (li8_act) as the kernels take it: one of three forms and its
 // numbers (act_math.h).

@@ -107,7 +107,9 @@ TILED = [
     (257, 512, 1002, {}), (129, 4096, 258, {}), (513, 256, 2730, {}), (33, 8208, 100, {}),
     (100, 528, 384, dict(fixed=400)),                      # every second column an outlier, gathered by the prepare kernel
 ]
-WIDE = [(2048, 64, 11008, 192), (2500, 64, 5000, 256)]     # the other two tile widths
+# the larger tiles, which few rows do not take (with outlier columns copied from the stages, too)
+WIDE = [(2048, 64, 11008, 192, {}), (2500, 64, 5000, 256, {}), (1100, 272, 6000, 128, dict(sparse=2e-3)),
+        (1100, 272, 5998, 128, {}), (1100, 528, 6010, 128, dict(fixed=400))]
 
 
 @pytest.mark.parametrize("T, K, N, kw", FEW + SPLIT + TILED)
@@ -134,14 +136,14 @@ def test_gated(T, K, N, kw, i):
     f.gated(activation=act, save=False)
 
 
-@pytest.mark.parametrize("T, K, N, tile", WIDE)
-def test_wide_tiles(T, K, N, tile):
+@pytest.mark.parametrize("T, K, N, tile, kw", WIDE)
+def test_wide_tiles(T, K, N, tile, kw):
     print(f"case wide {T}x{K}x{N}", flush=True)
     assert li8.plan(T, K, N)["tile_n"] == tile
-    f = Forward(T, K, N, seed=3, residual=True)
+    f = Forward(T, K, N, seed=3, residual=True, **kw)
     f.epilogue(activation="gelu", save=False)
     f.epilogue(activation="none", save=True)
-    f.gated(activation="silu", save=tile == 256)
+    f.gated(activation="silu", save=tile != 192)
 
 
 @pytest.mark.parametrize("act", ffn.ACTS)
@@ -167,7 +169,7 @@ def test_thresholds(T, K, N, threshold):
     f.gated(threshold, "gelu_tanh")
 
 
-@pytest.mark.parametrize("T, K, N", [(1, 64, 40), (8, 8208, 33), (70, 64, 40), (300, 128, 131), (2048, 64, 11008)])
+@pytest.mark.parametrize("T, K, N", [(1, 64, 40), (8, 8208, 33), (70, 64, 40), (300, 128, 131), (2048, 64, 11008), (1100, 64, 6001)])
 @pytest.mark.parametrize("save", [False, True])
 def test_residual_in_place(T, K, N, save):
     print(f"case in place {T}x{K}x{N} {save}", flush=True)
@@ -176,7 +178,7 @@ def test_residual_in_place(T, K, N, save):
 
 
 @pytest.mark.parametrize("T, K, N", [(1, 4096, 520), (8, 512, 4200), (12, 512, 4200), (16, 8192, 64), (7, 11008, 72), (300, 1040, 520),
-                                     (2048, 64, 11008), (2500, 64, 5000)])
+                                     (2048, 64, 11008), (2500, 64, 5000), (1100, 272, 6000)])
 def test_without_extras_it_is_the_linear_layer(T, K, N):
     """Bit for bit: the product stays fp32 up to the same single rounding."""
     print(f"case plain {T}x{K}x{N}", flush=True)
