@@ -373,6 +373,10 @@ __global__ __launch_bounds__(kRowThreads, 4) void k_grad_rows(GradArgs a, ColSum
 // Chunks of 16 codes are permuted in a row by twice the row's index so that
 // the 8 rows of a read and its two neighbouring chunks meet all 64 banks once.
 // Stages, waits and the tile order are those of k_gemm (gemm.hip).
+// Measured: 4096 x 4096 x 22016 in 590-610 us (1.23 PFLOP/s; a library's fp16 product of
+// two 16-bit operands takes 621), 4096 x 11008 x 4096 in 310-320 (library: 431).  The
+// matrix units are busy for 73 % of the cycles and the clock is at 1.6 GHz, the
+// board's power limit.
 // ---------------------------------------------------------------------------
 constexpr int kGN = 64;    // weight rows per stage
 constexpr int kGK = 256;   // columns of dX per tile
@@ -550,7 +554,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
     // One MFMA with up to two LDS reads after it until they are all issued, then
     // with the conversions' share
     constexpr int NMF = FM * FK, NRD = FM + FK, RPM = (NRD + NMF / 2) / (NMF / 2 ? NMF / 2 : 1);
-    auto interleave = [&](int nld) {
+    auto interleave = [&]() {
         int rd = 0;
 #pragma unroll
         for (int i = 0; i < NMF; i++) {
@@ -561,8 +565,6 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
             } else {
                 __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
             }
-            if (i < nld)
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -578,7 +580,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
                 lread(cur ^ 1, st, kk + 1);
                 mfmas(cur);
                 convert(cur ^ 1);
-                interleave(0);
+                interleave();
             } else if constexpr (!LAST) {
                 wait_loads_barrier<WAIT>();   // stage it+1 landed; stage it read by all
                 if constexpr (ISSUE)
@@ -587,7 +589,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
                 lread(cur ^ 1, st, 0);
                 mfmas(cur);
                 convert(cur ^ 1);
-                interleave(ISSUE ? LA + LB : 0);
+                interleave();
             } else {
                 mfmas(cur);
             }
@@ -691,7 +693,10 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
 // grad_pre.
 // 8 waves of 32 columns, BM rows, at most 256 n: half a wave forms a row, so its
 // maximum is a reduction over 32 lanes.  (Longer ranges in a loop, with the next
-// inputs and codes on their way, were built: FEWLOOP)
+// inputs and codes on their way, took 30 us at 16, 4096, 22016 and 57 at 64, 4096,
+// 22016, where k_grad_rows and k_grad_gemm take 27 and 31.)  37 x 4096 x 4096 with
+// gelu and bias: 14.2 us a call with its join, 7.6 us for one row; what is left is the
+// chain of loads, dZ (formed 16 times, 3 us of gelu's slopes) and 10 MB of sums.
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 64;      // most rows
 constexpr int kFewStages = 4;     // most stages of 64 n in a range
@@ -1106,8 +1111,9 @@ void launch_rows_as(const GradArgs &a, const ColSums &c, uint16_t *A, float *fac
                        dim3(kRowThreads), 0, s, a, c, A, fac);
 }
 
-// A wave for short rows (a workgroup left most of its threads without work),
-// else a workgroup.  Uneven rows take more registers for their addresses, so
+// A wave for short rows (a workgroup left most of its threads without work:
+// 3621 x 176 x 2 * 135 took 31.8 us a call, 13.3 with waves and the product's
+// smaller tile), else a workgroup.  Uneven rows take more registers for their addresses, so
 // only up to two rounds of them stay in registers.
 template <bool GATED, int KIND>
 void launch_rows(const GradArgs &a, const ColSums &c, uint16_t *A, float *fac, hipStream_t s)

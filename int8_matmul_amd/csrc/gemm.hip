@@ -36,6 +36,13 @@
 //  - Epilogue: per 32x32 block, dequantize, add the outlier MFMA, scale,
 //    convert to fp16 into LDS; then each wave writes its sub-tile with
 //    16-byte stores.
+//  - The epilogue variants (EPI_LINEAR, EPI_GATED) keep fl32(D * sW) in fp32
+//    through bias, activation, and residual or gate product, so each output is
+//    rounded once and Z is not written unless asked for.  A call of 4096 x 11008 x
+//    4096 takes 201 us plain and 203 with this epilogue; bias adds 0, silu 3, gelu
+//    8, residual 2, the kept Z 3.  The gated pair of 4096 x 4096 x 2 * 11008 takes 394 us (its
+//    kernel; 1.87 POP/s, bound like the plain product by the clock that the board's
+//    power allows).
 #include <type_traits>
 #include <utility>
 
@@ -642,8 +649,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         // ch's first column and how many of its features exist).  16-byte
         // stores at whatever alignment the row has (the hardware takes any);
         // element by element only a row's last chunk.  (777 x 1040 x 2 * 2731
-        // with the kept z, 2-byte stores by neighbouring lanes: 28.5 us the
-        // kernel, RAGGED with these.)
+        // with the kept z: the kernel takes 24.3 us, 28.5 with 2-byte stores by
+        // neighbouring lanes, 39.6 with eight 2-byte stores a lane.)
         auto store_rows = [&](auto cpr, uint16_t *out, int64_t ld, auto colof) {
             constexpr int CP = decltype(cpr)::value;
 #pragma unroll
