@@ -23,6 +23,9 @@
  * (LI8_ERR_SHAPE): forward calls of ceil(T/256) * ceil(N/128) >= 2^23, backward
  * calls of N > 2^21.  T, N or F of 0 is an
  * empty call (dX is then zero where it has elements, and so is dbias).
+ * Outputs and the workspace must not overlap inputs or one another, except for
+ * a residual that is Y itself.  llm_int8_plan is about llm_int8_linear; the
+ * calls here take its few-token paths for the same shapes.
  * Inputs must be finite, except that a row of gradients that holds an
  * infinity or NaN gives a dX row of infinities and NaN (what a loss scaler
  * looks for).  Results past fp16's range become infinities.
