@@ -21,7 +21,7 @@
  * allocated, synchronized or read back, no mutable state in the library.
  * T, K, N as there; a gated pair has N = 2F rows.  Refused besides
  * (LI8_ERR_SHAPE): forward calls of ceil(T/256) * ceil(N/128) >= 2^23, backward
- * calls of N > 2^21.  T, N or F of 0 is an
+ * calls of N > 2^21 or T > 2^30.  T, N or F of 0 is an
  * empty call (dX is then zero where it has elements, and so is dbias).
  * Outputs and the workspace must not overlap inputs or one another, except for
  * a residual that is Y itself.  llm_int8_plan is about llm_int8_linear; the

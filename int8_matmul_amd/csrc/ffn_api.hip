@@ -60,7 +60,7 @@ li8_status forward(const void *X, const int8_t *Wq, const float *sW, float thres
 li8_status backward_shape(int64_t T, int64_t K, int64_t N)
 {
     const li8_status st = check_shape(T, K, N);
-    return st == LI8_OK && N > kMaxGradN ? LI8_ERR_SHAPE : st;
+    return st == LI8_OK && (N > kMaxGradN || T > kMaxGradT) ? LI8_ERR_SHAPE : st;
 }
 
 li8_status backward(const void *dY, const void *pre, int32_t act, const int8_t *Wq, const float *sW, int64_t T,

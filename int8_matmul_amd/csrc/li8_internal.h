@@ -231,6 +231,9 @@ hipError_t launch_split_gemm(const int8_t *Wq, const float *sW, const uint16_t *
 // the product.  Most features: the operand's rows are reached with 32-bit
 // offsets from a tile's first row.
 constexpr int64_t kMaxGradN = (int64_t)1 << 21;
+// Most rows: the column sums step past a strip's last row with an int (K >= 16 keeps
+// T at 2^27; this is for K = 0).
+constexpr int64_t kMaxGradT = (int64_t)1 << 30;
 constexpr int kGradSplits = 32;
 constexpr int kMaxColStrips = 64;
 struct BackwardPlan {

@@ -140,3 +140,12 @@ def test_the_binding_refuses_on_the_host():
     for f in (lambda: li8.linear_epilogue(None, w, s), lambda: li8.gated_backward([1], y, w, s)):
         with pytest.raises(TypeError):
             f()
+
+
+def test_backward_refuses_more_rows_than_the_column_sums_count(lib):
+    """K = 0 allows rows past 2^30, where stepping past the last row would leave 32 bits."""
+    for name in BACK_CALLS:
+        for T in ((1 << 30) + 1, (1 << 31) - 1):
+            assert call(lib, name, BACK, T=T, K=0, N=1) == SHAPE
+            assert lib.llm_int8_backward_workspace_bytes(T, 0, 2) == 0
+    assert lib.llm_int8_backward_workspace_bytes(1 << 30, 0, 2) > 0
