@@ -26,9 +26,11 @@
  * Outputs and the workspace must not overlap inputs or one another, except for
  * a residual that is Y itself.  llm_int8_plan is about llm_int8_linear; the
  * calls here take its few-token paths for the same shapes.
- * Inputs must be finite, except that a row of gradients that holds an
- * infinity or NaN gives a dX row of infinities and NaN (what a loss scaler
- * looks for).  Results past fp16's range become infinities.
+ * X and the weight must be finite.  A NaN of a bias or residual reaches the
+ * outputs that it enters.  A row of gradients that holds an infinity or NaN
+ * gives a dX row of infinities and NaN (what a loss scaler looks for).
+ * Results past fp16's range become infinities; a row whose pre holds such
+ * ones may give infinities and NaN.
  */
 #ifndef LLM_INT8_FFN_H
 #define LLM_INT8_FFN_H

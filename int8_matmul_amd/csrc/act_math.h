@@ -52,7 +52,7 @@ template <int KIND>
 __device__ __forceinline__ float act_value(float z, const ActParams &p)
 {
     if constexpr (KIND == 0) {
-        return fmaxf(z, p.lo);
+        return z <= p.lo ? p.lo : z;   // (a NaN stays; no lower bound: lo is one)
     } else if constexpr (KIND == 1) {
         return z * act_sigmoid(z, p);
     } else {
@@ -69,8 +69,9 @@ template <int KIND>
 __device__ __forceinline__ void act_value_slope(float z, const ActParams &p, float &value, float &slope)
 {
     if constexpr (KIND == 0) {
-        value = fmaxf(z, p.lo);
-        slope = z > p.lo ? 1.0f : 0.0f;
+        const bool low = z <= p.lo;
+        value = low ? p.lo : z;
+        slope = low ? 0.0f : 1.0f;
     } else if constexpr (KIND == 1) {
         const float ln2 = 0.6931471805599453f;
         const float s = act_sigmoid(z, p), r = s * (1.0f - s);

@@ -27,7 +27,8 @@ li8_status forward(const void *X, const int8_t *Wq, const float *sW, float thres
         return LI8_ERR_INVALID_ARG;
     if (T == 0 || N == 0)
         return LI8_OK;
-    // tiles of 256 x 128 at least, 512 threads each: below 2^32 work-items
+    // 512 threads a tile of 256 x 128 at least (of 64 x 128 only where that is not
+    // more tiles, or few): below 2^32 work-items
     if (((T + 255) / 256) * ((N + 127) / 128) >= (int64_t)1 << 23)
         return LI8_ERR_SHAPE;
     if ((K > 0 && (!X || !Wq)) || !sW || !Y)

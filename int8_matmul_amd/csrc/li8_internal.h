@@ -141,15 +141,15 @@ GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated);
 // An activation (li8_act) as the kernels take it: one of three forms and its
 // numbers (act_math.h).
 struct ActParams {
-    int kind;       // 0: max(z, lo); 1: z s(.); 2: z P(z)
+    int kind;       // 0: z <= lo ? lo : z; 1: z s(.); 2: z P(z)
     float c1, c3;   // kind 1: exp(-x) = 2^(z (c1 + c3 z^2))
-    float lo;       // kind 0
+    float lo;       // kind 0; NaN: no bound
 };
 
 inline ActParams act_params(int act)
 {
     const double log2e = 1.4426950408889634, k = 1.5957691216057308;   // 2 sqrt(2/pi)
-    const float none = -__builtin_inff();
+    const float none = __builtin_nanf("");
     switch (act) {
     case LI8_ACT_RELU: return {0, 0.0f, 0.0f, 0.0f};
     case LI8_ACT_SILU: return {1, (float)-log2e, 0.0f, none};

@@ -544,3 +544,88 @@ def test_the_binding_refuses():
         li8.linear_epilogue(big, w, s, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(li8.Int8MatmulError, match="SHAPE"):
         li8.linear_epilogue(big[:, :24].contiguous(), w[:, :24].contiguous(), s)
+
+
+@pytest.mark.parametrize("act", ffn.ACTS)
+@pytest.mark.parametrize("T, K, N", [(5, 256, 66), (6, 8224, 34), (50, 256, 66)])
+def test_nans_reach_the_outputs_that_they_enter(act, T, K, N):
+    print(f"case nan {act} {T}x{K}x{N}", flush=True)
+    f, F = Forward(T, K, N, seed=11, residual=True), N // 2
+    x, w, s, b, r = (f.d[k] for k in ("X", "Wq", "sW", "bias", "residual"))
+    clean_y = host(li8.linear_epilogue(x, w, s, bias=b, activation=act, residual=r))
+    clean_h = host(li8.gated_linear(x, w, s, bias=b, activation=act))
+    nb, nr = b.clone(), r.clone()
+    nb[3] = nb[F + 7] = nr[1, 9] = float("nan")
+    y = host(li8.linear_epilogue(x, w, s, bias=nb, activation=act, residual=nr))
+    h = host(li8.gated_linear(x, w, s, bias=nb, activation=act))
+    ny, nh = np.zeros_like(y, bool), np.zeros_like(h, bool)
+    ny[:, [3, F + 7]] = ny[1, 9] = nh[:, [3, 7]] = True
+    assert np.array_equal(np.isnan(y), ny) and np.array_equal(np.isnan(h), nh)
+    assert np.array_equal(y[~ny], clean_y[~ny]) and np.array_equal(h[~nh], clean_h[~nh])
+
+
+def test_a_linear_gate_passes_an_overflowed_pre():
+    """act none: the slope is 1 at an infinity of the stored pre too, and the gradients are infinities where they are products with it."""
+    for T in (9, 70):
+        b = Backward(T, 64, 80, True, seed=12)
+        b.pre[2, 5] = -np.inf                               # the gate's value of feature 5
+        g = host(b.run("none")["grad_pre"])
+        want = ffn.grad_pre(b.dY, b.pre, "none", True)[0]
+        assert g[2, 5] == np.float16(want[2, 5]) and np.isinf(g[2, 45]) and np.isfinite(np.delete(g[2], 45)).all()
+
+
+BIG = (66000, 16, 33000)   # more than 2^31 elements of [T, N]
+
+
+def _big(shape, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.empty(shape, dtype=F16, device=DEV).normal_(generator=g)
+
+
+def _rows(t, rows):
+    return host(t[rows])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_forward_past_32_bit_offsets(gated):
+    T, K, N = BIG
+    print(f"case big forward {gated}", flush=True)
+    rng = np.random.default_rng(21)
+    Wq, sW = rng.integers(-127, 128, (N, K)).astype(np.int8), (rng.random(N) * 1e-3 + 1e-4).astype(np.float32)
+    x, bias, rows = _big((T, K), 1), (rng.standard_normal(N)).astype(np.float16), [0, 1, 32541, T - 2, T - 1]
+    pre = torch.empty((T, N), dtype=F16, device=DEV)
+    kw = dict(threshold=float("inf"), bias=dev(bias), activation="silu", pre=pre)
+    if gated:
+        out = li8.gated_linear(x, dev(Wq), dev(sW), **kw)
+        want = ffn.gated_linear(_rows(x, rows), Wq, sW, float("inf"), bias, "silu")
+    else:
+        out = _big((T, N), 2)
+        res = _rows(out, rows)
+        li8.linear_epilogue(x, dev(Wq), dev(sW), residual=out, out=out, **kw)
+        want = ffn.linear_epilogue(_rows(x, rows), Wq, sW, float("inf"), bias, "silu", res)
+    for t, w, k in ((out, want[0], "out"), (pre, want[1], "pre")):
+        assert ffn.check(_rows(t, rows), w, k) is None, ffn.check(_rows(t, rows), w, k)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_backward_past_32_bit_offsets(gated):
+    T, K, N = BIG
+    print(f"case big backward {gated}", flush=True)
+    rng = np.random.default_rng(22)
+    F, rows = N // 2 if gated else N, [0, 1, 32541, T - 2, T - 1]
+    Wq, sW = rng.integers(-127, 128, (N, K)).astype(np.int8), (rng.random(N) * 1e-3 + 1e-4).astype(np.float32)
+    dY, pre = _big((T, F), 3), _big((T, N), 4)
+    g, db = torch.empty((T, N), dtype=F16, device=DEV), torch.empty(N, device=DEV)
+    if gated:
+        dX = li8.gated_backward(dY, pre, dev(Wq), dev(sW), grad_pre=g, dbias=db)
+    else:
+        dX = li8.linear_backward(dY, dev(Wq), dev(sW), pre=pre, activation="silu", grad_pre=g, dbias=db)
+    want = ffn.backward(_rows(dY, rows), _rows(pre, rows), Wq, sW, "silu", gated)
+    for t, k in ((dX, "dX"), (g, "grad_pre")):
+        assert ffn.check(_rows(t, rows), want[k], k) is None, ffn.check(_rows(t, rows), want[k], k)
+    # the sums of some features over all rows
+    for f in (0, F - 1):
+        cols = [f, F + f] if gated else [f]
+        z, ez = ffn.grad_pre(host(dY[:, f:f + 1]), host(pre[:, cols]), "silu", gated)
+        w = (z.sum(0), ez.sum(0) + (T + 2) * ffn.U * (np.abs(z) + ez).sum(0))
+        assert ffn.check(host(db[cols]), w, "dbias") is None, ffn.check(host(db[cols]), w, "dbias")
