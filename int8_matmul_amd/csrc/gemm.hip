@@ -43,6 +43,7 @@
 //    8, residual 2, the kept Z 3.  The gated pair of 4096 x 4096 x 2 * 11008 takes 394 us (its
 //    kernel; 1.87 POP/s, bound like the plain product by the clock that the board's
 //    power allows).
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -67,7 +68,17 @@ typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 // neighbouring accumulator blocks; H, half as wide as Z, is all that is
 // written unless the caller keeps z.
 
-template <int BM, int BN, int BKS, int NS, int WM, int WN, int GM, bool F16W, bool STORE_ACC, int EPI>
+//
+// RANGE: K_ALL, the whole call in a workgroup.  K_PART and K_SUM, for calls of
+// few tiles and a long K: one workgroup per tile and range of K stores its int32
+// sums, and a second launch with tiles of its own adds the ranges (exactly, so
+// the results are K_ALL's) and goes on with the epilogue.  The sums lie in
+// acc_out by 32x32 blocks in the order of the registers, [range][block of
+// tokens][block of weight rows][4][64 lanes] of four: whole lines each way.
+enum { K_ALL, K_PART, K_SUM };
+
+template <int BM, int BN, int BKS, int NS, int WM, int WN, int GM, bool F16W, bool STORE_ACC, int EPI,
+          int RANGE = K_ALL>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     const int8_t *__restrict__ Xq, const int8_t *__restrict__ Wq,
     const float *__restrict__ sX, const float *__restrict__ sW,
@@ -96,7 +107,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     // gather them from Wq, a second read of the weight when the outlier
     // columns are spread over K.  It needs the outlier list and the prefix
     // counts per bit-set word (stage s starts at word 4s).
-    constexpr int CAP = (F16W || BN > 128) ? 0 : 256;
+    constexpr int CAP = (F16W || BN > 128 || RANGE != K_ALL) ? 0 : 256;
     constexpr int NWMAX = kFoldMaxK / 32;      // bit-set words
     constexpr int PF_SX = NS * SSZ, PF_SW = PF_SX + 4 * BM, PF_XO = PF_SW + 4 * BN;
     constexpr int PF_WO = PF_XO + 32 * BM;     // chunk 0 of the gathered WO, or WOT when folding
@@ -109,6 +120,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     constexpr int PF_END = EPI != EPI_PLAIN ? PF_BIAS + 4 * BN : PF_DUMMY + (CAP > 0 ? NT : 0);
     constexpr int LDSB = (PF_END > STG || EPI != EPI_PLAIN) ? PF_END : STG;
     static_assert(EPI == EPI_PLAIN || (!F16W && !STORE_ACC && 2 * BM * BN <= NS * SSZ), "epilogue variants");
+    static_assert(EPI != EPI_PLAIN || RANGE == K_ALL, "ranges of K: epilogue variants only");
     static_assert(EPI != EPI_GATED || FN % 2 == 0, "gate and up blocks in pairs");
     static_assert(FM * WM * 32 == BM && FN * WN * 32 == BN, "tile shape");
     static_assert(LA * NT == BM * CPR && LB * NT == BN * CPR, "loader shape");
@@ -121,10 +133,16 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
 
     // ---- tile of this workgroup ----
     int bid = blockIdx.x;
+    const int ranges = RANGE == K_ALL ? 1 : epi.ranges;
     {
-        const int nblk = tiles_m * tiles_n;
+        const int nblk = tiles_m * tiles_n * (RANGE == K_PART ? ranges : 1);
         const int per = nblk / 8, rem = nblk % 8, xcd = bid % 8, loc = bid / 8;
         bid = (xcd < rem) ? xcd * (per + 1) + loc : rem * (per + 1) + (xcd - rem) * per + loc;
+    }
+    int range = 0;
+    if constexpr (RANGE == K_PART) {
+        range = bid / (tiles_m * tiles_n);
+        bid -= range * (tiles_m * tiles_n);
     }
     const int width = GM * tiles_n;
     const int first_m = (bid / width) * GM;
@@ -138,7 +156,11 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     asm volatile("" ::"s"(sX), "s"(sW), "s"(XO), "s"(WO), "s"(Y), "s"(acc_out));
     const int nO = min(max(meta[0], 0), K);   // (a bad workspace cannot lengthen the loop)
     asm volatile("" ::"s"(nO));
-    const int nk = (K + BKS - 1) / BKS;
+    // stages of this workgroup: nk from stage kfirst on (K_PART: an even share, at least one)
+    const int nkall = (K + BKS - 1) / BKS;
+    const int kper = nkall / ranges, kmore = nkall - kper * ranges;
+    const int kfirst = RANGE == K_PART ? range * kper + min(range, kmore) : 0;
+    const int nk = RANGE == K_ALL ? nkall : RANGE == K_SUM ? 0 : kper + (range < kmore ? 1 : 0);
     // weight row of the tile's local row c (clamped to the last one)
     const int F = N >> 1;
     auto wrow = [&](int c) {
@@ -150,7 +172,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         }
     };
     float bias_v = 0.0f;
-    if constexpr (EPI != EPI_PLAIN)
+    if constexpr (EPI != EPI_PLAIN && RANGE != K_PART)
         if (epi.bias)
             bias_v = h2f(epi.bias[wrow(min(tid, BN - 1))]);
     const bool fold = CAP > 0 && nO > kFoldMin && nO <= CAP && K <= kFoldMaxK;   // (uniform)
@@ -174,7 +196,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         kmB[i] = K - q * 16;
     }
     auto issue = [&](int kt) {
-        const int k0 = kt * BKS;
+        const int k0 = (RANGE == K_PART ? kfirst + kt : kt) * BKS;
         int8_t *st = lds + (kt % NS) * SSZ;
 #pragma unroll
         for (int i = 0; i < LA; i++)
@@ -212,6 +234,46 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
 #pragma unroll
         for (int b = 0; b < FN; b++)
             acc[a][b] = v16i{};
+    // this lane's first 16-byte piece of the sums of 32x32 block (a, b) of this wave
+    // (past the last block: of the last one)
+    const int blocks_n = EPI == EPI_GATED ? 2 * ((F + 31) / 32) : (N + 31) / 32, blocks_m = (T + 31) / 32;
+    auto sums_of = [&](int r, int a, int b) {
+        const int mb = min((m0 >> 5) + wm * FM + a, blocks_m - 1), nb = min((n0 >> 5) + wn * FN + b, blocks_n - 1);
+        return reinterpret_cast<v4i *>(acc_out) + (((int64_t)r * blocks_m + mb) * blocks_n + nb) * 256 + lane;
+    };
+    if constexpr (RANGE == K_SUM) {
+        auto add = [&](int r, auto count) {   // `count` ranges, all loads in flight together
+            constexpr int C = decltype(count)::value;
+            v4i x[C][FM][FN][4];
+#pragma unroll
+            for (int i = 0; i < C; i++)
+#pragma unroll
+                for (int a = 0; a < FM; a++)
+#pragma unroll
+                    for (int b = 0; b < FN; b++)
+#pragma unroll
+                        for (int g = 0; g < 4; g++)
+                            x[i][a][b][g] = sums_of(r + i, a, b)[64 * g];
+#pragma unroll
+            for (int i = 0; i < C; i++)
+#pragma unroll
+                for (int a = 0; a < FM; a++)
+#pragma unroll
+                    for (int b = 0; b < FN; b++)
+#pragma unroll
+                        for (int k = 0; k < 16; k++)
+                            acc[a][b][k] += x[i][a][b][k >> 2][k & 3];
+        };
+        int r = 0;
+        for (; r + 4 <= ranges; r += 4)
+            add(r, std::integral_constant<int, 4>{});
+        if (r + 2 <= ranges) {
+            add(r, std::integral_constant<int, 2>{});
+            r += 2;
+        }
+        if (r < ranges)
+            add(r, std::integral_constant<int, 1>{});
+    }
 
     v4i fa[2][FM], fb[2][FN];
     auto lread = [&](int set, int kt, int kk) {
@@ -355,7 +417,11 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     // rows past T or N read zeros or clamp, and are never stored
     const __amdgpu_buffer_rsrc_t rXO = make_rsrc(XO, (int)(2u * (unsigned)T * (unsigned)K));
     const __amdgpu_buffer_rsrc_t rWO = make_rsrc(WO, (int)((unsigned)WOE * (unsigned)N * (unsigned)K));
-    {
+    // K_SUM: the sums share the gathered WO's place from its end; where they have
+    // run into it (nearly all columns outliers) the codes are taken from Wq
+    const bool direct = RANGE == K_SUM && (int64_t)((nO + 15) >> 4) * 16 * N >
+                                              reinterpret_cast<const int8_t *>(acc_out) - WO;
+    if constexpr (RANGE != K_PART) {
         auto prefetch = [&](__amdgpu_buffer_rsrc_t r, int off, auto bytes_c, int n, auto voff) {
             constexpr int B = decltype(bytes_c)::value;   // bytes per lane
 #pragma unroll
@@ -404,7 +470,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         wait_loads_barrier<0>();
         lread(0, 0, 0);
     }
-    if constexpr (EPI != EPI_PLAIN)   // (visible after the barriers below)
+    if constexpr (EPI != EPI_PLAIN && RANGE != K_PART)   // (visible after the barriers below)
         if (tid < BN)
             *reinterpret_cast<float *>(lds + PF_BIAS + 4 * tid) = bias_v;
 
@@ -434,6 +500,21 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     // (for this half-wave) feature of the wave's sub-tile.
     const int tok0 = m0 + wm * FM * 32 + (lane & 31);
     const int fea0 = n0 + wn * FN * 32 + 4 * khalf;
+    if constexpr (RANGE == K_PART) {
+#pragma unroll
+        for (int a = 0; a < FM; a++)
+#pragma unroll
+            for (int b = 0; b < FN; b++) {
+                v4i *dst = sums_of(range, a, b);
+                if ((m0 >> 5) + wm * FM + a < blocks_m && (n0 >> 5) + wn * FN + b < blocks_n)
+#pragma unroll
+                    for (int g = 0; g < 4; g++)
+                        __builtin_nontemporal_store(v4i{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2],
+                                                        acc[a][b][4 * g + 3]},
+                                                    dst + 64 * g);
+            }
+        return;
+    }
     if constexpr (STORE_ACC) {
 #pragma unroll
         for (int a = 0; a < FM; a++)
@@ -510,6 +591,20 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     v8h ox[2][FM];
     v2u ow[2][FN];     // int8 codes
     v8h ow16[2][FN];   // fp16 weight (the fp16-weight variant)
+    // chunk c of block b's codes by the outlier list (ranks past nO: codes times XO's zero pad)
+    auto wdirect = [&](int c, int b) {
+        const __amdgpu_buffer_rsrc_t rI = make_rsrc(idx_g, 4 * K);
+        const int row = wrow(wn * FN * 32 + 32 * b + (lane & 31)) * K;
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int r = 16 * c + 8 * khalf + e;
+            const int col = (int)__builtin_amdgcn_raw_buffer_load_b32(rI, r < nO ? 4 * r : kOutOfRange, 0, 0);
+            w[e >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rB, row + min(max(col, 0), K - 1), 0, 0)
+                         << (8 * (e & 3));
+        }
+        return v2u{w[0], w[1]};
+    };
     auto oload = [&](int set, int c) {
 #pragma unroll
         for (int a = 0; a < FM; a++)
@@ -523,6 +618,10 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
 #pragma unroll
             for (int b = 0; b < FN; b++)
                 ow[set][b] = *reinterpret_cast<const v2u *>(wot + c * (BN * 16) + (lfea + 32 * b) * 16 + khalf * 8);
+        } else if (direct) {
+#pragma unroll
+            for (int b = 0; b < FN; b++)
+                ow[set][b] = wdirect(c, b);
         } else {
 #pragma unroll
             for (int b = 0; b < FN; b++)
@@ -538,6 +637,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         for (int b = 0; b < FN; b++) {
             if constexpr (F16W)
                 ow16[0][b] = *reinterpret_cast<const v8h *>(lds + PF_WO + (lfea + 32 * b) * 32 + khalf * 16);
+            else if (direct)
+                ow[0][b] = wdirect(0, b);
             else
                 ow[0][b] = *reinterpret_cast<const v2u *>(lds + PF_WO + (lfea + 32 * b) * 16 + khalf * 8);
         }
@@ -841,15 +942,16 @@ hipError_t launch_cfg(const int8_t *Wq, const float *sW, int64_t T, int64_t K, i
     return hipGetLastError();
 }
 
-template <int BM, int BN, int BKS, int NS, int WM, int WN, int GM, int EPI>
+template <int BM, int BN, int BKS, int NS, int WM, int WN, int GM, int EPI, int RANGE = K_ALL>
 hipError_t launch_epi_cfg(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
-                          uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s)
+                          uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s,
+                          int32_t *sums = nullptr)
 {
     // (a pair's tile of BN rows is BN/2 of its N/2 features)
     const int tiles_m = (int)((T + BM - 1) / BM);
     const int tiles_n = EPI == EPI_GATED ? (int)((N / 2 + BN / 2 - 1) / (BN / 2)) : (int)((N + BN - 1) / BN);
-    hipLaunchKernelGGL((k_gemm<BM, BN, BKS, NS, WM, WN, GM, false, false, EPI>),
-                       dim3((unsigned)(tiles_m * tiles_n)), dim3(WM * WN * 64), 0, s,
+    hipLaunchKernelGGL((k_gemm<BM, BN, BKS, NS, WM, WN, GM, false, false, EPI, RANGE>),
+                       dim3((unsigned)(tiles_m * tiles_n * (RANGE == K_PART ? epi.ranges : 1))), dim3(WM * WN * 64), 0, s,
                        reinterpret_cast<const int8_t *>(ws + L.Xq), Wq,
                        reinterpret_cast<const float *>(ws + L.sX), sW,
                        reinterpret_cast<const int32_t *>(ws + L.meta),
@@ -857,7 +959,7 @@ hipError_t launch_epi_cfg(const int8_t *Wq, const float *sW, int64_t T, int64_t 
                        reinterpret_cast<const int8_t *>(ws + L.WO),
                        reinterpret_cast<const int32_t *>(ws + L.idx),
                        reinterpret_cast<const int32_t *>(ws + L.wpre), (int)T, (int)K, (int)N, tiles_m,
-                       tiles_n, Y, nullptr, epi);
+                       tiles_n, Y, sums, epi);
     return hipGetLastError();
 }
 
@@ -921,6 +1023,25 @@ hipError_t launch_gemm(const int8_t *Wq, const float *sW, int64_t T, int64_t K, 
 // 64 x 4096 x 2 * 11008 38.1 -> 26.7; with two rounds of them 1024 x 4096 x 4096 43.2 ->
 // 40.4 and gated 512 x 1024 x 2 * 4096 19.4 -> 20.3; with three gated 256 x 4096 x 2 * 11008
 // 41.8 -> 52.1.
+//
+// Where even these are fewer than the CUs, ranges of K (K_PART, K_SUM) while all
+// their workgroups run at once, by a model in us: 0.42 a stage or the weight at
+// 5 TB/s, and for the second launch 3.5, 0.5 a round of its loads, and the sums
+// written and read.  Whole calls, ranges of the model's choice against one and others: 64 x 4096 x
+// 4096 4: 17.9, 1: 20.4, 8: 18.9; 64 x 11008 x 4096 4: 25.3, 1: 38.5, 8: 25.4; 128 x
+// 11008 x 4096 4: 26.6, 1: 38.9, 2: 30.7; 256 x 11008 x 4096 2: 33.9, 1: 40.8, 4: 36.6;
+// 64 x 28672 x 8192 2: 57, 1: 83.7, 3: 55.8; 160 x 6272 x 176 8: 17.6, 1: 25.7; but 64 x
+// 2048 x 2048 1: 15.0, 4: 15.1.  The sums go where outlier columns are gathered,
+// from its end, so the workspace is the plain layer's; more ranges than fit are
+// not taken.
+constexpr int kEpiRanges = 16;
+// Bytes of the ranges' sums: whole 32x32 blocks.
+static int64_t epi_sums_bytes(int64_t T, int64_t N, int64_t ranges, bool gated)
+{
+    const int64_t blocks_n = gated ? 2 * ((N / 2 + 31) / 32) : (N + 31) / 32;
+    return ranges * ((T + 31) / 32) * blocks_n * 4096;
+}
+
 GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated)
 {
     const GemmPlan p = gemm_plan(T, K, N, gated);
@@ -928,15 +1049,44 @@ GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated)
         return (double)(((T + bm - 1) / bm * ((N + bn - 1) / bn) + kCUs - 1) / kCUs);
     };
     const double cost = rounds(p.bm, p.bn) * (p.bn == 256 ? 1.0 : p.bn == 192 ? 0.75 * 1.15 : 0.5 * 1.35);
-    if (0.33 * rounds(64, 128) < cost)
-        return {64, 128, K <= kFoldMaxK ? 256 : 0};
-    return p;
+    if (0.33 * rounds(64, 128) >= cost)
+        return p;
+    const int64_t nk = (K + 127) / 128, tiles = (T + 63) / 64 * ((N + 127) / 128);
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= std::min<int64_t>(kEpiRanges, nk) && (s == 1 || tiles * s <= kCUs); s++) {
+        const int64_t bytes = epi_sums_bytes(T, N, s, gated);
+        if (s > 1 && bytes > N * K)
+            break;
+        double us = std::max(0.42 * (double)((nk + s - 1) / s), (double)(N * K) / 5e6);
+        if (s > 1)
+            us += 3.5 + 0.5 * (s / 4 + (s >> 1 & 1) + (s & 1)) + (double)bytes / 2.7e6;
+        if (us < least) {
+            least = us;
+            best = s;
+        }
+    }
+    return {64, 128, best == 1 && K <= kFoldMaxK ? 256 : 0, best};
 }
 
 hipError_t launch_gemm_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
                            uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s)
 {
     const GemmPlan p = epi_plan(T, K, N, epi.gated);
+    if (p.ranges > 1) {   // (the sums at the end of the gathered WO's place)
+        EpiParams e = epi;
+        e.ranges = p.ranges;
+        int32_t *sums = reinterpret_cast<int32_t *>(const_cast<char *>(ws) + L.WO +
+                                                    (N * K - epi_sums_bytes(T, N, p.ranges, epi.gated)) / 256 * 256);
+        const hipError_t err =
+            epi.gated ? launch_epi_cfg<64, 128, 128, 4, 2, 2, 4, EPI_GATED, K_PART>(Wq, sW, T, K, N, Y, ws, L, e, s, sums)
+                      : launch_epi_cfg<64, 128, 128, 4, 2, 4, 4, EPI_LINEAR, K_PART>(Wq, sW, T, K, N, Y, ws, L, e, s, sums);
+        if (err != hipSuccess)
+            return err;
+        return epi.gated
+                   ? launch_epi_cfg<32, 64, 128, 2, 1, 1, 4, EPI_GATED, K_SUM>(Wq, sW, T, K, N, Y, ws, L, e, s, sums)
+                   : launch_epi_cfg<32, 64, 128, 2, 1, 2, 4, EPI_LINEAR, K_SUM>(Wq, sW, T, K, N, Y, ws, L, e, s, sums);
+    }
     if (p.bm == 64)
         return epi.gated ? launch_epi_cfg<64, 128, 128, 4, 2, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s)
                          : launch_epi_cfg<64, 128, 128, 4, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);

@@ -629,3 +629,37 @@ def test_backward_past_32_bit_offsets(gated):
         z, ez = ffn.grad_pre(host(dY[:, f:f + 1]), host(pre[:, cols]), "silu", gated)
         w = (z.sum(0), ez.sum(0) + (T + 2) * ffn.U * (np.abs(z) + ez).sum(0))
         assert ffn.check(host(db[cols]), w, "dbias") is None, ffn.check(host(db[cols]), w, "dbias")
+
+
+# few tiles and a long K, whose int32 sums come from several workgroups; T, K, N
+RANGED = [(17, 4096, 8), (64, 4096, 258), (33, 8208, 100), (100, 11008, 74), (200, 6272, 386), (250, 16400, 66), (65, 2064, 34)]
+
+
+@pytest.mark.parametrize("T, K, N", RANGED)
+@pytest.mark.parametrize("kw, threshold", [({}, 6.0), (dict(sparse=2e-3), 6.0), (dict(fixed=700), 6.0), ({}, float("inf"))])
+def test_ranges_of_k(T, K, N, kw, threshold):
+    print(f"case ranges {T}x{K}x{N} {kw} {threshold}", flush=True)
+    f = Forward(T, K, N, seed=13, residual=True, **kw)
+    act = ffn.ACTS[(T + len(kw)) % 5]
+    f.epilogue(threshold, act)
+    f.epilogue(threshold, act, save=False, in_place=True)
+    f.gated(threshold, act)
+    x, w, s = f.d["X"], f.d["Wq"], f.d["sW"]
+    Y = li8.linear(x, w, s, threshold).view(torch.int16)
+    pre = torch.empty((T, N), dtype=F16, device=DEV)
+    assert torch.equal(li8.linear_epilogue(x, w, s, threshold).view(torch.int16), Y)
+    li8.gated_linear(x, w, s, threshold, pre=pre)
+    assert torch.equal(pre.view(torch.int16), Y)
+
+
+@pytest.mark.parametrize("T, K, N", [(17, 4096, 8), (64, 4096, 130), (100, 6160, 74)])
+def test_ranges_of_k_with_every_column_an_outlier(T, K, N):
+    """The gathered columns then fill the place where the ranges' sums lie."""
+    print(f"case ranges all {T}x{K}x{N}", flush=True)
+    f = Forward(T, K, N, seed=14)
+    f.X[f.X == 0] = 1.0
+    f.d["X"] = dev(f.X)
+    f.epilogue(0.0, "silu")
+    f.gated(0.0, "silu")
+    x, w, s = f.d["X"], f.d["Wq"], f.d["sW"]
+    assert torch.equal(li8.linear_epilogue(x, w, s, 0.0).view(torch.int16), li8.linear(x, w, s, 0.0).view(torch.int16))
