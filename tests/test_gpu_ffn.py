@@ -434,7 +434,7 @@ def calls(T, K, F, seed):
     return run, o, (x, dy, dh)
 
 
-SIZES = [(5, 256, 40), (8, 8208, 20), (40, 1024, 520), (300, 528, 260)]
+SIZES = [(5, 256, 40), (8, 8208, 20), (40, 1024, 520), (300, 528, 260), (50, 6160, 130)]
 
 
 @pytest.mark.parametrize("T, K, F", SIZES)
