@@ -107,7 +107,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     // gather them from Wq, a second read of the weight when the outlier
     // columns are spread over K.  It needs the outlier list and the prefix
     // counts per bit-set word (stage s starts at word 4s).
-    constexpr int CAP = (F16W || BN > 128 || RANGE != K_ALL) ? 0 : 256;
+    // (not with three stages of a 64x128 tile, which leave room for two workgroups a CU)
+    constexpr int CAP = (F16W || BN > 128 || RANGE != K_ALL || (BM == 64 && NS == 3)) ? 0 : 256;
     constexpr int NWMAX = kFoldMaxK / 32;      // bit-set words
     constexpr int PF_SX = NS * SSZ, PF_SW = PF_SX + 4 * BM, PF_XO = PF_SW + 4 * BN;
     constexpr int PF_WO = PF_XO + 32 * BM;     // chunk 0 of the gathered WO, or WOT when folding
@@ -175,7 +176,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
     if constexpr (EPI != EPI_PLAIN && RANGE != K_PART)
         if (epi.bias)
             bias_v = h2f(epi.bias[wrow(min(tid, BN - 1))]);
-    const bool fold = CAP > 0 && nO > kFoldMin && nO <= CAP && K <= kFoldMaxK;   // (uniform)
+    // (uniform; the variants: as epi_plan told the prepare kernel)
+    const bool fold = CAP > 0 && nO > kFoldMin && nO <= CAP && (EPI == EPI_PLAIN ? K <= kFoldMaxK : epi.fold > 0);
 
     // ---- global -> LDS loaders: load i of this lane fills LDS chunk
     // p = i*NT + wid*64 + lane of the stage (row p / CPR, physical chunk
@@ -1024,6 +1026,15 @@ hipError_t launch_gemm(const int8_t *Wq, const float *sW, int64_t T, int64_t K, 
 // 40.4 and gated 512 x 1024 x 2 * 4096 19.4 -> 20.3; with three gated 256 x 4096 x 2 * 11008
 // 41.8 -> 52.1.
 //
+// More tiles than CUs: three stages ahead and no fold's buffers, so that two workgroups
+// share a CU (1024 x 4096 x 4096 42.9 -> 38.1, 512 x 4096 x 4608 37.2 -> 30.7, gated 256 x
+// 2048 x 2 * 5504 25.9 -> 22.0; with one round of them it loses 2 %).  The fold's copies
+// cost these short stages more than the gather costs, except where the weight has many
+// rows: 70 outlier columns, fold and gather, 512 x 4096 x 4096 32.0 and 28.7, gated 100 x
+// 4096 x 2 * 4096 31.0 and 26.7, 64 x 4096 x 11008 28.0 and 28.8, gated 64 x 4096 x 2 *
+// 11008 29.9 and 36.8.
+constexpr int64_t kEpiFoldMinN = 12288;
+//
 // Where even these are fewer than the CUs, ranges of K (K_PART, K_SUM) while all
 // their workgroups run at once, by a model in us: 0.42 a stage or the weight at
 // 5 TB/s, and for the second launch 3.5, 0.5 a round of its loads, and the sums
@@ -1051,7 +1062,8 @@ GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated)
     const double cost = rounds(p.bm, p.bn) * (p.bn == 256 ? 1.0 : p.bn == 192 ? 0.75 * 1.15 : 0.5 * 1.35);
     if (0.33 * rounds(64, 128) >= cost)
         return p;
-    const int64_t nk = (K + 127) / 128, tiles = (T + 63) / 64 * ((N + 127) / 128);
+    const int64_t nk = (K + 127) / 128;
+    const int64_t tiles = (T + 63) / 64 * (gated ? (N / 2 + 63) / 64 : (N + 127) / 128);
     int best = 1;
     double least = 1e300;
     for (int s = 1; s <= std::min<int64_t>(kEpiRanges, nk) && (s == 1 || tiles * s <= kCUs); s++) {
@@ -1066,16 +1078,18 @@ GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated)
             best = s;
         }
     }
-    return {64, 128, best == 1 && K <= kFoldMaxK ? 256 : 0, best};
+    const bool two = tiles > kCUs;
+    return {64, 128, best == 1 && !two && K <= kFoldMaxK && N > kEpiFoldMinN ? 256 : 0, best, two};
 }
 
 hipError_t launch_gemm_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
                            uint16_t *Y, const char *ws, const WsLayout &L, const EpiParams &epi, hipStream_t s)
 {
     const GemmPlan p = epi_plan(T, K, N, epi.gated);
+    EpiParams e = epi;
+    e.fold = p.fold;
+    e.ranges = p.ranges;
     if (p.ranges > 1) {   // (the sums at the end of the gathered WO's place)
-        EpiParams e = epi;
-        e.ranges = p.ranges;
         int32_t *sums = reinterpret_cast<int32_t *>(const_cast<char *>(ws) + L.WO +
                                                     (N * K - epi_sums_bytes(T, N, p.ranges, epi.gated)) / 256 * 256);
         const hipError_t err =
@@ -1087,18 +1101,21 @@ hipError_t launch_gemm_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t
                    ? launch_epi_cfg<32, 64, 128, 2, 1, 1, 4, EPI_GATED, K_SUM>(Wq, sW, T, K, N, Y, ws, L, e, s, sums)
                    : launch_epi_cfg<32, 64, 128, 2, 1, 2, 4, EPI_LINEAR, K_SUM>(Wq, sW, T, K, N, Y, ws, L, e, s, sums);
     }
+    if (p.bm == 64 && p.two)
+        return epi.gated ? launch_epi_cfg<64, 128, 128, 3, 2, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, e, s)
+                         : launch_epi_cfg<64, 128, 128, 3, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, e, s);
     if (p.bm == 64)
-        return epi.gated ? launch_epi_cfg<64, 128, 128, 4, 2, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s)
-                         : launch_epi_cfg<64, 128, 128, 4, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
+        return epi.gated ? launch_epi_cfg<64, 128, 128, 4, 2, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, e, s)
+                         : launch_epi_cfg<64, 128, 128, 4, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, e, s);
     if (epi.gated)
         return p.bn == 128
-                   ? launch_epi_cfg<256, 128, 128, 2, 4, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s)
-                   : launch_epi_cfg<256, 256, 128, 2, 2, 4, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, epi, s);
+                   ? launch_epi_cfg<256, 128, 128, 2, 4, 2, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, e, s)
+                   : launch_epi_cfg<256, 256, 128, 2, 2, 4, 4, EPI_GATED>(Wq, sW, T, K, N, Y, ws, L, e, s);
     if (p.bn == 128)
-        return launch_epi_cfg<256, 128, 128, 2, 4, 2, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
+        return launch_epi_cfg<256, 128, 128, 2, 4, 2, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, e, s);
     if (p.bn == 192)
-        return launch_epi_cfg<256, 192, 128, 2, 4, 2, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
-    return launch_epi_cfg<256, 256, 128, 2, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, epi, s);
+        return launch_epi_cfg<256, 192, 128, 2, 4, 2, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, e, s);
+    return launch_epi_cfg<256, 256, 128, 2, 2, 4, 4, EPI_LINEAR>(Wq, sW, T, K, N, Y, ws, L, e, s);
 }
 
 } // namespace li8

@@ -131,7 +131,8 @@ constexpr int kFoldMin = 64;
 constexpr int64_t kFoldMaxK = 8192;
 struct GemmPlan {
     int bm, bn, fold;
-    int ranges = 1;   // of K (epi_plan only)
+    int ranges = 1;     // of K (epi_plan only)
+    bool two = false;   // two workgroups a CU (epi_plan's 64x128 tile)
 };
 // gated: the N = 2F rows of a gated pair, whose tiles take gate and up rows in
 // pairs of 32-row blocks (not the 192-wide tiles, whose waves hold three blocks).
@@ -172,7 +173,9 @@ struct EpiParams {
     uint16_t *pre;
     ActParams act;
     bool gated;
-    int ranges = 1;   // of K, in a tiled call that splits it
+    // of a tiled call's plan
+    int fold = 0;
+    int ranges = 1;
 };
 
 // Launcher (gemm.hip).

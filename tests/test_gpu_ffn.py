@@ -663,3 +663,19 @@ def test_ranges_of_k_with_every_column_an_outlier(T, K, N):
     f.gated(0.0, "silu")
     x, w, s = f.d["X"], f.d["Wq"], f.d["sW"]
     assert torch.equal(li8.linear_epilogue(x, w, s, 0.0).view(torch.int16), li8.linear(x, w, s, 0.0).view(torch.int16))
+
+
+@pytest.mark.parametrize("T, K, N", [(1024, 272, 2178), (700, 528, 4100), (64, 272, 12546), (100, 272, 16382), (64, 528, 8194)])
+@pytest.mark.parametrize("fixed", [3, 70, 150, 260])
+def test_small_tiles_in_rounds_and_with_many_outlier_columns(T, K, N, fixed):
+    print(f"case small tiles {T}x{K}x{N} {fixed}", flush=True)
+    f = Forward(T, K, N, seed=15, fixed=fixed)
+    x, w, s = f.d["X"], f.d["Wq"], f.d["sW"]
+    Y = li8.linear(x, w, s).view(torch.int16)
+    pre = torch.empty((T, N), dtype=F16, device=DEV)
+    assert torch.equal(li8.linear_epilogue(x, w, s).view(torch.int16), Y)
+    li8.gated_linear(x, w, s, pre=pre)
+    assert torch.equal(pre.view(torch.int16), Y)
+    if fixed == 150 and T <= 100:
+        f.epilogue(activation="silu")
+        f.gated(activation="gelu")
