@@ -1028,14 +1028,16 @@ hipError_t launch_gemm(const int8_t *Wq, const float *sW, int64_t T, int64_t K, 
 //
 // More tiles than CUs: three stages ahead and no fold's buffers, so that two workgroups
 // share a CU (1024 x 4096 x 4096 42.9 -> 38.1, 512 x 4096 x 4608 37.2 -> 30.7, gated 256 x
-// 2048 x 2 * 5504 25.9 -> 22.0; with one round of them it loses 2 %).  The fold's copies
-// cost these short stages more than the gather costs, except where the weight has many
-// rows: 70 outlier columns, fold and gather, 512 x 4096 x 4096 32.0 and 28.7, gated 100 x
-// 4096 x 2 * 4096 31.0 and 26.7, 64 x 4096 x 11008 28.0 and 28.8, gated 64 x 4096 x 2 *
-// 11008 29.9 and 36.8.
-constexpr int64_t kEpiFoldMinN = 12288;
+// 2048 x 2 * 5504 25.9 -> 22.0; with one round of them it loses 2 %).
 //
-// Where even these are fewer than the CUs, ranges of K (K_PART, K_SUM) while all
+// The fold's copies cost short stages more than the gather costs, except where
+// the weight has many rows.  70 outlier columns, fold and gather: 512 x 4096 x 4096
+// 32.0 and 28.7, gated 100 x 4096 x 2 * 4096 31.0 and 26.7, 64 x 4096 x 11008 28.0 and
+// 28.8, gated 64 x 4096 x 2 * 11008 29.9 and 36.8; 256x128 tiles, 250 of them: 1500 x
+// 1024 x 4096 38.7 and 33.0, gated 512 x 2048 x 2 * 5504 41.2 and 38.6, 512 x 4096 x 11008
+// 56.7 and 56.3, 512 x 5120 x 13824 65.1 and 71.3.
+constexpr int64_t kEpiFoldMinN = 12288;
+// Where 64x128 tiles are fewer than the CUs, ranges of K (K_PART, K_SUM) while all
 // their workgroups run at once, by a model in us: 0.42 a stage or the weight at
 // 5 TB/s, and for the second launch 3.5, 0.5 a round of its loads, and the sums
 // written and read.  Whole calls, ranges of the model's choice against one and others: 64 x 4096 x
@@ -1060,8 +1062,9 @@ GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated)
         return (double)(((T + bm - 1) / bm * ((N + bn - 1) / bn) + kCUs - 1) / kCUs);
     };
     const double cost = rounds(p.bm, p.bn) * (p.bn == 256 ? 1.0 : p.bn == 192 ? 0.75 * 1.15 : 0.5 * 1.35);
+    const bool many = N > kEpiFoldMinN;
     if (0.33 * rounds(64, 128) >= cost)
-        return p;
+        return {p.bm, p.bn, many ? p.fold : 0};
     const int64_t nk = (K + 127) / 128;
     const int64_t tiles = (T + 63) / 64 * (gated ? (N / 2 + 63) / 64 : (N + 127) / 128);
     int best = 1;
@@ -1079,7 +1082,7 @@ GemmPlan epi_plan(int64_t T, int64_t K, int64_t N, bool gated)
         }
     }
     const bool two = tiles > kCUs;
-    return {64, 128, best == 1 && !two && K <= kFoldMaxK && N > kEpiFoldMinN ? 256 : 0, best, two};
+    return {64, 128, many && best == 1 && !two && K <= kFoldMaxK ? 256 : 0, best, two};
 }
 
 hipError_t launch_gemm_epi(const int8_t *Wq, const float *sW, int64_t T, int64_t K, int64_t N,
