@@ -752,7 +752,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(
         // ch's first column and how many of its features exist).  16-byte
         // stores at whatever alignment the row has (the hardware takes any);
         // element by element only a row's last chunk.  (777 x 1040 x 2 * 2731
-        // with the kept z: the kernel takes 24.3 us, 28.5 with 2-byte stores by
+        // with the kept z: the kernel took 24.3 us (now 22.0), 28.5 with 2-byte stores by
         // neighbouring lanes, 39.6 with eight 2-byte stores a lane.)
         auto store_rows = [&](auto cpr, uint16_t *out, int64_t ld, auto colof) {
             constexpr int CP = decltype(cpr)::value;
