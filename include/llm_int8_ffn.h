@@ -27,10 +27,12 @@
  * a residual that is Y itself.  llm_int8_plan is about llm_int8_linear; the
  * calls here take its few-token paths for the same shapes.
  * X and the weight must be finite.  A NaN of a bias or residual reaches the
- * outputs that it enters.  A row of gradients that holds an infinity or NaN
- * gives a dX row of infinities and NaN (what a loss scaler looks for).
- * Results past fp16's range become infinities; a row whose pre holds such
- * ones may give infinities and NaN.
+ * outputs that it enters.  At Z = +inf (by its bias) every activation is +inf; at
+ * -inf none keeps it, relu is 0 and the smooth ones are 0 times infinity, NaN.
+ * A row of gradients that holds an infinity or NaN gives a dX row of infinities
+ * and NaN (what a loss scaler looks for).  Results past fp16's range become
+ * infinities.  Where pre holds such ones the slopes are those of its side (1 and
+ * 0; none: 1); a pair's row may give infinities and NaN, as their products.
  */
 #ifndef LLM_INT8_FFN_H
 #define LLM_INT8_FFN_H

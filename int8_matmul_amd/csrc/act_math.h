@@ -25,10 +25,13 @@
 
 namespace li8 {
 
-// s(x) with exp(-x) = 2^(z (c1 + c3 z^2)): 0 and 1 at the ends, never NaN for finite z
+// s(x) with exp(-x) = 2^(z (c1 + c3 z^2)): 0 and 1 at the ends, infinities among
+// them, NaN for a NaN only.  (z^2 stops at the largest finite number: with silu's c3 =
+// 0 an infinite one would be 0 times infinity, from |z| = 1.85e19 on.)
 __device__ __forceinline__ float act_sigmoid(float z, const ActParams &p)
 {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * (p.c1 + p.c3 * (z * z))));
+    const float zz = __builtin_fminf(z * z, 3.402823466e38f);
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * (p.c1 + p.c3 * zz)));
 }
 
 // The normal integral at z, and e = exp(-z^2 / 2).
@@ -63,8 +66,8 @@ __device__ __forceinline__ float act_value(float z, const ActParams &p)
 
 // Value and slope at z.  The slope of relu at 0 is 0.  Kind 1 with
 // x = z (a1 + a3 z^2) is z s(x), whose slope is s + z s (1 - s) x'; far out
-// s (1 - s) is 0 and x' large, so the product is taken as zero there rather
-// than 0 times infinity.
+// s (1 - s) is 0 and x' large, infinite or NaN, so the product is taken as zero
+// there rather than 0 times infinity.
 template <int KIND>
 __device__ __forceinline__ void act_value_slope(float z, const ActParams &p, float &value, float &slope)
 {
