@@ -39,7 +39,7 @@ __all__ = [
     "KVCache", "KVBatch", "Rope", "new_kv_cache", "kv_append", "kv_read", "kv_attention",
     "kv_attention_plan", "kv_attention_workspace_bytes", "new_kv_attention_workspace",
     "linear_epilogue", "gated_linear", "linear_backward", "gated_backward",
-    "backward_workspace_bytes", "new_backward_workspace", "ACTIVATIONS",
+    "backward_workspace_bytes", "new_backward_workspace", "ACTIVATIONS", "epilogue_plan", "backward_plan",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -156,6 +156,9 @@ def load_library() -> ctypes.CDLL:
     L.llm_int8_backward_workspace_bytes.argtypes = [i64, i64, i64]
     L.llm_int8_linear_backward.restype = ctypes.c_int
     L.llm_int8_linear_backward.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    for plan in ("llm_int8_epilogue_plan", "llm_int8_backward_plan"):
+        getattr(L, plan).restype = ctypes.c_int
+        getattr(L, plan).argtypes = [i64, i64, i64, i32, vp]
     L.llm_int8_gated_backward.restype = ctypes.c_int
     L.llm_int8_gated_backward.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
     _lib = L
@@ -1006,6 +1009,30 @@ def gated_linear(X: torch.Tensor, Wq: torch.Tensor, sW: torch.Tensor, threshold:
     The workspace is that of ``linear`` for N = 2F."""
     return _forward("llm_int8_gated_linear", X, Wq, sW, float(threshold), bias, activation, None, out, pre, workspace,
                     True)
+
+
+def _plan(name: str, fields: tuple, paths: dict, T: int, K: int, N: int, gated: bool) -> dict:
+    out = (ctypes.c_int32 * len(fields))()
+    _check(name, getattr(load_library(), name)(T, K, N, int(bool(gated)), out))
+    return {f: paths[v] if f == "path" else v for f, v in zip(fields, out)}
+
+
+def epilogue_plan(T: int, K: int, N: int, gated: bool = False) -> dict:
+    """Which kernels ``linear_epilogue`` and ``gated_linear`` run for a weight of N rows (2F of a
+    pair): path, tile_m, tile_n, fold_lo, fold_hi, ranges (of K), per_cu; see
+    include/llm_int8_ffn_plan.h."""
+    return _plan("llm_int8_epilogue_plan", ("path", "tile_m", "tile_n", "fold_lo", "fold_hi", "ranges", "per_cu"), PATHS,
+                 T, K, N, gated)
+
+
+BACKWARD_PATHS = {0: "empty", 1: "few", 2: "tiled", 3: "rows"}
+
+
+def backward_plan(T: int, K: int, N: int, gated: bool = False) -> dict:
+    """The same of the gradients: path, tile (rows), ranges (of the weight's rows), row_threads,
+    row_rounds, strips."""
+    return _plan("llm_int8_backward_plan", ("path", "tile", "ranges", "row_threads", "row_rounds", "strips"),
+                 BACKWARD_PATHS, T, K, N, gated)
 
 
 def backward_workspace_bytes(T: int, K: int, N: int) -> int:

@@ -1085,6 +1085,24 @@ BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N)
     return best;
 }
 
+// A wave for short rows (a workgroup left most of its threads without work:
+// 3621 x 176 x 2 * 135 took 31.8 us a call, 13.3 with waves and the product's
+// smaller tile), else a workgroup.  Uneven rows take more registers for their addresses, so
+// only up to two rounds of them stay in registers.
+RowPlan row_plan(int64_t F)
+{
+    const int64_t g = (F + 7) / 8, rounds = (g + kRowThreads - 1) / kRowThreads;
+    if (g <= 2 * 64)
+        return {64, (int)((g + 63) / 64)};
+    return {kRowThreads, rounds <= (row_mode((int)F) == MOVED ? 2 : 4) ? (int)rounds : 0};
+}
+
+// 512 rows a strip, while that leaves enough workgroups for the chip
+int col_strips(int64_t T, int64_t F)
+{
+    return (int)std::max<int64_t>(1, std::min<int64_t>({kMaxColStrips, (T + 255) / 512, 2048 / ((F + 127) / 128)}));
+}
+
 BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
 {
     const size_t A = 256;
@@ -1111,42 +1129,36 @@ void launch_rows_as(const GradArgs &a, const ColSums &c, uint16_t *A, float *fac
                        dim3(kRowThreads), 0, s, a, c, A, fac);
 }
 
-// A wave for short rows (a workgroup left most of its threads without work:
-// 3621 x 176 x 2 * 135 took 31.8 us a call, 13.3 with waves and the product's
-// smaller tile), else a workgroup.  Uneven rows take more registers for their addresses, so
-// only up to two rounds of them stay in registers.
+template <bool GATED, int KIND, int MODE>
+void launch_rows_mode(const GradArgs &a, const ColSums &c, const RowPlan &p, uint16_t *A, float *fac, hipStream_t s)
+{
+    if (p.threads == 64)
+        return p.rounds == 1 ? launch_rows_as<GATED, KIND, MODE, 64, 1>(a, c, A, fac, s)
+                             : launch_rows_as<GATED, KIND, MODE, 64, 2>(a, c, A, fac, s);
+    switch (p.rounds) {
+    case 1: return launch_rows_as<GATED, KIND, MODE, kRowThreads, 1>(a, c, A, fac, s);
+    case 2: return launch_rows_as<GATED, KIND, MODE, kRowThreads, 2>(a, c, A, fac, s);
+    case 0: return launch_rows_as<GATED, KIND, MODE, kRowThreads, 0>(a, c, A, fac, s);
+    }
+    if constexpr (MODE == EVEN) {
+        if (p.rounds == 3)
+            launch_rows_as<GATED, KIND, MODE, kRowThreads, 3>(a, c, A, fac, s);
+        else
+            launch_rows_as<GATED, KIND, MODE, kRowThreads, 4>(a, c, A, fac, s);
+    }
+}
+
 template <bool GATED, int KIND>
 void launch_rows(const GradArgs &a, const ColSums &c, uint16_t *A, float *fac, hipStream_t s)
 {
-    const int F = GATED ? a.N / 2 : a.N, g = (F + 7) / 8, mode = row_mode(F);
-    if (mode == SHORT) {
+    const int F = GATED ? a.N / 2 : a.N, mode = row_mode(F);
+    const RowPlan p = row_plan(F);
+    if (mode == SHORT)
         launch_rows_as<GATED, KIND, SHORT, 64, 1>(a, c, A, fac, s);
-    } else if (mode == MOVED) {
-        if (g <= 64)
-            launch_rows_as<GATED, KIND, MOVED, 64, 1>(a, c, A, fac, s);
-        else if (g <= 2 * 64)
-            launch_rows_as<GATED, KIND, MOVED, 64, 2>(a, c, A, fac, s);
-        else if (g <= kRowThreads)
-            launch_rows_as<GATED, KIND, MOVED, kRowThreads, 1>(a, c, A, fac, s);
-        else if (g <= 2 * kRowThreads)
-            launch_rows_as<GATED, KIND, MOVED, kRowThreads, 2>(a, c, A, fac, s);
-        else
-            launch_rows_as<GATED, KIND, MOVED, kRowThreads, 0>(a, c, A, fac, s);
-    } else if (g <= 64) {
-        launch_rows_as<GATED, KIND, EVEN, 64, 1>(a, c, A, fac, s);
-    } else if (g <= 2 * 64) {
-        launch_rows_as<GATED, KIND, EVEN, 64, 2>(a, c, A, fac, s);
-    } else if (g <= kRowThreads) {
-        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 1>(a, c, A, fac, s);
-    } else if (g <= 2 * kRowThreads) {
-        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 2>(a, c, A, fac, s);
-    } else if (g <= 3 * kRowThreads) {
-        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 3>(a, c, A, fac, s);
-    } else if (g <= 4 * kRowThreads) {
-        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 4>(a, c, A, fac, s);
-    } else {
-        launch_rows_as<GATED, KIND, EVEN, kRowThreads, 0>(a, c, A, fac, s);
-    }
+    else if (mode == MOVED)
+        launch_rows_mode<GATED, KIND, MOVED>(a, c, p, A, fac, s);
+    else
+        launch_rows_mode<GATED, KIND, EVEN>(a, c, p, A, fac, s);
 }
 
 // f(integral_constant<int, KIND>) for the call's activation.
@@ -1230,9 +1242,8 @@ hipError_t launch_backward(const uint16_t *dY, const uint16_t *pre, const ActPar
     const int features = (int)(gated ? N / 2 : N);
     ColSums c{};
     if (dbias && !few) {
-        // 512 rows a strip, while that leaves enough workgroups for the chip
         c.blocks = (features + 127) / 128;
-        c.strips = std::max(1, std::min({kMaxColStrips, (int)((T + 255) / 512), 2048 / c.blocks}));
+        c.strips = col_strips(T, features);
         c.out = c.strips > 1 ? reinterpret_cast<float *>(ws + L.cols) : dbias;
         if (c.strips > 1) {
             join.cols = c.out;

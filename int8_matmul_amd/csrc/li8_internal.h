@@ -246,6 +246,14 @@ struct BackwardPlan {
     bool few;   // the one kernel for few rows
 };
 BackwardPlan backward_plan(int64_t T, int64_t K, int64_t N);
+// How k_grad_rows takes a row of F > 0 features: its threads, and the rounds of eight
+// features a thread that stay in registers (0: any number, formed twice).
+struct RowPlan {
+    int threads, rounds;
+};
+RowPlan row_plan(int64_t F);
+// Strips of the tokens for dbias, F > 0 features a row of a part (not for few rows).
+int col_strips(int64_t T, int64_t F);
 // Workspace: the product's operand A fp16 [T,Np], its rows' factors fp32 [T],
 // dbias' partial sums fp32 [kMaxColStrips][N], the split product's partial
 // sums fp32 [splits][T,K].
