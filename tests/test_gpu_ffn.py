@@ -1,6 +1,6 @@
 """GPU tests of the feed-forward operators against their 64-bit forms: every element
-within the bound of its own roundings (oracle/ffn.py), at sizes that reach every
-kernel variant and its edges."""
+within the bound of its own roundings (oracle/ffn.py), at the edges of sizes and values.
+(test_gpu_ffn_tiles.py goes through the kernel variants by their plans.)"""
 import dataclasses
 
 import numpy as np
@@ -248,7 +248,7 @@ ROWS = [
     (48, 256, 2050), (49, 512, 2046), (64, 1024, 514), (5, 4096, 300), (8, 64, 8190),
     # few rows, long weight
     (2, 5120, 4400), (20, 8448, 2048), (40, 11008, 1030), (64, 4096, 5002),
-    # tiles of 128 and 256 rows, split and not, one stage and more
+    # tiles of 32 and 64 rows, split and not, one stage and more
     (65, 16, 2), (100, 256, 64), (128, 272, 130), (129, 1040, 514), (256, 512, 1000), (257, 272, 4106), (300, 16, 62),
     (700, 2064, 770), (2050, 256, 66),
 ]
