@@ -73,3 +73,42 @@ def test_gradients_of_training_sizes(T, K, N, gated, tile, split, rounds):
         z, ez = ffn.grad_pre(base.host(dY[:, f:f + 1]), base.host(pre[:, cols]), "silu", gated)
         w = (z.sum(0), ez.sum(0) + (T + 2) * ffn.U * (np.abs(z) + ez).sum(0))
         assert ffn.check(base.host(db[cols]), w, "dbias") is None, ffn.check(base.host(db[cols]), w, "dbias")
+
+
+# features of a row, and the rounds of 512 x 8 that stay in registers
+ROUNDS = [(4096, 1), (4104, 2), (8192, 2), (8200, 3), (11008, 3), (12288, 3), (12296, 4), (13824, 4), (16384, 4), (16392, 0),
+          (1032, 1), (2050, 1), (4098, 2), (8190, 2), (8194, 0)]
+
+
+@pytest.mark.parametrize("F, rounds", ROUNDS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])   # every form of the kernel
+def test_rounds_of_long_rows(F, rounds, gated, act):
+    print(f"case rounds {F} {gated} {act}", flush=True)
+    N, T = F * (1 + gated), 67
+    p = li8.backward_plan(T, 32, N, gated)
+    assert (p["path"], p["row_threads"], p["row_rounds"]) == ("tiled", 512, rounds), p
+    base.Backward(T, 32, N, gated, seed=F).check(act)
+
+
+@pytest.mark.parametrize("F, rounds", [(5, 1), (8, 1), (510, 1), (512, 1), (514, 2), (1016, 2), (1022, 2), (1024, 2)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+def test_rounds_of_short_rows(F, rounds, gated, act):
+    """A wave for each row."""
+    print(f"case short rows {F} {gated} {act}", flush=True)
+    N, T = F * (1 + gated), 131
+    p = li8.backward_plan(T, 48, N, gated)
+    assert (p["path"], p["row_threads"], p["row_rounds"]) == ("tiled", 64, rounds), p
+    base.Backward(T, 48, N, gated, seed=F).check(act)
+
+
+@pytest.mark.parametrize("T, tile", [(20, 32), (50, 64)])
+@pytest.mark.parametrize("N", [512, 510])                 # whole groups of eight, and ragged ones
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+def test_forms_of_the_kernel_for_few_rows(T, tile, N, gated, act):
+    print(f"case few rows {T} {N} {gated} {act}", flush=True)
+    p = li8.backward_plan(T, 272, N, gated)
+    assert (p["path"], p["tile"]) == ("few", tile), p
+    base.Backward(T, 272, N, gated, seed=T).check(act)
