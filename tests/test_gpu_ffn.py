@@ -107,7 +107,7 @@ TILED = [
     (257, 512, 1002, {}), (129, 4096, 258, {}), (513, 256, 2730, {}), (33, 8208, 100, {}),
     (100, 528, 384, dict(fixed=400)),                      # every second column an outlier, gathered by the prepare kernel
 ]
-# the larger tiles, which few rows do not take (with outlier columns copied from the stages, too)
+# the larger tiles, which few rows do not take (outlier columns gathered)
 WIDE = [(2048, 64, 11008, 192, {}), (2500, 64, 5000, 256, {}), (1100, 272, 6000, 128, dict(sparse=2e-3)),
         (1100, 272, 5998, 128, {}), (1100, 528, 6010, 128, dict(fixed=400))]
 

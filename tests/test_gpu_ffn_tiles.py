@@ -112,3 +112,68 @@ def test_forms_of_the_kernel_for_few_rows(T, tile, N, gated, act):
     p = li8.backward_plan(T, 272, N, gated)
     assert (p["path"], p["tile"]) == ("few", tile), p
     base.Backward(T, 272, N, gated, seed=T).check(act)
+
+
+FOLD = [(400, 272, 12546, 256, 128), (64, 272, 12546, 64, 128), (400, 528, 13826, 256, 128)]
+
+
+@pytest.mark.parametrize("T, K, N, tile_m, tile_n", FOLD)
+@pytest.mark.parametrize("outliers", [3, 64, 65, 150, 256, 257])
+def test_outlier_columns_copied_from_the_stages(T, K, N, tile_m, tile_n, outliers):
+    """Both sides of the counts at which the product copies them and the prepare kernel does not gather, in a workspace
+    that holds no codes."""
+    print(f"case fold {T}x{K}x{N} {outliers}", flush=True)
+    for gated in (False, True):
+        p = li8.epilogue_plan(T, K, N, gated)
+        assert (p["tile_m"], p["tile_n"], p["fold_lo"], p["fold_hi"]) == (tile_m, tile_n, 64, 256), p
+    f = base.Forward(T, K, N, seed=16, fixed=outliers, residual=True)
+    assert len(oracle.detect_outliers(f.X, 6.0)[1]) == outliers
+    f.epilogue(activation="gelu", save=True)
+    f.ws = base.dirty(f.ws.numel())
+    f.gated(activation="silu", save=False)
+    x, w, s = f.d["X"], f.d["Wq"], f.d["sW"]
+    Y = li8.linear(x, w, s).view(torch.int16)
+    pre = torch.empty((T, N), dtype=F16, device=DEV)
+    assert torch.equal(li8.linear_epilogue(x, w, s, workspace=base.dirty(f.ws.numel())).view(torch.int16), Y)
+    li8.gated_linear(x, w, s, pre=pre, workspace=base.dirty(f.ws.numel()))
+    assert torch.equal(pre.view(torch.int16), Y)
+
+
+@pytest.mark.parametrize("outliers", [6, 100, 250])
+def test_a_chunk_through_an_up_projection_is_the_linear_layer(outliers):
+    """512 x 5120 x 13824, whose 40 stages pass the ring many times: bit for bit the plain layer's product."""
+    T, K, N = 512, 5120, 13824
+    print(f"case fold {T}x{K}x{N} {outliers}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(outliers)
+    x = torch.randn((T, K), generator=g, device=DEV).clamp(-5.9, 5.9).half()
+    x[:, torch.randperm(K, generator=g, device=DEV)[:outliers]] *= 40
+    w = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    s = torch.rand(N, generator=g, device=DEV) * 1e-3 + 1e-4
+    assert int((x.abs() > 6).any(0).sum()) == outliers and li8.epilogue_plan(T, K, N)["fold_hi"] == 256
+    Y = li8.linear(x, w, s).view(torch.int16)
+    ws, pre = base.dirty(li8.linear_workspace_bytes(T, K, N)), torch.empty((T, N), dtype=F16, device=DEV)
+    assert torch.equal(li8.linear_epilogue(x, w, s, workspace=ws).view(torch.int16), Y)
+    li8.gated_linear(x, w, s, pre=pre, workspace=base.dirty(ws.numel()))
+    assert torch.equal(pre.view(torch.int16), Y)
+
+
+# T, K, tile (rows 64 x 128, ranges of K), N: every tile of the epilogue variants by its plan
+VARIANTS = [
+    (64, 272, 12546, dict(tile_m=64, tile_n=128, ranges=1, per_cu=1), dict(tile_m=64, tile_n=128, ranges=1, per_cu=1)),
+    (1024, 272, 2178, dict(tile_m=64, tile_n=128, ranges=1, per_cu=2), dict(tile_m=64, tile_n=128, ranges=1, per_cu=2)),
+    (100, 4112, 258, dict(tile_m=64, tile_n=128, per_cu=1), dict(tile_m=64, tile_n=128, per_cu=1)),
+    (1100, 272, 6000, dict(tile_m=256, tile_n=128, ranges=1), dict(tile_m=256, tile_n=128, ranges=1)),
+    (2048, 80, 11008, dict(tile_m=256, tile_n=192, ranges=1), dict(tile_m=256, tile_n=256, ranges=1)),
+    (2500, 80, 5002, dict(tile_m=256, tile_n=256, ranges=1), dict(tile_m=256, tile_n=256, ranges=1)),
+]
+
+
+@pytest.mark.parametrize("T, K, N, linear, gated", VARIANTS)
+def test_epilogue_tiles(T, K, N, linear, gated):
+    print(f"case epilogue tile {T}x{K}x{N}", flush=True)
+    for want, pair in ((linear, False), (gated, True)):
+        p = li8.epilogue_plan(T, K, N, pair)
+        assert want.items() <= p.items() and (p["ranges"] > 1) == (T == 100), p
+    f = base.Forward(T, K, N, seed=17, residual=True, sparse=1e-3)
+    f.epilogue(activation="gelu_tanh")
+    f.gated(activation="silu")
