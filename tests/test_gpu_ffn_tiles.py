@@ -177,3 +177,21 @@ def test_epilogue_tiles(T, K, N, linear, gated):
     f = base.Forward(T, K, N, seed=17, residual=True, sparse=1e-3)
     f.epilogue(activation="gelu_tanh")
     f.gated(activation="silu")
+
+
+@pytest.mark.parametrize("act", ffn.ACTS)
+@pytest.mark.parametrize("T, K", [(5, 64), (6, 8224), (40, 64), (40, 4112)])
+def test_gates_over_their_range(act, T, K):
+    """Gates from -60000 to 60000, densest where the exponentials leave fp32, times up values from 2^-6 to 300: products
+    past fp16's range and in the underflowed tails."""
+    print(f"case gates {act} {T}x{K}", flush=True)
+    F = 264
+    f = base.Forward(T, K, 2 * F, seed=18, fixed=0)
+    gate = np.concatenate([np.linspace(-110, 110, 200), np.exp(np.linspace(4.8, 11, 32)), -np.exp(np.linspace(4.8, 11, 32))])
+    up = 2.0 ** np.random.default_rng(19).uniform(-6, 8.2, F) * (1 - 2 * (np.arange(F) % 2))
+    f.bias = np.concatenate([gate, up]).astype(np.float16)
+    f.d["bias"] = base.dev(f.bias)
+    Hh, _ = f.gated(activation=act)
+    h = base.host(Hh)
+    assert np.isinf(h).any() and not np.isnan(h).any()
+    assert act == "none" or (np.abs(h[:, gate < -105]) <= 2.0 ** -24).all()
