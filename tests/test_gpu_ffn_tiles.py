@@ -195,3 +195,20 @@ def test_gates_over_their_range(act, T, K):
     h = base.host(Hh)
     assert np.isinf(h).any() and not np.isnan(h).any()
     assert act == "none" or (np.abs(h[:, gate < -105]) <= 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("T, K, N", [(8, 11008, 4096), (16, 11008, 4096), (3, 9216, 13826), (16, 9216, 13826)])
+@pytest.mark.parametrize("kw", [{}, dict(sparse=1e-3)])
+def test_few_tokens_in_long_slices(T, K, N, kw):
+    """Slices of K past 4096 columns (many weight rows): twice the weight loads of shorter ones in flight."""
+    print(f"case long slices {T}x{K}x{N} {kw}", flush=True)
+    assert li8.epilogue_plan(T, K, N, True)["path"] == "few_tokens_split"
+    f = base.Forward(T, K, N, seed=23, residual=True, **kw)
+    f.epilogue(activation="silu")
+    f.gated(activation="gelu")
+    x, w, s = f.d["X"], f.d["Wq"], f.d["sW"]
+    Y = li8.linear(x, w, s).view(torch.int16)
+    pre = torch.empty((T, N), dtype=F16, device=DEV)
+    assert torch.equal(li8.linear_epilogue(x, w, s).view(torch.int16), Y)
+    li8.gated_linear(x, w, s, pre=pre)
+    assert torch.equal(pre.view(torch.int16), Y)
