@@ -416,13 +416,13 @@ __device__ __forceinline__ v4i rsrc_words(const void *p, int bytes)
 // load_to_lds, but written out: behind the builtin the compiler lets every
 // transposing LDS read wait for all loads in flight (vmcnt(0)).  It has no
 // register to write, and what it writes to LDS is ordered by
-// wait_loads_barrier, which counts it.  M0 holds the LDS address (one wait state
-// before its use); nothing else in k_grad_gemm uses M0.
+// wait_loads_barrier, which counts it.  The LDS address is in M0 by the operand's
+// constraint, so the compiler knows that M0 is taken (one wait state before its use).
 __device__ __forceinline__ void load_to_lds_raw(v4i r, uint32_t dst, int voffset, int soffset)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(dst), "v"(voffset), "s"(r), "s"(soffset));
+                 : "{m0}"(dst), "v"(voffset), "s"(r), "s"(soffset));
 }
 
 // Permutation of the 16-byte chunks of A's 128-byte rows: 16 rows' reads of one
