@@ -1111,9 +1111,10 @@ BackwardLayout backward_layout(int64_t T, int64_t K, int64_t N)
     L.Np = (int)((N + kGN - 1) / kGN * kGN);
     size_t off = 0;
     const bool rows = !p.few || K == 0;   // (K = 0: no product, and few rows go the general way)
+    const int strips = rows ? col_strips(T, (N + 1) / 2) : 1;   // (a pair's; a single weight has no more)
     L.A = off;     off = align_up(off + (rows ? 2 * (size_t)T * (size_t)L.Np : 0), A);
     L.fac = off;   off = align_up(off + (rows ? 4 * (size_t)T : 0), A);
-    L.cols = off;  off = align_up(off + (rows ? 4 * (size_t)kMaxColStrips * (size_t)N : 0), A);
+    L.cols = off;  off = align_up(off + (strips > 1 ? 4 * (size_t)strips * (size_t)N : 0), A);
     L.part = off;  off = align_up(off + (p.splits > 1 ? 4 * (size_t)p.splits * (size_t)T * (size_t)K : 0), A);
     L.total = off;
     return L;

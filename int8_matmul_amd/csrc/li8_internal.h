@@ -255,8 +255,8 @@ RowPlan row_plan(int64_t F);
 // Strips of the tokens for dbias, F > 0 features a row of a part (not for few rows).
 int col_strips(int64_t T, int64_t F);
 // Workspace: the product's operand A fp16 [T,Np], its rows' factors fp32 [T],
-// dbias' partial sums fp32 [kMaxColStrips][N], the split product's partial
-// sums fp32 [splits][T,K].
+// dbias' partial sums fp32 [strips][N] where a call has several strips, the
+// split product's partial sums fp32 [splits][T,K].  (T > 0, N > 0.)
 struct BackwardLayout {
     size_t A, fac, cols, part, total;
     int Np;

@@ -108,3 +108,24 @@ def test_ranges_of_k_fit_where_the_sums_go():
                         blocks = 2 * cd(N // 2, 32) if gated else cd(N, 32)
                         assert p["tile_m"] == 64 and tiles * p["ranges"] <= 256 and p["ranges"] <= cd(K, 128)
                         assert p["ranges"] * cd(T, 32) * blocks * 4096 <= N * K
+
+
+def test_the_backward_workspace_holds_what_a_call_uses(lib):
+    """The operand, its rows' factors, the strips of dbias where there are several, the ranges' sums; no more."""
+    def up(n):
+        return cd(n, 256) * 256
+
+    for T in (1, 65, 300, 768, 769, 1300, 4096, 1 << 20):
+        for K in (0, 16, 1040, 4096):
+            for N in (1, 2, 64, 4098, 22016, 1 << 18, 1 << 21):
+                if T * K >= 1 << 31 or N * K >= 1 << 31:
+                    continue
+                got = lib.llm_int8_backward_workspace_bytes(T, K, N)
+                plans = [li8.backward_plan(T, K, N, g) for g in ([False, True] if N % 2 == 0 else [False])]
+                part = up(4 * plans[0]["ranges"] * T * K) if plans[0]["ranges"] > 1 else 0
+                if plans[0]["path"] == "few":
+                    assert got == part
+                    continue
+                strips = max(p["strips"] for p in plans)
+                least = up(2 * T * cd(N, 64) * 64) + up(4 * T) + part + (up(4 * strips * N) if strips > 1 else 0)
+                assert got == least or (N == 1 and got >= least), (T, K, N)

@@ -212,3 +212,18 @@ def test_few_tokens_in_long_slices(T, K, N, kw):
     assert torch.equal(li8.linear_epilogue(x, w, s).view(torch.int16), Y)
     li8.gated_linear(x, w, s, pre=pre)
     assert torch.equal(pre.view(torch.int16), Y)
+
+
+@pytest.mark.parametrize("T, K, N", [(50, 272, 512), (300, 272, 4098), (2050, 272, 4098), (1300, 0, 6002), (70, 48, 8202)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_the_backward_workspace_is_enough(T, K, N, gated):
+    """A workspace of exactly the bytes asked for, between others that stay as they are."""
+    print(f"case workspace {T}x{K}x{N} {gated}", flush=True)
+    n = li8.backward_workspace_bytes(T, K, N)
+    buf = torch.full((n + (1 << 17),), 7, dtype=torch.uint8, device=DEV)
+    b = base.Backward(T, K, N, gated, seed=25)
+    got = b.run("silu", workspace=buf[1 << 16:(1 << 16) + n])
+    assert (buf[:1 << 16] == 7).all() and (buf[(1 << 16) + n:] == 7).all()
+    want = ffn.backward(b.dY, b.pre, b.Wq, b.sW, "silu", gated)
+    for k, t in got.items():
+        assert ffn.check(base.host(t), want[k], k) is None, ffn.check(base.host(t), want[k], k)
