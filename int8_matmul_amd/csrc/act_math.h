@@ -13,7 +13,7 @@
 //   P(-x) = exp(-x^2 / 2) Q(1 / (1 + 0.3 x)),    x >= 0,
 // Q a polynomial of degree 8 without constant term fitted to
 // erfcx(x / sqrt(2)) / 2 on [0, 14] for the smallest largest relative error
-// (1.5e-7; 4.8e-7 as evaluated in fp32), so the tail keeps its relative
+// (1.7e-7; 4.4e-7 as evaluated in fp32), so the tail keeps its relative
 // accuracy; exp, 1/x: one unit in the last place each, plus |x^2/2| units
 // from the rounded exponent.  Results are rounded to fp16 next (2^-11), which
 // these errors (below 2^-18 for |z| <= 7) do not reach.

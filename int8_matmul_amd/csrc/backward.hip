@@ -252,10 +252,12 @@ __device__ void grad_cols(const GradArgs &a, const ColSums &c, int block)
 
 // TPR threads a row: 64 (a wave, eight rows a workgroup) or all 512.
 // NR > 0: the row's NR rounds of 8 TPR features, their inputs requested ahead (all
-// of them; of four rounds of a pair one at a time: two workgroups a CU have
-// 128 registers), their results in registers between the maximum and the
-// conversion; 0: rows of any length, computed a second time.  (512 threads against
-// 1024 with half the rounds: F = 11008, 4096 rows, dZ kept: 133 and 164 us.)
+// of them; of four rounds of a pair one at a time), their results in registers
+// between the maximum and the conversion; 0: rows of any length, computed a second
+// time.  Two workgroups a CU have 128 registers a thread: four rounds of a pair take
+// more even so, and 22 to 24 of them go to scratch memory; no other form spills.
+// (512 threads against 1024 with half the rounds: F = 11008, 4096 rows, dZ kept: 133
+// and 164 us.)
 // The launch's first workgroups form the column sums, where asked for: with 75
 // rows a launch of their own costs more than they do.
 template <bool GATED, int KIND, int MODE, int TPR, int NR>
@@ -688,7 +690,8 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
 // rows itself (the same inputs serve all column tiles from the L2), so nothing
 // has to wait for a kernel that knows whole rows: a row's power of two is that of
 // its largest value in the range, and the partial sums are stored without it.
-// The weight's codes are requested before anything else.  Every range's
+// The weight's codes are requested before anything else; a wave's loads complete in
+// order, so its inputs, requested after them, come when its codes have.  Every range's
 // workgroup of the first column tile sees all rows of its dZ: it writes dbias and
 // grad_pre.
 // 8 waves of 32 columns, BM rows, at most 256 n: half a wave forms a row, so its
@@ -697,6 +700,9 @@ __global__ __launch_bounds__(WM *WN * 64) void k_grad_gemm(
 // 22016, where k_grad_rows and k_grad_gemm take 27 and 31.)  37 x 4096 x 4096 with
 // gelu and bias: 14.2 us a call with its join, 7.6 us for one row; what is left is the
 // chain of loads, dZ (formed 16 times, 3 us of gelu's slopes) and 10 MB of sums.
+// (The operand in two fp16 parts, its value and the rest of its rounding, takes dX's error
+// from 2.9e-4 to its own rounding's 2.1e-4 and costs 5 to 10 %, 37 x 4096 x 4096 15.2 ->
+// 16.4 us, as the waves read twice the A from LDS; one part is what k_grad_gemm has.)
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 64;      // most rows
 constexpr int kFewStages = 4;     // most stages of 64 n in a range

@@ -1035,7 +1035,9 @@ hipError_t launch_gemm(const int8_t *Wq, const float *sW, int64_t T, int64_t K, 
 // 32.0 and 28.7, gated 100 x 4096 x 2 * 4096 31.0 and 26.7, 64 x 4096 x 11008 28.0 and
 // 28.8, gated 64 x 4096 x 2 * 11008 29.9 and 36.8; 256x128 tiles, 250 of them: 1500 x
 // 1024 x 4096 38.7 and 33.0, gated 512 x 2048 x 2 * 5504 41.2 and 38.6, 512 x 4096 x 11008
-// 56.7 and 56.3, 512 x 5120 x 13824 65.1 and 71.3.
+// 56.7 and 56.3, 512 x 5120 x 13824 65.1 and 71.3.  (The weight's rows alone decide; the
+// tokens, K and the count of outlier columns, on which the gather's cost depends too, do
+// not, and near the limit either way costs up to 3 % of the better one.)
 constexpr int64_t kEpiFoldMinN = 12288;
 // Where 64x128 tiles are fewer than the CUs, ranges of K (K_PART, K_SUM) while all
 // their workgroups run at once, by a model in us: 0.42 a stage or the weight at
