@@ -25,7 +25,8 @@
  * empty call (dX is then zero where it has elements, and so is dbias).
  * Outputs and the workspace must not overlap inputs or one another, except for
  * a residual that is Y itself.  llm_int8_plan is about llm_int8_linear; the
- * calls here take its few-token paths for the same shapes.
+ * calls here take its few-token paths for the same shapes
+ * (llm_int8_ffn_plan.h says which kernels they run).
  * X and the weight must be finite.  A NaN of a bias or residual reaches the
  * outputs that it enters.  At Z = +inf (by its bias) every activation is +inf; at
  * -inf none keeps it, relu is 0 and the smooth ones are 0 times infinity, NaN.
